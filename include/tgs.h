@@ -254,6 +254,55 @@ tgs_status tgs_gtopk_merge(const int32_t* idx, const float* val, int32_t P, int6
                            int32_t* out_idx, float* out_val, uint8_t* out_mask, void* workspace,
                            size_t workspace_bytes, hipStream_t stream);
 
+/* -------------------------------------------------------------------------
+ * Operators of the training step around the sparsifier: the token embedding
+ * (whose dense gradient the top-k step compresses) and the Muon update of the
+ * weight matrices.  They hold values in the types below, compute in fp32 and
+ * round once, to nearest even, where they store.  The conventions above hold,
+ * except that arrays need only their own type's alignment and workspaces must
+ * be 256-byte aligned.
+ * ------------------------------------------------------------------------- */
+typedef int32_t tgs_dtype;
+#define TGS_FP32 0
+#define TGS_BF16 1
+#define TGS_FP16 2
+#define TGS_INT32 3
+#define TGS_INT64 4
+
+/* Bytes of workspace tgs_embedding_lookup needs (0 if T is invalid). */
+size_t tgs_embedding_lookup_workspace_bytes(int64_t T);
+
+/*
+ * Embedding lookup with scaling: out[t][:] = scale * table[tokens[t]][:].
+ *   tokens    [T] int32 or int64.  A negative token is a masked place: its
+ *             row is +0.  A token >= V sets the bad-input bit of the device
+ *             error word, and its row is +0.
+ *   table     [V][D] fp32, bf16 or fp16, row-major.
+ *   out       [T][D] fp32, bf16 or fp16: fp32(table) * scale, rounded once.
+ * 0 <= T, 1 <= V, 1 <= D, each at most 2^31 - 1; scale is finite.
+ */
+tgs_status tgs_embedding_lookup(const void* tokens, tgs_dtype tokens_dtype, int64_t T, const void* table,
+                                tgs_dtype table_dtype, int64_t V, int64_t D, float scale, void* out,
+                                tgs_dtype out_dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace tgs_embedding_grad needs (0 if the sizes or types are
+   invalid): 16 bytes a place for the sort, and two partial rows for every 8
+   to 64 places. */
+size_t tgs_embedding_grad_workspace_bytes(int64_t T, int64_t V, int64_t D, tgs_dtype grad_dtype, tgs_dtype out_dtype);
+
+/*
+ * Gradient of the lookup with respect to the table, by sorted tokens:
+ *   S[v][:] = scale * sum of grad[t][:] over the places with tokens[t] == v
+ *   accumulate == 0: out = S, rows that no token names are +0
+ *   accumulate != 0: out = out + S, rows that no token names are not touched
+ * The sums are fp32, in an order that depends on the tokens alone, so equal
+ * inputs give equal bits.  Masked places (negative tokens) and tokens >= V
+ * (bad-input bit) add to nothing: their rows of grad may hold anything.
+ */
+tgs_status tgs_embedding_grad(const void* tokens, tgs_dtype tokens_dtype, int64_t T, const void* grad,
+                              tgs_dtype grad_dtype, int64_t V, int64_t D, float scale, void* out, tgs_dtype out_dtype,
+                              int32_t accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Waits for `stream`, then reads and clears the device error word of
    `workspace`: TGS_OK if no kernel flagged a problem since it was last read,
    TGS_EINVAL for an input index outside its range (a merge row's index out

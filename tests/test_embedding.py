@@ -1,0 +1,376 @@
+"""Embedding lookup and its gradient.
+
+The oracle is the definition in 64 bits.  Tolerances count roundings: an fp32
+operation is off by at most 2^-24 of its result, the final rounding to the
+output's type by eps / 2 of it (plus half the smallest subnormal where the
+type has a short exponent).
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+U = 2.0**-24
+FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+EINVAL, EWORKSPACE = -1, -2
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def tiny(dtype):
+    return torch.finfo(dtype).tiny * torch.finfo(dtype).eps / 2
+
+
+def exact_lookup(tokens, table, scale):
+    t = tokens.long()
+    out = torch.zeros(t.shape + (table.shape[1],), dtype=torch.float64)
+    real = t >= 0
+    out[real] = table.double()[t[real]] * scale
+    return out
+
+
+def exact_grad(tokens, grad, V, scale):
+    """(sum, sum of absolute values, number of places) a row."""
+    t = tokens.long().reshape(-1)
+    g = grad.double().reshape(t.numel(), grad.shape[-1])
+    real = (t >= 0) & (t < V)
+    total = torch.zeros(V, g.shape[1], dtype=torch.float64)
+    size = torch.zeros_like(total)
+    total.index_add_(0, t[real], g[real])
+    size.index_add_(0, t[real], g[real].abs())
+    count = torch.bincount(t[real], minlength=V).double()[:, None]
+    return total * scale, size * abs(scale), count
+
+
+def assert_lookup(out, tokens, table, scale):
+    want = exact_lookup(tokens, table, scale)
+    got = out.cpu().double()
+    # scale to fp32, the product, the rounding to the output's type
+    tol = want.abs() * (2.001 * U + half_step(out.dtype)) + tiny(out.dtype)
+    assert got.shape == want.shape
+    assert ((got - want).abs() <= tol).all()
+
+
+def assert_grad(out, tokens, grad, V, scale, base=None):
+    total, size, count = exact_grad(tokens, grad, V, scale)
+    want = total if base is None else total + base.double()
+    # count - 1 additions, up to 5 joining zeros and partial sums, scale, its product, and the addition to base
+    tol = size * (count + 8) * U * 1.01 + want.abs() * (U + half_step(out.dtype)) * 1.01 + tiny(out.dtype)
+    got = out.cpu().double()
+    assert got.shape == want.shape
+    bad = ~((got - want).abs() <= tol)
+    assert not bad.any(), "%d values off, first at %s" % (int(bad.sum()), torch.nonzero(bad)[0].tolist())
+
+
+def make_tokens(T, V, masked, dtype, rng, skew=True):
+    u = rng.random(T)
+    t = np.minimum((np.exp(u * np.log(V + 1)) - 1).astype(np.int64), V - 1) if skew else (u * V).astype(np.int64)
+    t[rng.random(T) < masked] = -1
+    return torch.from_numpy(t).to(dtype)
+
+
+# ------------------------------------------------------------------- CPU --
+def abi():
+    import top_gradient_sparsification_amd as tgs
+    return tgs.library()
+
+
+def lookup_call(lib, **kw):
+    a = dict(tokens=0x100000, it=3, T=16, table=0x200000, tt=0, V=100, D=8, scale=1.0, out=0x900000, ot=0,
+             ws=0xA00000, wsn=32768)
+    a.update(kw)
+    p = ctypes.c_void_p
+    return lib.tgs_embedding_lookup(p(a["tokens"]), a["it"], a["T"], p(a["table"]), a["tt"], a["V"], a["D"],
+                                    a["scale"], p(a["out"]), a["ot"], p(a["ws"]), a["wsn"], None)
+
+
+def grad_call(lib, **kw):
+    a = dict(tokens=0x100000, it=3, T=16, grad=0x200000, gt=0, V=100, D=8, scale=1.0, out=0x900000, ot=0, acc=0,
+             ws=0xA000000, wsn=1 << 30)
+    a.update(kw)
+    p = ctypes.c_void_p
+    return lib.tgs_embedding_grad(p(a["tokens"]), a["it"], a["T"], p(a["grad"]), a["gt"], a["V"], a["D"], a["scale"],
+                                  p(a["out"]), a["ot"], a["acc"], p(a["ws"]), a["wsn"], None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(T=2**31), dict(V=0), dict(V=2**31), dict(D=0), dict(D=2**31),
+    dict(it=0), dict(it=9), dict(ot=3), dict(scale=float("nan")), dict(scale=float("inf")),
+    dict(tokens=None), dict(out=None), dict(ws=None), dict(tokens=0x100002), dict(out=0x900001), dict(ws=0xA00010),
+    dict(tokens=0x100004, it=4),
+    dict(out=0x100010),           # over the tokens
+    dict(out=0x200010),           # over the table or the incoming gradient
+])
+def test_refusals_before_any_launch(kw):
+    lib = abi()
+    assert lookup_call(lib, **kw) == EINVAL, lib.tgs_last_error()
+    assert b"embedding_lookup" in lib.tgs_last_error()
+    assert grad_call(lib, **kw) == EINVAL, lib.tgs_last_error()
+    assert b"embedding_grad" in lib.tgs_last_error()
+
+
+def test_refusals_of_each():
+    lib = abi()
+    assert lookup_call(lib, table=None) == EINVAL
+    assert lookup_call(lib, tt=4) == EINVAL
+    assert lookup_call(lib, wsn=100) == EWORKSPACE
+    assert lookup_call(lib, out=0xA00000 + 64) == EINVAL  # in the workspace
+    assert grad_call(lib, grad=None) == EINVAL
+    assert grad_call(lib, gt=3) == EINVAL
+    need = lib.tgs_embedding_grad_workspace_bytes(16, 100, 8, 0, 0)
+    assert need > 32768
+    assert grad_call(lib, wsn=need - 1) == EWORKSPACE
+    assert grad_call(lib, out=0xA000000 + 64) == EINVAL
+    for bad in ((-1, 10, 8, 0, 0), (10, 0, 8, 0, 0), (10, 10, 0, 0, 0), (10, 10, 8, 3, 0), (10, 10, 8, 0, 4),
+                (2**31, 10, 8, 0, 0)):
+        assert lib.tgs_embedding_grad_workspace_bytes(*bad) == 0, bad
+    assert lib.tgs_embedding_lookup_workspace_bytes(-1) == 0
+
+
+def test_binding_refusals_on_the_cpu():
+    import top_gradient_sparsification_amd as tgs
+    ids, table = torch.zeros(4, dtype=torch.int64), torch.zeros(10, 8)
+    with pytest.raises(TypeError, match="GPU tensor"):
+        tgs.embedding_lookup(ids, table)
+    with pytest.raises(TypeError, match="table must be one of"):
+        tgs.embedding_lookup(ids, table.double())
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        tgs.embedding_lookup(ids, [1.0])
+    with pytest.raises(TypeError, match="GPU tensor"):
+        tgs.embedding_grad(ids, table[:4], 10)
+    with pytest.raises(TypeError, match="grad must be one of"):
+        tgs.embedding_grad(ids, table.int(), 10)
+
+
+def test_the_oracle_counts_masked_places_and_repeats():
+    t = torch.tensor([2, -1, 0, 2])
+    g = torch.tensor([[1.0], [100.0], [2.0], [4.0]])
+    total, size, count = exact_grad(t, g, 3, 0.5)
+    assert total.flatten().tolist() == [1.0, 0.0, 2.5] and count.flatten().tolist() == [1, 0, 2]
+    assert size.flatten().tolist() == [1.0, 0.0, 2.5]
+    assert exact_lookup(t, torch.tensor([[1.0], [2.0], [3.0]]), 2.0).flatten().tolist() == [6.0, 0.0, 2.0, 6.0]
+    with pytest.raises(AssertionError):
+        assert_grad(torch.tensor([[1.0], [0.0], [2.5 + 1e-5]]), t, g, 3, 0.5)
+
+
+# ------------------------------------------------------------------- GPU --
+@pytest.mark.gpu
+@pytest.mark.parametrize("table_dtype", FLOATS)
+@pytest.mark.parametrize("out_dtype", FLOATS)
+@pytest.mark.parametrize("D", [1, 3, 8, 130, 1001])
+def test_lookup_types_and_widths(tgs_gpu, table_dtype, out_dtype, D):
+    rng = np.random.default_rng(D)
+    V, T = 517, 301
+    table = torch.from_numpy(rng.standard_normal((V, D)).astype(np.float32)).to(table_dtype)
+    for ids, scale in ((torch.int32, 1.0), (torch.int64, 0.37)):
+        tokens = make_tokens(T, V, 0.2, ids, rng)
+        out = tgs_gpu.embedding_lookup(tokens.cuda(), table.cuda(), scale=scale, out_dtype=out_dtype)
+        assert out.dtype == out_dtype
+        assert_lookup(out, tokens, table, scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,D", [(1, 1, 1), (1, 50_001, 4096), (7, 3, 2047), (4099, 50_001, 257), (1025, 9, 4)])
+def test_lookup_sizes(tgs_gpu, T, V, D):
+    rng = np.random.default_rng(T + D)
+    table = torch.from_numpy(rng.standard_normal((V, D)).astype(np.float32)).bfloat16()
+    tokens = make_tokens(T, V, 0.0, torch.int64, rng, skew=False)
+    tokens[-1] = V - 1
+    assert_lookup(tgs_gpu.embedding_lookup(tokens.cuda(), table.cuda(), scale=8.0), tokens, table, 8.0)
+
+
+@pytest.mark.gpu
+def test_lookup_shapes_masks_and_specials(tgs_gpu):
+    table = torch.tensor([[float("nan"), 1.0, float("inf"), -0.0, 1e-40], [2.0, -3.0, 65504.0, 1e30, -1e30]]).cuda()
+    tokens = torch.tensor([[-1, 0, -2**31], [1, -7, 0]], dtype=torch.int32).cuda()
+    out = tgs_gpu.embedding_lookup(tokens, table)
+    assert out.shape == (2, 3, 5)
+    got = out.cpu()
+    for i, j in ((0, 0), (0, 2), (1, 1)):  # masked: zeros, whatever the table holds
+        assert (got[i, j].view(torch.int32) == 0).all()
+    assert torch.equal(got[0, 1].view(torch.int32), table[0].cpu().view(torch.int32))
+    half = tgs_gpu.embedding_lookup(tokens, table, out_dtype=torch.float16).cpu()
+    assert half[1, 0].tolist()[3:] == [float("inf"), float("-inf")]
+    assert tgs_gpu.embedding_lookup(tokens[:0], table).shape == (0, 3, 5)
+    all_masked = tgs_gpu.embedding_lookup(torch.full((9,), -1, device="cuda"), table)
+    assert (all_masked == 0).all()
+
+
+@pytest.mark.gpu
+def test_tokens_past_the_table_are_reported(tgs_gpu):
+    table = torch.ones(5, 8, device="cuda")
+    tokens = torch.tensor([0, 5, 2**40, 4], device="cuda")
+    ws = torch.zeros(tgs_gpu.embedding_grad_workspace_bytes(4, 5, 8), dtype=torch.uint8, device="cuda")
+    out = tgs_gpu.embedding_lookup(tokens, table, ws=ws)
+    assert out.sum(1).tolist() == [8.0, 0.0, 0.0, 8.0]
+    with pytest.raises(ValueError):
+        tgs_gpu.check_device_error(ws)
+    tgs_gpu.check_device_error(ws)
+    g = tgs_gpu.embedding_grad(tokens, torch.ones(4, 8, device="cuda"), 5, ws=ws)
+    assert g.sum(1).tolist() == [8.0, 0.0, 0.0, 0.0, 8.0]
+    with pytest.raises(ValueError):
+        tgs_gpu.check_device_error(ws)
+
+
+@pytest.mark.gpu
+def test_unaligned_views_and_refusals(tgs_gpu):
+    rng = np.random.default_rng(5)
+    flat = torch.from_numpy(rng.standard_normal(1 + 40 * 24).astype(np.float32)).bfloat16()
+    table = flat[1:].view(40, 24)
+    tokens = make_tokens(100, 40, 0.1, torch.int64, rng)
+    out = torch.empty(1 + 100 * 24, dtype=torch.float32, device="cuda")[1:].view(100, 24)
+    dev = flat.cuda()[1:].view(40, 24)
+    assert tgs_gpu.embedding_lookup(tokens.cuda(), dev, scale=0.5, out=out) is out
+    assert_lookup(out, tokens, table, 0.5)
+    with pytest.raises(ValueError, match="contiguous"):
+        tgs_gpu.embedding_lookup(tokens.cuda(), dev.t())
+    with pytest.raises(ValueError, match="shape"):
+        tgs_gpu.embedding_lookup(tokens.cuda(), dev, out=out[:5])
+    with pytest.raises(TypeError):
+        tgs_gpu.embedding_lookup(tokens.cuda(), dev, out_dtype=torch.int32)
+    with pytest.raises(TypeError):
+        tgs_gpu.embedding_lookup(tokens.cuda().short(), dev)
+    with pytest.raises(ValueError, match="accumulate needs out"):
+        tgs_gpu.embedding_grad(tokens.cuda(), out, 40, accumulate=True)
+    with pytest.raises(ValueError, match="shape of tokens"):
+        tgs_gpu.embedding_grad(tokens.cuda()[:7], out, 40)
+    with pytest.raises(ValueError, match="scale"):
+        tgs_gpu.embedding_grad(tokens.cuda(), out, 40, scale=float("nan"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("grad_dtype", FLOATS)
+@pytest.mark.parametrize("out_dtype", FLOATS)
+@pytest.mark.parametrize("D", [1, 5, 130, 264])
+def test_grad_types_and_widths(tgs_gpu, grad_dtype, out_dtype, D):
+    rng = np.random.default_rng(D)
+    V, T = 211, 509
+    for ids, scale, acc in ((torch.int32, 0.37, False), (torch.int64, 1.0, True)):
+        tokens = make_tokens(T, V, 0.1, ids, rng)
+        grad = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(grad_dtype)
+        base = torch.from_numpy(rng.standard_normal((V, D)).astype(np.float32)).to(out_dtype) if acc else None
+        out = base.cuda() if acc else None
+        got = tgs_gpu.embedding_grad(tokens.cuda(), grad.cuda(), V, scale=scale, out_dtype=out_dtype, out=out,
+                                     accumulate=acc)
+        assert got.dtype == out_dtype
+        assert_grad(got, tokens, grad, V, scale, base)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,D,masked", [
+    (1, 1, 1, 0.0), (1, 1000, 9, 0.0), (2, 2, 4096, 0.0), (64, 1, 33, 0.0),
+    (4096, 700, 17, 0.05), (4097, 700, 17, 0.5),                    # one workgroup sorts, then many
+    (9_000, 3, 40, 0.0), (20_000, 1, 8, 0.0),                       # tokens that span many chunks
+    (5_000, 1023, 12, 0.1), (5_000, 1024, 12, 0.1),                 # one digit, then two
+    (6_000, 2_000_000, 3, 0.1), (3_000, 3_000_000, 2, 0.1),         # three digits
+    (300_001, 40_000, 6, 0.02),                                     # every sorting workgroup used
+])
+def test_grad_sizes(tgs_gpu, T, V, D, masked):
+    rng = np.random.default_rng(T)
+    tokens = make_tokens(T, V, masked, torch.int64, rng)
+    if masked == 0.0:
+        tokens[0] = V - 1
+    grad = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32))
+    ws = torch.zeros(tgs_gpu.embedding_grad_workspace_bytes(T, V, D), dtype=torch.uint8, device="cuda")
+    ws[32768:] = 0xFF  # scratch holds NaN bits
+    got = tgs_gpu.embedding_grad(tokens.cuda(), grad.cuda(), V, ws=ws)
+    tgs_gpu.check_device_error(ws)
+    assert_grad(got, tokens, grad, V, 1.0)
+
+
+@pytest.mark.gpu
+def test_grad_masked_places_may_hold_anything(tgs_gpu):
+    T, V, D = 6_000, 50, 20
+    rng = np.random.default_rng(1)
+    tokens = make_tokens(T, V, 0.4, torch.int32, rng)
+    grad = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32))
+    clean = grad.clone()
+    grad[tokens < 0] = float("nan")
+    grad[(tokens < 0).nonzero()[::2, 0]] = float("inf")
+    clean[tokens < 0] = 0
+    got = tgs_gpu.embedding_grad(tokens.cuda(), grad.cuda(), V)
+    assert_grad(got, tokens, clean, V, 1.0)
+    # every place masked: zeros, or what was there
+    none = torch.full((T,), -1, device="cuda")
+    assert (tgs_gpu.embedding_grad(none, grad.cuda(), V).cpu().view(torch.int32) == 0).all()
+    base = torch.from_numpy(rng.standard_normal((V, D)).astype(np.float32)).cuda()
+    keep = base.clone()
+    tgs_gpu.embedding_grad(none, grad.cuda(), V, out=base, accumulate=True)
+    assert torch.equal(base, keep)
+    # no places at all
+    assert (tgs_gpu.embedding_grad(none[:0], grad.cuda()[:0], V) == 0).all()
+    tgs_gpu.embedding_grad(none[:0], grad.cuda()[:0], V, out=base, accumulate=True)
+    assert torch.equal(base, keep)
+    # an infinity reaches its own token's row and column only
+    tokens = torch.tensor([3, 7, 3], device="cuda")
+    g = torch.ones(3, D, device="cuda")
+    g[2, 4] = float("inf")
+    out = tgs_gpu.embedding_grad(tokens, g, V)
+    assert out[3, 4] == float("inf") and torch.isfinite(out).sum() == V * D - 1
+
+
+@pytest.mark.gpu
+def test_grad_is_the_lookups_adjoint_and_difference(tgs_gpu):
+    """<g, lookup(E + h dE) - lookup(E)> / h = <grad, dE>: the lookup is linear
+    in the table, so the difference is exact up to rounding."""
+    rng = np.random.default_rng(2)
+    T, V, D, scale = 700, 90, 24, 0.37
+    tokens = make_tokens(T, V, 0.1, torch.int64, rng).cuda()
+    E, dE = (torch.from_numpy(rng.standard_normal((V, D)).astype(np.float32)).cuda() for _ in range(2))
+    g = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).cuda()
+    out = tgs_gpu.embedding_grad(tokens, g, V, scale=scale).double()
+    d = tgs_gpu.embedding_lookup(tokens, E + dE, scale=scale).double() - tgs_gpu.embedding_lookup(
+        tokens, E, scale=scale).double()
+    left, right = (g.double() * d).sum(), (out * dE.double()).sum()
+    # five roundings of values below 2 * 5 * scale a term, T * D terms of either sign
+    bound = (g.double().abs() * (E.double().abs() + dE.double().abs())[tokens.clamp(min=0)]).sum() * scale * 8 * U
+    bound = bound + (out.abs() * dE.double().abs()).sum() * 200 * U
+    assert (left - right).abs() <= bound
+
+
+@pytest.mark.gpu
+def test_grad_same_bits_every_run_on_any_stream_and_in_a_graph(tgs_gpu):
+    rng = np.random.default_rng(3)
+    T, V, D = 30_000, 5_000, 96
+    tokens = make_tokens(T, V, 0.05, torch.int64, rng).cuda()
+    grad = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).bfloat16().cuda()
+    want = tgs_gpu.embedding_grad(tokens, grad, V)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert torch.equal(tgs_gpu.embedding_grad(tokens, grad, V), want)
+        rows = tgs_gpu.embedding_lookup(tokens, want)
+    side.synchronize()
+    ws = torch.zeros(tgs_gpu.embedding_grad_workspace_bytes(T, V, D, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    out, look = torch.empty_like(want), torch.empty_like(rows)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tgs_gpu.embedding_grad(tokens, grad, V, out=out, ws=ws)
+        tgs_gpu.embedding_lookup(tokens, out, out=look, ws=ws)
+    for seed in (4, 5, 6):
+        gen = np.random.default_rng(seed)
+        tokens.copy_(make_tokens(T, V, 0.05, torch.int64, gen))
+        grad.copy_(torch.from_numpy(gen.standard_normal((T, D)).astype(np.float32)))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = tgs_gpu.embedding_grad(tokens, grad, V)
+        assert torch.equal(out, eager)
+        assert torch.equal(look, tgs_gpu.embedding_lookup(tokens, eager))
+    assert_grad(out, tokens.cpu(), grad.cpu(), V, 1.0)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(tgs_gpu):
+    V, D = 70_001, 32_768  # 2.3e9 elements
+    tokens = torch.tensor([V - 1, 0, -1, 65_537, V - 1], device="cuda")
+    g = torch.ones(5, D, dtype=torch.float16, device="cuda")
+    g[3] = 2.0
+    table = tgs_gpu.embedding_grad(tokens, g, V, out_dtype=torch.float16)
+    assert table[V - 1].eq(2).all() and table[0].eq(1).all() and table[65_537].eq(2).all()
+    assert not table[1:65_537].any() and not table[65_538:V - 1].any()
+    rows = tgs_gpu.embedding_lookup(tokens, table)
+    assert rows[:, 0].tolist() == [2, 1, 0, 2, 2] and rows[:, D - 1].tolist() == [2, 1, 0, 2, 2]

@@ -24,6 +24,11 @@ Operations (cited by page title and section):
 * ``rtopk_ef_step``     -- k random entries of the top r (arxivdaily listing,
   entry "rTop-k: A Statistical Estimation Approach to Distributed SGD").
 
+Operators of the training step around it:
+
+* ``embedding_lookup`` / ``embedding_grad`` -- rows of an embedding table with
+  scaling, and the table's dense gradient by sorted tokens.
+
 There is no fallback: if ``libtgs.so`` is missing or cannot be loaded, every
 call raises.
 """
@@ -111,6 +116,15 @@ def _load():
         lib.tgs_rtopk_workspace_bytes.restype = sz
         lib.tgs_rtopk_ef_step.argtypes = [vp, vp, i64, i64, i64, u64, u64, vp, vp, vp, sz, vp]
         lib.tgs_rtopk_ef_step.restype = i32
+        f32 = ctypes.c_float
+        lib.tgs_embedding_lookup_workspace_bytes.argtypes = [i64]
+        lib.tgs_embedding_lookup_workspace_bytes.restype = sz
+        lib.tgs_embedding_lookup.argtypes = [vp, i32, i64, vp, i32, i64, i64, f32, vp, i32, vp, sz, vp]
+        lib.tgs_embedding_lookup.restype = i32
+        lib.tgs_embedding_grad_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+        lib.tgs_embedding_grad_workspace_bytes.restype = sz
+        lib.tgs_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, f32, vp, i32, i32, vp, sz, vp]
+        lib.tgs_embedding_grad.restype = i32
         lib.tgs_status_string.argtypes = [i32]
         lib.tgs_status_string.restype = ctypes.c_char_p
         lib.tgs_last_error.argtypes = []
@@ -584,6 +598,110 @@ def gtopk_merge(idx: torch.Tensor, val: torch.Tensor, n: int, ws: torch.Tensor |
     return out_idx, out_val, mask
 
 
+# ------------------------------------ operators of the training step around --
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int32: 3, torch.int64: 4}
+_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+_TOKENS = (torch.int32, torch.int64)
+
+
+def _require_any(t, dtypes, name, device=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be one of %s, got %s" % (name, ", ".join(map(str, dtypes)), t.dtype))
+    if not t.is_cuda:
+        raise TypeError("%s must be a GPU tensor" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def embedding_lookup_workspace_bytes(T: int) -> int:
+    return int(_load().tgs_embedding_lookup_workspace_bytes(T))
+
+
+def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1.0, out_dtype=None, out=None,
+                     ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows of an embedding table: ``out[..., :] = scale * table[tokens[...]]``.
+
+    ``tokens`` (int32 or int64, any shape) index ``table`` (fp32, bf16 or
+    fp16, ``[V, D]``); a negative token is a masked place and gives a row of
+    zeros.  ``out`` has the shape ``tokens.shape + (D,)`` and the type
+    ``out_dtype`` (the table's if not given).  A token >= V gives zeros and
+    sets the bad-input bit that ``check_device_error(ws)`` reports."""
+    _require_any(table, _FLOATS, "table")
+    dev = table.device
+    _require_any(tokens, _TOKENS, "tokens", dev)
+    if table.dim() != 2:
+        raise ValueError("table must have shape [V, D]")
+    V, D = table.shape
+    if out is None:
+        out_dtype = out_dtype or table.dtype
+        if out_dtype not in _FLOATS:
+            raise TypeError("out_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
+        out = torch.empty((*tokens.shape, D), dtype=out_dtype, device=dev)
+    else:
+        _require_any(out, _FLOATS if out_dtype is None else (out_dtype,), "out", dev)
+        if out.shape != (*tokens.shape, D):
+            raise ValueError("out must have shape %s" % ((*tokens.shape, D),))
+    if ws is None:
+        ws = workspace("embedding", 32768, dev)
+    st = _load().tgs_embedding_lookup(_ptr(tokens), _DTYPES[tokens.dtype], tokens.numel(), _ptr(table),
+                                      _DTYPES[table.dtype], V, D, scale, _ptr(out), _DTYPES[out.dtype],
+                                      ws.data_ptr(), ws.numel(), _stream_handle(dev))
+    if st:
+        _check(st, "tgs_embedding_lookup")
+    return out
+
+
+def embedding_grad_workspace_bytes(T: int, V: int, D: int, grad_dtype=torch.float32, out_dtype=torch.float32) -> int:
+    return int(_load().tgs_embedding_grad_workspace_bytes(T, V, D, _DTYPES[grad_dtype], _DTYPES[out_dtype]))
+
+
+def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, scale: float = 1.0, out_dtype=None,
+                   out=None, accumulate: bool = False, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of ``embedding_lookup`` with respect to its table:
+    ``out[v] = scale * (sum of grad[t] over the places with tokens[t] == v)``,
+    added to ``out`` with ``accumulate``.
+
+    ``grad`` has the shape ``tokens.shape + (D,)``; ``out`` is
+    ``[num_rows, D]`` of type ``out_dtype`` (fp32 if not given, so the result
+    feeds the sparsifier's steps).  Sums are fp32 in a fixed order: equal
+    inputs give equal bits.  Masked places (negative tokens) add to nothing;
+    tokens >= num_rows neither, and set the bad-input bit that
+    ``check_device_error(ws)`` reports."""
+    _require_any(grad, _FLOATS, "grad")
+    dev = grad.device
+    _require_any(tokens, _TOKENS, "tokens", dev)
+    if grad.dim() < 1 or grad.shape[:-1] != tokens.shape:
+        raise ValueError("grad must have the shape of tokens and one dimension more")
+    V, D = int(num_rows), grad.shape[-1]
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out_dtype = out_dtype or torch.float32
+        if out_dtype not in _FLOATS:
+            raise TypeError("out_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
+        out = torch.empty((V, D), dtype=out_dtype, device=dev)
+    else:
+        _require_any(out, _FLOATS if out_dtype is None else (out_dtype,), "out", dev)
+        if out.shape != (V, D):
+            raise ValueError("out must have shape %s" % ((V, D),))
+    lib = _load()
+    T, gt, ot = tokens.numel(), _DTYPES[grad.dtype], _DTYPES[out.dtype]
+    if ws is None:
+        need = lib.tgs_embedding_grad_workspace_bytes(T, V, D, gt, ot)
+        if need == 0:
+            raise ValueError("invalid sizes T=%d num_rows=%d D=%d" % (T, V, D))
+        ws = workspace("embedding", need, dev)
+    st = lib.tgs_embedding_grad(_ptr(tokens), _DTYPES[tokens.dtype], T, _ptr(grad), gt, V, D, scale, _ptr(out), ot,
+                                bool(accumulate), ws.data_ptr(), ws.numel(), _stream_handle(dev))
+    if st:
+        _check(st, "tgs_embedding_grad")
+    return out
+
+
 def check_device_error(ws: torch.Tensor):
     """Waits for the current stream, then reads and clears the workspace's
     device error word: raises ValueError for bad merge input, TgsError for a
@@ -622,6 +740,7 @@ __all__ = [
     "gtopk_workspace_bytes", "check_device_error", "error_word", "workspace_init", "set_option",
     "threshold_estimate", "threshold_estimate_workspace_bytes", "threshold_ef_step_dev",
     "estimated_threshold_ef_step", "rtopk_ef_step", "rtopk_workspace_bytes",
+    "embedding_lookup", "embedding_lookup_workspace_bytes", "embedding_grad", "embedding_grad_workspace_bytes",
     "profile_next_call", "profile_elapsed_ms", "library", "workspace",
     "TgsError", "OPT_TOPK_PATH", "OPT_MAIN_GRID", "LIB_PATH",
 ]
