@@ -303,6 +303,50 @@ tgs_status tgs_embedding_grad(const void* tokens, tgs_dtype tokens_dtype, int64_
                               tgs_dtype grad_dtype, int64_t V, int64_t D, float scale, void* out, tgs_dtype out_dtype,
                               int32_t accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Bytes of workspace tgs_newton_schulz needs (0 if the sizes or the type are
+   invalid): 8 bytes an entry of x (padded to tiles of 64 or 128 a side) and 4
+   of the smaller square with 16-bit types, twice that with fp32. */
+size_t tgs_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, tgs_dtype dtype);
+
+/*
+ * Orthogonalises a stack of matrices by Newton-Schulz products: for each
+ *   X <- x / (|x|_F + eps), then `steps` times
+ *   A = X X^T,  X <- a X + (b A + c A^2) X        (X^T X where rows > cols)
+ *   x, out    [batch][rows][cols] of one type (fp32, bf16, fp16).  out may be
+ *             x itself, and must not overlap it otherwise.
+ * 1 <= batch <= 65535, 1 <= rows, cols <= 65536, 1 <= steps <= 64, eps >= 0.
+ * Coefficients with which a singular value that starts in [0, 1] could pass
+ * 2^30 are refused.  The products use fp16 operands scaled by powers of two
+ * and fp32 sums: fp32 results are as exact as with fp32 products (three fp16
+ * products each), 16-bit results are within half the error of their final
+ * rounding for matrices like gradients.  A NaN or infinity in x makes its
+ * matrix's result NaN.  Equal inputs give equal bits.
+ */
+tgs_status tgs_newton_schulz(const void* x, tgs_dtype dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps,
+                             float a, float b, float c, float eps, void* out, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/* Bytes of workspace tgs_muon_step needs (0 if the sizes or the type are
+   invalid): what tgs_newton_schulz needs for the weights' type. */
+size_t tgs_muon_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, tgs_dtype weight_dtype);
+
+/*
+ * One Muon step for a stack of weight matrices:
+ *   momentum <- beta momentum + grad
+ *   u = grad + beta momentum (nesterov != 0), or momentum
+ *   O = u orthogonalised as tgs_newton_schulz does
+ *   weight <- (1 - lr weight_decay) weight - lr sqrt(max(1, rows / cols)) O
+ *   weight    [batch][rows][cols] fp32, bf16 or fp16, in/out.
+ *   grad      [batch][rows][cols] fp32, bf16 or fp16, read only.
+ *   momentum  [batch][rows][cols] fp32, in/out.
+ * The arrays must not overlap.  Sizes, coefficients, exactness (by the
+ * weights' type) as tgs_newton_schulz.
+ */
+tgs_status tgs_muon_step(void* weight, tgs_dtype weight_dtype, const void* grad, tgs_dtype grad_dtype, float* momentum,
+                         int64_t batch, int64_t rows, int64_t cols, float lr, float beta, int32_t nesterov,
+                         float weight_decay, int32_t steps, float a, float b, float c, float eps, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
 /* Waits for `stream`, then reads and clears the device error word of
    `workspace`: TGS_OK if no kernel flagged a problem since it was last read,
    TGS_EINVAL for an input index outside its range (a merge row's index out

@@ -28,6 +28,8 @@ Operators of the training step around it:
 
 * ``embedding_lookup`` / ``embedding_grad`` -- rows of an embedding table with
   scaling, and the table's dense gradient by sorted tokens.
+* ``newton_schulz`` / ``muon_step`` -- a matrix orthogonalised by Newton-Schulz
+  products, and the Muon update of weight matrices that takes it.
 
 There is no fallback: if ``libtgs.so`` is missing or cannot be loaded, every
 call raises.
@@ -125,6 +127,15 @@ def _load():
         lib.tgs_embedding_grad_workspace_bytes.restype = sz
         lib.tgs_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, f32, vp, i32, i32, vp, sz, vp]
         lib.tgs_embedding_grad.restype = i32
+        lib.tgs_newton_schulz_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        lib.tgs_newton_schulz_workspace_bytes.restype = sz
+        lib.tgs_newton_schulz.argtypes = [vp, i32, i64, i64, i64, i32, f32, f32, f32, f32, vp, vp, sz, vp]
+        lib.tgs_newton_schulz.restype = i32
+        lib.tgs_muon_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        lib.tgs_muon_workspace_bytes.restype = sz
+        lib.tgs_muon_step.argtypes = [vp, i32, vp, i32, vp, i64, i64, i64, f32, f32, i32, f32, i32, f32, f32, f32, f32,
+                                      vp, sz, vp]
+        lib.tgs_muon_step.restype = i32
         lib.tgs_status_string.argtypes = [i32]
         lib.tgs_status_string.restype = ctypes.c_char_p
         lib.tgs_last_error.argtypes = []
@@ -702,6 +713,92 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, scal
     return out
 
 
+NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _matrices(t, name):
+    """(batch, rows, cols) of a matrix or a stack of matrices."""
+    if t.dim() == 2:
+        return 1, t.shape[0], t.shape[1]
+    if t.dim() == 3:
+        return t.shape[0], t.shape[1], t.shape[2]
+    raise ValueError("%s must have shape [rows, cols] or [batch, rows, cols]" % name)
+
+
+def newton_schulz_workspace_bytes(batch: int, rows: int, cols: int, dtype=torch.float32) -> int:
+    return int(_load().tgs_newton_schulz_workspace_bytes(batch, rows, cols, _DTYPES[dtype]))
+
+
+def newton_schulz(x: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps: float = 1e-7,
+                  out=None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Orthogonalises a matrix, or each of a stack of matrices: ``X = x /
+    (|x|_F + eps)``, then ``steps`` times ``X <- a X + (b A + c A^2) X`` with
+    ``A = X X^T`` (over the shorter side).  ``out`` has ``x``'s shape and type
+    (fp32, bf16, fp16) and may be ``x`` itself."""
+    _require_any(x, _FLOATS, "x")
+    dev = x.device
+    b, m, n = _matrices(x, "x")
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _require_any(out, (x.dtype,), "out", dev)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+    if x.numel() == 0:
+        return out
+    lib = _load()
+    dt = _DTYPES[x.dtype]
+    if ws is None:
+        need = lib.tgs_newton_schulz_workspace_bytes(b, m, n, dt)
+        if need == 0:
+            raise ValueError("invalid sizes batch=%d rows=%d cols=%d" % (b, m, n))
+        ws = workspace("muon", need, dev)
+    ca, cb, cc = coefficients
+    st = lib.tgs_newton_schulz(x.data_ptr(), dt, b, m, n, steps, ca, cb, cc, eps, out.data_ptr(), ws.data_ptr(),
+                               ws.numel(), _stream_handle(dev))
+    if st:
+        _check(st, "tgs_newton_schulz")
+    return out
+
+
+def muon_workspace_bytes(batch: int, rows: int, cols: int, weight_dtype=torch.float32) -> int:
+    return int(_load().tgs_muon_workspace_bytes(batch, rows, cols, _DTYPES[weight_dtype]))
+
+
+def muon_step(weight: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: float, beta: float = 0.95,
+              nesterov: bool = True, weight_decay: float = 0.0, steps: int = 5,
+              coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps: float = 1e-7, ws: torch.Tensor | None = None):
+    """One Muon step for a weight matrix, or a stack of them: ``momentum <-
+    beta momentum + grad``, ``u = grad + beta momentum`` (or ``momentum``
+    without ``nesterov``), ``O = newton_schulz(u)``, ``weight <- (1 - lr
+    weight_decay) weight - lr sqrt(max(1, rows / cols)) O``.  ``weight`` and
+    ``grad`` are fp32, bf16 or fp16, ``momentum`` is fp32; weight and momentum
+    are updated in place.  Returns ``weight``."""
+    _require_any(weight, _FLOATS, "weight")
+    dev = weight.device
+    _require_any(grad, _FLOATS, "grad", dev)
+    _require_any(momentum, (torch.float32,), "momentum", dev)
+    b, m, n = _matrices(weight, "weight")
+    if grad.shape != weight.shape or momentum.shape != weight.shape:
+        raise ValueError("weight, grad and momentum must have one shape")
+    if weight.numel() == 0:
+        return weight
+    lib = _load()
+    wt = _DTYPES[weight.dtype]
+    if ws is None:
+        need = lib.tgs_muon_workspace_bytes(b, m, n, wt)
+        if need == 0:
+            raise ValueError("invalid sizes batch=%d rows=%d cols=%d" % (b, m, n))
+        ws = workspace("muon", need, dev)
+    ca, cb, cc = coefficients
+    st = lib.tgs_muon_step(weight.data_ptr(), wt, grad.data_ptr(), _DTYPES[grad.dtype], momentum.data_ptr(), b, m, n,
+                           lr, beta, bool(nesterov), weight_decay, steps, ca, cb, cc, eps, ws.data_ptr(), ws.numel(),
+                           _stream_handle(dev))
+    if st:
+        _check(st, "tgs_muon_step")
+    return weight
+
+
 def check_device_error(ws: torch.Tensor):
     """Waits for the current stream, then reads and clears the workspace's
     device error word: raises ValueError for bad merge input, TgsError for a
@@ -740,6 +837,8 @@ __all__ = [
     "gtopk_workspace_bytes", "check_device_error", "error_word", "workspace_init", "set_option",
     "threshold_estimate", "threshold_estimate_workspace_bytes", "threshold_ef_step_dev",
     "estimated_threshold_ef_step", "rtopk_ef_step", "rtopk_workspace_bytes",
+    "newton_schulz", "newton_schulz_workspace_bytes", "muon_step", "muon_workspace_bytes",
+    "NEWTON_SCHULZ_COEFFICIENTS",
     "embedding_lookup", "embedding_lookup_workspace_bytes", "embedding_grad", "embedding_grad_workspace_bytes",
     "profile_next_call", "profile_elapsed_ms", "library", "workspace",
     "TgsError", "OPT_TOPK_PATH", "OPT_MAIN_GRID", "LIB_PATH",
