@@ -142,8 +142,11 @@ def test_the_oracle_on_closed_forms():
 
 
 # ------------------------------------------------------------------- GPU --
-SHAPES = [(1, 1), (1, 9), (9, 1), (3, 5), (33, 31), (64, 64), (65, 63), (127, 129), (40, 700), (1000, 24), (130, 1030),
-          (300, 200), (513, 520), (530, 1100), (1100, 530), (3, 20, 36), (5, 70, 33), (2, 520, 640)]
+SHAPES = [(1, 1), (1, 9), (9, 1), (3, 5), (33, 31), (64, 64), (65, 63), (127, 129), (40, 700), (1000, 24),
+          (130, 1030), (300, 200), (513, 520), (530, 1100), (1100, 530), (3, 20, 36), (5, 70, 33), (2, 520, 640),
+          # shorter side up to 64: one workgroup a matrix, then chunks of columns
+          (64, 512), (513, 64), (30, 1024), (1025, 20), (32, 257), (129, 33), (16, 128), (1, 5000), (64, 8192),
+          (8192, 31), (40, 40, 2000), (130, 1500, 17), (7, 64, 600)]
 
 
 @pytest.mark.gpu
@@ -253,6 +256,7 @@ def muon_exact(w, g, m, lr, beta, nesterov, wd):
 @pytest.mark.parametrize("weight_dtype", FLOATS)
 @pytest.mark.parametrize("grad_dtype", FLOATS)
 @pytest.mark.parametrize("shape,nesterov", [((33, 50), True), ((129, 40), False), ((2, 70, 90), True),
+                                            ((3, 2000, 30), True), ((50, 700), True),
                                             ((530, 700), False)])
 def test_muon_step(tgs_gpu, weight_dtype, grad_dtype, shape, nesterov):
     lr, beta, wd = 0.02, 0.95, 0.1

@@ -31,22 +31,28 @@
 #include <cmath>
 #include <type_traits>
 
-#include "tgs_host.h"
-#include "tgs_types.h"
+#include "tgs_orthogonal.h"
 
 namespace tgs {
 
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int kBK = 64;        // summation indices a stage: rows of 128 bytes in LDS
-constexpr int kNormBlocks = 128;  // partial sums of squares a matrix
 
 // ------------------------------------------------------- norm and packing --
+struct NormArgs {
+  const void* x;    // [batch][rows][cols] matrix or gradient
+  float* momentum;  // [batch][rows][cols], or null: x itself is orthogonalised
+  double* part;     // [batch][blocks]
+  int64_t count;    // rows * cols
+  int blocks, nesterov;
+  float beta;
+};
+
 struct PackArgs {
-  const void* x;     // [batch][rows][cols] matrix or gradient
-  float* momentum;   // [batch][rows][cols], or null: x itself is orthogonalised
-  double* part;      // [batch][blocks]
+  const void* x;
+  const float* momentum;
+  const double* part;
   _Float16* xh;      // [batch][mp][np] high and low parts of X
   _Float16* xl;
   _Float16* th;      // [batch][np][mp] the transpose
@@ -59,13 +65,8 @@ struct PackArgs {
   double eps;
 };
 
-// The value that is orthogonalised, given the gradient and the new momentum.
-__device__ __forceinline__ float muon_u(const PackArgs& a, float g, float m) {
-  return a.nesterov ? fmaf(a.beta, m, g) : m;
-}
-
 template <class T, bool MUON>
-__global__ __launch_bounds__(256) void k_ns_norm(PackArgs a) {
+__global__ __launch_bounds__(256) void k_ns_norm(NormArgs a) {
   __shared__ double s_sum[4];
   const int64_t base = (int64_t)blockIdx.y * a.count;
   const T* x = (const T*)a.x + base;
@@ -82,8 +83,8 @@ __global__ __launch_bounds__(256) void k_ns_norm(PackArgs a) {
       for (int e = 0; e < E; ++e) {
         float v = to_f32(g.v[e]);
         if (MUON) {
-          m.v[e] = fmaf(a.beta, m.v[e], v);
-          v = muon_u(a, v, m.v[e]);
+          m.v[e] = new_momentum(a.beta, m.v[e], v);
+          v = muon_u(a.nesterov, a.beta, v, m.v[e]);
         }
         sum = fma((double)v, (double)v, sum);
       }
@@ -92,9 +93,9 @@ __global__ __launch_bounds__(256) void k_ns_norm(PackArgs a) {
       for (int64_t j = i; j < a.count; ++j) {
         float v = to_f32(x[j]);
         if (MUON) {
-          const float m = fmaf(a.beta, mom[j], v);
+          const float m = new_momentum(a.beta, mom[j], v);
           mom[j] = m;
-          v = muon_u(a, v, m);
+          v = muon_u(a.nesterov, a.beta, v, m);
         }
         sum = fma((double)v, (double)v, sum);
       }
@@ -107,9 +108,21 @@ __global__ __launch_bounds__(256) void k_ns_norm(PackArgs a) {
   if (threadIdx.x == 0) a.part[(int64_t)blockIdx.y * a.blocks + blockIdx.x] = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
 }
 
-__device__ __forceinline__ void split_half(float v, _Float16& h, _Float16& l) {
-  h = (_Float16)v;
-  l = (_Float16)(v - (float)h);
+void launch_norm(const NsCall& q, double* part, int blocks, hipStream_t stream) {
+  NormArgs a{};
+  a.x = q.x;
+  a.momentum = q.momentum;
+  a.part = part;
+  a.count = q.rows * q.cols;
+  a.blocks = blocks;
+  a.nesterov = q.nesterov;
+  a.beta = q.beta;
+  with_float_dtype(q.x_dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    const dim3 grid(blocks, (unsigned)q.batch);
+    if (q.momentum) hipLaunchKernelGGL((k_ns_norm<T, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_ns_norm<T, false>), grid, dim3(256), 0, stream, a);
+  });
 }
 
 // One 64 x 64 tile of x: normalised, scaled, written to X and its transpose,
@@ -136,7 +149,7 @@ __global__ __launch_bounds__(256) void k_ns_pack(PackArgs a) {
     float v = 0.0f;
     if (r < a.rows && c < a.cols) {
       v = to_f32(x[(int64_t)r * a.cols + c]);
-      if (MUON) v = muon_u(a, v, mom[(int64_t)r * a.cols + c]);
+      if (MUON) v = muon_u(a.nesterov, a.beta, v, mom[(int64_t)r * a.cols + c]);
       v = (float)((double)v * inv) * a.sx;
     }
     s_t[i][tx] = v;
@@ -465,12 +478,6 @@ __global__ __launch_bounds__(WR* WC* kWave) void k_ns_product(ProductArgs a) {
 }
 
 // ------------------------------------------------------------------ host --
-constexpr int kMaxSteps = 64;
-
-struct StepScales {
-  float x[kMaxSteps + 1], a[kMaxSteps], p[kMaxSteps];
-};
-
 // 2^e with bound * 2^e <= 2^14.
 static float scale_for(double bound) {
   int e = 0;
@@ -510,7 +517,7 @@ static bool step_scales(int steps, double a, double b, double c, StepScales* s) 
 
 struct NsPlan {
   int m, n, mp, np, tall, tile, blocks;
-  bool split;
+  bool split, small;
   size_t part, diag_a, diag_p, x, t[2], e, p, total;  // byte offsets
   int64_t x_low, t_low, e_low, p_low;                 // elements between high and low parts
 };
@@ -521,6 +528,11 @@ static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPla
   p->m = (int)std::min(rows, cols);
   p->n = (int)std::max(rows, cols);
   p->split = split;
+  p->small = p->m <= kSmallSide;
+  if (p->small) {
+    p->total = small_workspace_bytes(batch, rows, cols);
+    return true;
+  }
   p->tile = p->m > 512 ? 128 : 64;
   auto up = [](int64_t v, int64_t to) { return (v + to - 1) / to * to; };
   p->mp = (int)up(p->m, p->tile);
@@ -546,21 +558,6 @@ static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPla
   p->total = at;
   return true;
 }
-
-struct NsCall {
-  const char* what;
-  const void* x;
-  tgs_dtype x_dtype;
-  float* momentum;
-  void* out;
-  tgs_dtype out_dtype;
-  int64_t batch, rows, cols;
-  float beta;
-  int nesterov;
-  float keep, gain;
-  int steps;
-  double a, b, c, eps;
-};
 
 template <Product K, bool SPLIT, class TW, bool MUON>
 static void launch_product(const NsPlan& p, const ProductArgs& a, int batch, hipStream_t stream) {
@@ -636,11 +633,17 @@ static void run_steps(const NsCall& q, const NsPlan& p, const StepScales& s, cha
 
 template <bool MUON>
 static tgs_status ns_run(const NsCall& q, const NsPlan& p, const StepScales& s, void* workspace, hipStream_t stream) {
+  if (p.small) {
+    small_run(q, s, workspace, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(TGS_EHIP, "%s: launch failed: %s", q.what, hipGetErrorString(e));
+    return TGS_OK;
+  }
   char* ws = (char*)workspace;
   PackArgs k{};
   k.x = q.x;
   k.momentum = q.momentum;
-  k.part = (double*)(ws + p.part);
+  k.part = (const double*)(ws + p.part);
   k.xh = (_Float16*)(ws + p.x);
   k.xl = k.xh + p.x_low;
   k.th = (_Float16*)(ws + p.t[0]);
@@ -656,10 +659,10 @@ static tgs_status ns_run(const NsCall& q, const NsPlan& p, const StepScales& s, 
   k.beta = q.beta;
   k.sx = s.x[0];
   k.eps = q.eps;
+  launch_norm(q, (double*)(ws + p.part), p.blocks, stream);
   const dim3 tiles((p.tall ? p.mp : p.np) / 64, (p.tall ? p.np : p.mp) / 64, (unsigned)q.batch);
   with_float_dtype(q.x_dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    hipLaunchKernelGGL((k_ns_norm<T, MUON>), dim3(p.blocks, (unsigned)q.batch), dim3(256), 0, stream, k);
     hipLaunchKernelGGL((k_ns_pack<T, MUON>), tiles, dim3(256), 0, stream, k);
   });
   with_float_dtype(q.out_dtype, [&](auto* t) {

@@ -1,0 +1,56 @@
+// What the two routes of the Newton-Schulz operators share: the host's plan of
+// a call, the scales of its steps, and the small route's entry.
+#pragma once
+
+#include "tgs_host.h"
+#include "tgs_types.h"
+
+namespace tgs {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+
+constexpr int kMaxSteps = 64;
+constexpr int kNormBlocks = 128;  // partial sums of squares a matrix
+
+// Powers of two that X (before each step, 1 after the last), A and P are held at.
+struct StepScales {
+  float x[kMaxSteps + 1], a[kMaxSteps], p[kMaxSteps];
+};
+
+struct NsCall {
+  const char* what;
+  const void* x;  // matrix, or gradient of a Muon step
+  tgs_dtype x_dtype;
+  float* momentum;  // null: x itself is orthogonalised
+  void* out;        // result, or the weights that are updated
+  tgs_dtype out_dtype;
+  int64_t batch, rows, cols;
+  float beta;
+  int nesterov;
+  float keep, gain;  // w = keep * w + gain * O
+  int steps;
+  double a, b, c, eps;
+};
+
+// v = high + low fp16 part.
+__device__ __forceinline__ void split_half(float v, _Float16& h, _Float16& l) {
+  h = (_Float16)v;
+  l = (_Float16)(v - (float)h);
+}
+
+// The new momentum, and the value that is orthogonalised.
+__device__ __forceinline__ float new_momentum(float beta, float m, float g) { return fmaf(beta, m, g); }
+__device__ __forceinline__ float muon_u(int nesterov, float beta, float g, float m) {
+  return nesterov ? fmaf(beta, m, g) : m;
+}
+
+// Sums of squares of what is orthogonalised (and the momentum's update): one
+// partial sum a workgroup at part[batch][blocks].
+void launch_norm(const NsCall& q, double* part, int blocks, hipStream_t stream);
+
+// The route for matrices whose shorter side is at most kSmallSide.
+constexpr int kSmallSide = 64;
+size_t small_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+void small_run(const NsCall& q, const StepScales& s, void* workspace, hipStream_t stream);
+
+}  // namespace tgs
