@@ -304,8 +304,9 @@ tgs_status tgs_embedding_grad(const void* tokens, tgs_dtype tokens_dtype, int64_
                               int32_t accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace tgs_newton_schulz needs (0 if the sizes or the type are
-   invalid): 8 bytes an entry of x (padded to tiles of 64 or 128 a side) and 4
-   of the smaller square with 16-bit types, twice that with fp32. */
+   invalid): 8 bytes an entry of x (padded to 128 a side) and 4 of the smaller
+   square with 16-bit types, twice that with fp32, and up to 17 MB for sums
+   that workgroups share. */
 size_t tgs_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, tgs_dtype dtype);
 
 /*

@@ -13,6 +13,17 @@
 //   update   P X = P (X^T)^T    operands P, X^T
 // X is kept in both orders; the update's epilogue writes both.
 //
+// A workgroup makes a tile of C: stages of 128 bytes a row of both operands go
+// from memory to a ring in LDS (asynchronous loads, one to three stages ahead),
+// the operands of the next 16 summation indices are read while these are
+// multiplied.  Square tiles of 64 to 256 a side, picked by a model of the time
+// (pick_shape).  256 tiles of 256 (4,096 square, update) take 141 us, as a library's
+// 4,096 product does (114 us without the epilogue); the symmetric products of
+// that size take 253 tiles of 192 rather than 136 of 256, which leave half the
+// device idle (four products of 4,096: 1,653 against 1,843 us for the whole
+// call).  Small matrices with a long side have few tiles with long sums, so
+// workgroups share them (gram of 200 x 8,000: 31 -> 12 us).
+//
 // What is rounded.  The diagonals of A and P are large against the rest near
 // the end (A tends to the identity), so they are held apart in fp32 and the
 // products see only the off-diagonal part E of A and of P:
@@ -37,7 +48,16 @@ namespace tgs {
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 
-constexpr int kBK = 64;        // summation indices a stage: rows of 128 bytes in LDS
+constexpr int kBK = 64;         // elements of a row a stage: rows of 128 bytes in LDS
+constexpr int kSplitCols = 32;  // columns of high parts, then as many of low parts, in a split row
+
+// Where a matrix of rows of ld elements holds (row, col).  Split matrices
+// interleave: 32 columns' high parts, then their low parts, so that a stage of
+// 128 bytes a row holds both.
+template <bool SPLIT>
+__device__ __forceinline__ int64_t place_of(int row, int col, int ld) {
+  return SPLIT ? (int64_t)row * 2 * ld + (col / kSplitCols) * 2 * kSplitCols + col % kSplitCols : (int64_t)row * ld + col;
+}
 
 // ------------------------------------------------------- norm and packing --
 struct NormArgs {
@@ -53,12 +73,14 @@ struct PackArgs {
   const void* x;
   const float* momentum;
   const double* part;
-  _Float16* xh;      // [batch][mp][np] high and low parts of X
-  _Float16* xl;
-  _Float16* th;      // [batch][np][mp] the transpose
-  _Float16* tl;      // null: high part only
+  _Float16* x_out;   // X, then low parts x_low behind
+  _Float16* t_out;   // the transpose; with split, low parts as X
+  int64_t x_low;
   int64_t count;     // rows * cols
   int rows, cols, mp, np, blocks;
+  int split;
+  u32* arrived;  // counters to clear
+  int arrive;
   int tall;          // rows > cols: X is the transpose of x
   int nesterov;
   float beta, sx;
@@ -72,7 +94,7 @@ __global__ __launch_bounds__(256) void k_ns_norm(NormArgs a) {
   const T* x = (const T*)a.x + base;
   float* mom = MUON ? a.momentum + base : nullptr;
   double sum = 0.0;
-  constexpr int E = 4;
+  constexpr int E = 8;
   const int64_t step = (int64_t)gridDim.x * 256 * E;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * E; i < a.count; i += step) {
     if (i + E <= a.count) {
@@ -134,11 +156,19 @@ __global__ __launch_bounds__(256) void k_ns_pack(PackArgs a) {
   const int64_t base = (int64_t)blockIdx.z * a.count;
   const T* x = (const T*)a.x + base;
   const float* mom = MUON ? a.momentum + base : nullptr;
-  // every wave adds the partial sums itself, in the same order
+  {
+    const int64_t i = (((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+    if (i < a.arrive) a.arrived[i] = 0;
+  }
+  // every workgroup adds the partial sums itself, in the same order
+  __shared__ double s_sum[4];
   double sum = 0.0;
-  for (int i = lane_id(); i < a.blocks; i += kWave) sum += a.part[(int64_t)blockIdx.z * a.blocks + i];
+  for (int i = threadIdx.x; i < a.blocks; i += 256) sum += a.part[(int64_t)blockIdx.z * a.blocks + i];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  if (lane_id() == 0) s_sum[threadIdx.x / kWave] = sum;
+  __syncthreads();
+  sum = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
   const double inv = 1.0 / (sqrt(sum) + a.eps);
   // rows and columns of x's own order
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
@@ -155,10 +185,17 @@ __global__ __launch_bounds__(256) void k_ns_pack(PackArgs a) {
     s_t[i][tx] = v;
   }
   __syncthreads();
-  const int64_t plane = (int64_t)blockIdx.z * a.mp * a.np;
   // in x's order: X, or its transpose where x is tall
+  const int64_t plane = (int64_t)blockIdx.z * a.mp * a.np * (a.split ? 2 : 1);
   const int ld = a.tall ? a.mp : a.np, ldt = a.tall ? a.np : a.mp;
   const int vec = threadIdx.x % 8, line = threadIdx.x / 8;
+  auto put = [&](int row, int col, int stride, bool is_x, h8 h, h8 l) {
+    _Float16* to = (is_x ? a.x_out : a.t_out) + plane +
+                   (a.split ? place_of<true>(row, col, stride) : place_of<false>(row, col, stride));
+    *(h8*)to = h;
+    if (a.split) *(h8*)(to + kSplitCols) = l;
+    else if (is_x) *(h8*)(to + a.x_low) = l;
+  };
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int i = half * 32 + line;
@@ -173,19 +210,8 @@ __global__ __launch_bounds__(256) void k_ns_pack(PackArgs a) {
       hx[e] = p;
       lx[e] = q;
     }
-    const int64_t at = plane + (int64_t)(r0 + i) * ld + c0 + vec * 8;
-    const int64_t att = plane + (int64_t)(c0 + i) * ldt + r0 + vec * 8;
-    if (a.tall) {
-      *(h8*)(a.th + at) = h;
-      if (a.tl) *(h8*)(a.tl + at) = l;
-      *(h8*)(a.xh + att) = hx;
-      *(h8*)(a.xl + att) = lx;
-    } else {
-      *(h8*)(a.xh + at) = h;
-      *(h8*)(a.xl + at) = l;
-      *(h8*)(a.th + att) = hx;
-      if (a.tl) *(h8*)(a.tl + att) = lx;
-    }
+    put(r0 + i, c0 + vec * 8, ld, !a.tall, h, l);
+    put(c0 + i, r0 + vec * 8, ldt, a.tall, hx, lx);
   }
 }
 
@@ -193,26 +219,25 @@ __global__ __launch_bounds__(256) void k_ns_pack(PackArgs a) {
 enum Product { kGram, kSquare, kUpdate, kLast };
 
 struct ProductArgs {
-  // operands of C = L R^T: [rows][ld], summation length k (a multiple of 64);
-  // the low parts lie `low` elements behind the high ones
+  // operands of C = L R^T: rows `stride` elements apart, `stages` stages of 64 elements
   const _Float16* l;
   const _Float16* r;
-  int64_t l_low, r_low;
   int64_t l_batch, r_batch;  // elements between matrices of a batch
-  int ld, k;
+  int stride, stages;
   int mp, np;      // C is [mp][mp] (gram, square) or [mp][np]
-  int tiles_n;     // column tiles (update)
+  int tiles, tiles_n;  // tiles a matrix; of them in a row (update)
+  int units, share;  // gram, square: stages of all tiles, and of them a workgroup's
+  float* sums;       // gram, square: [workgroups][2][B * B] partial sums of tiles that workgroups share
+  u32* arrived;      // of their workgroups, per tile; zero between products
   float scale;     // accumulator to true value
   // in/out of the epilogues
   float* diag_a;   // [batch][mp] diagonal of A
   float* diag_p;   // [batch][mp] diagonal of P
-  _Float16* e;     // gram: out, square: in; off-diagonal part of A, low part e_low behind
+  _Float16* e;     // gram: out, square: in; off-diagonal part of A
   _Float16* p;     // square: out
-  int64_t e_low, p_low;
-  _Float16* xh;    // update: X in and out
-  _Float16* xl;
-  _Float16* th;    // update: transpose out
-  _Float16* tl;
+  _Float16* x;     // update: X in and out
+  _Float16* t;     // update: transpose out
+  int64_t x_low;   // X's low parts behind its high ones (not split)
   float store;     // scale of what is stored
   float load;      // 1 / scale of X or E as read
   float ca, cb, cc;
@@ -222,258 +247,397 @@ struct ProductArgs {
   float keep, gain;  // muon: w = keep * w + gain * O
 };
 
-// Stage layout: row r of a 64-column stage is 8 chunks of 16 bytes, chunk c at
-// place c ^ ((r >> 1) & 7).
+// A workgroup's share of a product: a B x B tile, WR x WC waves, a ring of S
+// stages in LDS.  SHARE: workgroups take equal runs of the list of all tiles'
+// stages (symmetric products).
+template <int B_, int WR_, int WC_, int S_, bool SHARE_ = false>
+struct Shape {
+  static constexpr bool SHARE = SHARE_;
+  static constexpr int B = B_, WR = WR_, WC = WC_, S = S_, WAVES = WR_ * WC_;
+  static constexpr int WM = B_ / WR_, WN = B_ / WC_, MI = WM / 32, NI = WN / 32;
+  static constexpr int LOADS = 2 * B_ / (8 * WAVES);  // 16-byte loads a lane and stage
+};
+
+// Stage layout: row r of a 64-element stage is 8 chunks of 16 bytes, chunk c at
+// place c ^ ((r >> 1) & 7): 16 lanes that read one chunk of 16 rows then cover
+// all 64 banks.
 __device__ __forceinline__ int chunk_place(int r, int c) { return c ^ ((r >> 1) & 7); }
 
 // 16 bytes a lane from global memory to LDS (base + 16 * lane), asynchronously.
-__device__ __forceinline__ void load_to_lds(const _Float16* from, _Float16* to) {
+__device__ __forceinline__ void load_to_lds(const char* from, _Float16* to) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
                                    (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
-template <int ROWS, int WAVES>
-__device__ __forceinline__ void load_stage(const _Float16* base, const u32 (&off)[ROWS / (8 * WAVES)], _Float16* lds,
-                                           int wave) {
-#pragma unroll
-  for (int i = 0; i < ROWS / (8 * WAVES); ++i) load_to_lds(base + off[i], lds + (i * WAVES + wave) * 8 * kBK);
+// Waits until at most `left` (0, 1 or 2) stages of N loads each are in flight
+// and every read of LDS is done, then meets the other waves: what they loaded
+// is there, and what they read may be overwritten.
+template <int N>
+__device__ __forceinline__ void stage_barrier(int left) {
+  if (left >= 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * N) : "memory");
+  else if (left == 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+  else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <int MI, int NI>
-__device__ __forceinline__ void multiply_stage(const _Float16* sl, const _Float16* sr, int l_row, int r_row,
-                                               f16v (&acc)[MI][NI]) {
-  const int lane = lane_id(), i = lane & 31, hi = lane >> 5;
-#pragma unroll
-  for (int kk = 0; kk < kBK / 16; ++kk) {
-    h8 x[MI], y[NI];
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      const int row = l_row + mi * 32 + i;
-      x[mi] = *(const h8*)(sl + row * kBK + chunk_place(row, kk * 2 + hi) * 8);
-    }
-#pragma unroll
-    for (int ni = 0; ni < NI; ++ni) {
-      const int row = r_row + ni * 32 + i;
-      y[ni] = *(const h8*)(sr + row * kBK + chunk_place(row, kk * 2 + hi) * 8);
-    }
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni)
-        acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[mi], y[ni], acc[mi][ni], 0, 0, 0);
-  }
-}
+// What the epilogue reads for eight columns of one row, fetched ahead of the
+// stores before it (which the compiler must take for changing it).
+template <class TW>
+struct Fetched {
+  h8 hi, lo;       // X, or E
+  float d_row;     // of P's diagonal, or A's
+  Vec<TW, 8> old;  // weights
+};
 
 // Eight columns of one row of the result, in place in v: the epilogue's values
 // in the scale that is stored; written in row order.
-template <Product K, bool SPLIT, class TW, bool MUON>
-__device__ __forceinline__ void finish_row(const ProductArgs& a, int64_t plane_c, int64_t diag, int row, int col,
-                                           float (&v)[8], float d_row) {
-  const int ldc = K == kGram || K == kSquare ? a.mp : a.np;
-  const int64_t at = plane_c + (int64_t)row * ldc + col;
-  if constexpr (K == kGram) {
-    h8 h, l;
+template <Product K, bool SPLIT, class TW>
+__device__ __forceinline__ void finish_row(const ProductArgs& a, int64_t at, int64_t diag, int row, int col,
+                                           float (&v)[8], const Fetched<TW>& f, const float (&d_col)[8]) {
+  const int64_t x_low = SPLIT ? kSplitCols : a.x_low;
+  h8 h, l;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (K == kGram) {
       const float t = v[e] * a.scale;
       if (row == col + e) a.diag_a[diag + row] = t;
       v[e] = row == col + e ? 0.0f : t * a.store;
-      _Float16 p, q;
-      split_half(v[e], p, q);
-      h[e] = p;
-      l[e] = q;
-    }
-    *(h8*)(a.e + at) = h;
-    if (SPLIT) *(h8*)(a.e + a.e_low + at) = l;
-  } else if constexpr (K == kSquare) {
-    const h8 eh = *(const h8*)(a.e + at);
-    h8 el;
-    if (SPLIT) el = *(const h8*)(a.e + a.e_low + at);
-    h8 h, l;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float off = ((float)eh[e] + (SPLIT ? (float)el[e] : 0.0f)) * a.load;
+    } else if constexpr (K == kSquare) {
+      const float off = ((float)f.hi[e] + (SPLIT ? (float)f.lo[e] : 0.0f)) * a.load;
       const float sq = v[e] * a.scale;
-      const float d_col = a.diag_a[diag + col + e];
-      if (row == col + e) a.diag_p[diag + row] = fmaf(a.cc, fmaf(d_row, d_row, sq), a.cb * d_row);
-      const float t = fmaf(a.cc, sq, fmaf(a.cc, d_row + d_col, a.cb) * off);
+      if (row == col + e) a.diag_p[diag + row] = fmaf(a.cc, fmaf(f.d_row, f.d_row, sq), a.cb * f.d_row);
+      const float t = fmaf(a.cc, sq, fmaf(a.cc, f.d_row + d_col[e], a.cb) * off);
       v[e] = row == col + e ? 0.0f : t * a.store;
-      _Float16 p, q;
-      split_half(v[e], p, q);
-      h[e] = p;
-      l[e] = q;
+    } else {
+      const float x = ((float)f.hi[e] + (float)f.lo[e]) * a.load;
+      v[e] = fmaf(a.ca + f.d_row, x, v[e] * a.scale) * a.store;
     }
-    *(h8*)(a.p + at) = h;
-    if (SPLIT) *(h8*)(a.p + a.p_low + at) = l;
-  } else {
-    const h8 xh = *(const h8*)(a.xh + at), xl = *(const h8*)(a.xl + at);
-    h8 h, l;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = ((float)xh[e] + (float)xl[e]) * a.load;
-      v[e] = fmaf(a.ca + d_row, x, v[e] * a.scale) * a.store;
-      if (K == kUpdate) {
-        _Float16 p, q;
-        split_half(v[e], p, q);
-        h[e] = p;
-        l[e] = q;
-      }
-    }
-    if (K == kUpdate) {
-      *(h8*)(a.xh + at) = h;
-      *(h8*)(a.xl + at) = l;
-    }
+    _Float16 p, q;
+    split_half(v[e], p, q);
+    h[e] = p;
+    l[e] = q;
+  }
+  if constexpr (K == kUpdate) {
+    *(h8*)(a.x + at) = h;
+    *(h8*)(a.x + at + x_low) = l;
+  } else if constexpr (K != kLast) {
+    _Float16* to = (K == kGram ? a.e : a.p) + at;
+    *(h8*)to = h;
+    if (SPLIT) *(h8*)(to + kSplitCols) = l;
   }
 }
 
 // Eight consecutive results of the last step, to the caller's array.
 template <class TW, bool MUON>
-__device__ __forceinline__ void put_result(const ProductArgs& a, int64_t plane_o, int r, int c, const float (&v)[8]) {
+__device__ __forceinline__ void put_result(const ProductArgs& a, int64_t plane_o, int r, int c, const float (&v)[8],
+                                           Vec<TW, 8> old) {
   if (r >= a.rows || c >= a.cols) return;
   TW* p = (TW*)a.out + plane_o + (int64_t)r * a.cols + c;
   if (c + 8 <= a.cols) {
-    Vec<TW, 8> y;
-    if (MUON) y = load_vec<TW, 8>(p);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      y.v[e] = from_f32<TW>(MUON ? fmaf(a.keep, to_f32(y.v[e]), a.gain * v[e]) : v[e]);
-    store_vec<TW, 8>(p, y);
+      old.v[e] = from_f32<TW>(MUON ? fmaf(a.keep, to_f32(old.v[e]), a.gain * v[e]) : v[e]);
+    store_vec<TW, 8>(p, old);
   } else {
-    for (int e = 0; e < 8 && c + e < a.cols; ++e)
-      p[e] = from_f32<TW>(MUON ? fmaf(a.keep, to_f32(p[e]), a.gain * v[e]) : v[e]);
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (c + e < a.cols) p[e] = from_f32<TW>(MUON ? fmaf(a.keep, to_f32(p[e]), a.gain * v[e]) : v[e]);
   }
 }
 
-template <Product K, bool SPLIT, class TW, bool MUON, int BM, int BN, int WR, int WC>
-__global__ __launch_bounds__(WR* WC* kWave) void k_ns_product(ProductArgs a) {
-  constexpr int WAVES = WR * WC, WM = BM / WR, WN = BN / WC, MI = WM / 32, NI = WN / 32;
-  __shared__ __align__(16) _Float16 s_l0[BM * kBK], s_r0[BN * kBK], s_l1[BM * kBK], s_r1[BN * kBK];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+template <Product K, bool SPLIT, class TW, bool MUON, class G>
+__global__ __launch_bounds__(G::WAVES* kWave, G::B == 192 ? 1 : 2) void k_ns_product(ProductArgs a) {
+  constexpr int B = G::B, S = G::S, WAVES = G::WAVES, WC = G::WC, WM = G::WM, WN = G::WN, MI = G::MI, NI = G::NI;
   constexpr bool SYM = K == kGram || K == kSquare;
-  int tm, tn;
-  if (SYM) {  // the t-th tile of the lower triangle, row by row
-    const int t = blockIdx.x;
-    tm = (int)((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
-    while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
-    while (tm * (tm + 1) / 2 > t) --tm;
-    tn = t - tm * (tm + 1) / 2;
-  } else {
-    tm = blockIdx.x / a.tiles_n;
-    tn = blockIdx.x - tm * a.tiles_n;
+  static_assert(S == 2 || S == 4, "ring");
+  // one array a stage, so that reads of one are seen not to depend on loads to another
+  __shared__ __align__(16) _Float16 s_0[2 * B * kBK], s_1[2 * B * kBK], s_2[S > 2 ? 2 * B * kBK : 8],
+      s_3[S > 2 ? 2 * B * kBK : 8];
+  __shared__ int s_state;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+  // Workgroups go to the 8 XCDs in turn: each XCD takes a run of neighbouring tiles.
+  int id = blockIdx.x;
+  {
+    const int xcd = id % 8, q = gridDim.x / 8, rest = gridDim.x % 8;
+    id = xcd * q + min(xcd, rest) + id / 8;
   }
-  const int batch = blockIdx.y;
-  // this lane's part of each stage: 8 rows of 8 chunks a wave and load
-  u32 off_l[BM / (8 * WAVES)], off_r[BN / (8 * WAVES)];
-#pragma unroll
-  for (int i = 0; i < BM / (8 * WAVES); ++i) {
-    const int row = (i * WAVES + wave) * 8 + lane / 8;
-    off_l[i] = (u32)(row * a.ld + chunk_place(row, lane % 8) * 8);
-  }
-#pragma unroll
-  for (int i = 0; i < BN / (8 * WAVES); ++i) {
-    const int row = (i * WAVES + wave) * 8 + lane / 8;
-    off_r[i] = (u32)(row * a.ld + chunk_place(row, lane % 8) * 8);
-  }
-  const _Float16* gl = a.l + (int64_t)batch * a.l_batch + (int64_t)tm * BM * a.ld;
-  const _Float16* gr = a.r + (int64_t)batch * a.r_batch + (int64_t)tn * BN * a.ld;
-  const int kt = a.k / kBK, nt = SPLIT ? 3 * kt : kt;
-  // stage t of the sum: high x low, low x high, high x high where split
-  auto load = [&](int t, _Float16* sl, _Float16* sr) {
-    int64_t ol, orr;
-    if (SPLIT) {
-      const int seg = t >= 2 * kt ? 2 : t >= kt ? 1 : 0;
-      const int64_t k0 = (int64_t)(t - seg * kt) * kBK;
-      ol = k0 + (seg == 1 ? a.l_low : 0);
-      orr = k0 + (seg == 0 ? a.r_low : 0);
+  // Shared tiles: the stages of all tiles form one list and every workgroup takes
+  // an equal run of it.  The last workgroup to arrive at a tile that several
+  // share adds their sums, in the order of the stages, and goes on to the epilogue.
+  const int wg = id, nt = a.stages;
+  int unit = G::SHARE ? wg * a.share : 0;
+  const int unit_end = G::SHARE ? min(unit + a.share, a.units) : 1;
+  while (unit < unit_end) {
+    int first = 0, last = nt;  // stages of the tile
+    if (G::SHARE) {
+      id = unit / nt;
+      first = unit - id * nt;
+      last = min(nt, first + unit_end - unit);
+      unit += last - first;
     } else {
-      ol = orr = (int64_t)t * kBK;
+      unit = 1;
     }
-    load_stage<BM, WAVES>(gl + ol, off_l, sl, wave);
-    load_stage<BN, WAVES>(gr + orr, off_r, sr, wave);
-  };
-  const int l_row = (wave / WC) * WM, r_row = (wave % WC) * WN;
-  f16v acc[MI][NI];
+    const int tile = id, batch = id / a.tiles;
+    id -= batch * a.tiles;
+    int tm, tn;
+    if (SYM) {  // the id-th tile of the lower triangle, row by row
+      tm = (int)((sqrtf(8.0f * id + 1.0f) - 1.0f) * 0.5f);
+      while ((tm + 1) * (tm + 2) / 2 <= id) ++tm;
+      while (tm * (tm + 1) / 2 > id) --tm;
+      tn = id - tm * (tm + 1) / 2;
+    } else {  // groups of four tile rows, column by column
+      const int group = id / (4 * a.tiles_n), r0 = group * 4, rows = min(4, (a.mp + B - 1) / B - r0);
+      id -= group * 4 * a.tiles_n;
+      tn = id / rows;
+      tm = r0 + id - tn * rows;
+    }
+    // this lane's part of each stage, in bytes: 8 rows of 8 chunks a wave and load
+    constexpr int HALF = G::LOADS / 2;
+    u32 off_l[HALF], off_r[HALF];
+    const int cols_c = SYM ? a.mp : a.np;  // a tile may hang over: rows past the end are read as the last one
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi)
+    for (int i = 0; i < HALF; ++i) {
+      const int row = (i * WAVES + wave) * 8 + lane / 8;
+      off_l[i] = (u32)(min(row, a.mp - 1 - tm * B) * a.stride + chunk_place(row, lane % 8) * 8) * 2;
+      off_r[i] = (u32)(min(row, cols_c - 1 - tn * B) * a.stride + chunk_place(row, lane % 8) * 8) * 2;
+    }
+    const char* gl = (const char*)(a.l + batch * a.l_batch + (int64_t)tm * B * a.stride + (int64_t)first * kBK);
+    const char* gr = (const char*)(a.r + batch * a.r_batch + (int64_t)tn * B * a.stride + (int64_t)first * kBK);
+    const int count = last - first;
+    auto ring = [&](int i) -> _Float16* { return i == 0 ? s_0 : i == 1 ? s_1 : i == 2 ? s_2 : s_3; };
+    auto load = [&](int t, _Float16* to) {
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
+      for (int i = 0; i < HALF; ++i) load_to_lds(gl + (int64_t)t * (kBK * 2) + off_l[i], to + (i * WAVES + wave) * 8 * kBK);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) acc[mi][ni][q] = 0.0f;
-  load(0, s_l0, s_r0);
-  __syncthreads();
-  for (int t = 0; t < nt; t += 2) {
-    if (t + 1 < nt) load(t + 1, s_l1, s_r1);
-    multiply_stage<MI, NI>(s_l0, s_r0, l_row, r_row, acc);
-    __syncthreads();
-    if (t + 1 >= nt) break;
-    if (t + 2 < nt) load(t + 2, s_l0, s_r0);
-    multiply_stage<MI, NI>(s_l1, s_r1, l_row, r_row, acc);
-    __syncthreads();
-  }
-  // Epilogue: every wave turns its tile in its own part of LDS, 32 rows at a
-  // time: once out in row order (16 bytes a lane), once transposed.
-  constexpr int LD = WN + 2;
-  static_assert(32 * LD * 4 * (WAVES / 4) <= BM * kBK * 2 && BM == BN, "a wave's strip fits its part of a stage");
-  _Float16* part = wave * 4 / WAVES == 0 ? s_l0 : wave * 4 / WAVES == 1 ? s_r0 : wave * 4 / WAVES == 2 ? s_l1 : s_r1;
-  float* strip = (float*)part + (wave % (WAVES / 4)) * 32 * LD;
-  const int64_t diag = (int64_t)batch * a.mp;
-  const int64_t plane_c = (int64_t)batch * a.mp * (SYM ? a.mp : a.np);
-  const int64_t plane_o = (int64_t)batch * a.rows * a.cols;
-  const int row0 = tm * BM + l_row, col0 = tn * BN + r_row;
+      for (int i = 0; i < HALF; ++i)
+        load_to_lds(gr + (int64_t)t * (kBK * 2) + off_r[i], to + B * kBK + (i * WAVES + wave) * 8 * kBK);
+    };
+    // Operands of 16 summation indices: [high, low parts][blocks of 32 rows]
+    constexpr int PARTS = SPLIT ? 2 : 1, KK = SPLIT ? 2 : 4;
+    const int l_row = (wave / WC) * WM, r_row = (wave % WC) * WN;
+    const int i32 = lane & 31, hi = lane >> 5;
+    h8 x[2][PARTS][MI], y[2][PARTS][NI];
+    auto read = [&](const _Float16* from, int kk, int to) {
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi) {
+      for (int p = 0; p < PARTS; ++p) {
+        const int place = chunk_place(i32, p * 4 + kk * 2 + hi) * 8;  // l_row, r_row: multiples of 32
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
+        for (int mi = 0; mi < MI; ++mi) x[to][p][mi] = *(const h8*)(from + (l_row + mi * 32 + i32) * kBK + place);
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        strip[(8 * (q / 4) + 4 * (lane >> 5) + q % 4) * LD + ni * 32 + (lane & 31)] = acc[mi][ni][q];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    constexpr int VR = WN / 8;  // vectors a row
+        for (int ni = 0; ni < NI; ++ni) y[to][p][ni] = *(const h8*)(from + (B + r_row + ni * 32 + i32) * kBK + place);
+      }
+    };
+    f16v acc[MI][NI];
 #pragma unroll
-    for (int it = 0; it < 32 * VR / kWave; ++it) {
-      const int r = (it * kWave + lane) / VR, c = (it * kWave + lane) % VR * 8;
-      float* s = strip + r * LD + c;
-      float v[8];
+    for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = s[e];
-      const int row = row0 + mi * 32 + r;
-      const float d_row = K == kGram ? 0.0f : (K == kSquare ? a.diag_a : a.diag_p)[diag + row];
-      finish_row<K, SPLIT, TW, MUON>(a, plane_c, diag, row, col0 + c, v, d_row);
-      if (K == kLast && !a.tall) {
-        put_result<TW, MUON>(a, plane_o, row, col0 + c, v);
-      } else {
+      for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = v[e];
+        for (int q = 0; q < 16; ++q) acc[mi][ni][q] = 0.0f;
+    auto multiply = [&](int from) {
+#pragma unroll
+      for (int q = SPLIT ? 0 : 2; q < 3; ++q)  // high low, low high, high high
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni)
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[from][q == 1 ? PARTS - 1 : 0][mi],
+                                                                 y[from][q == 0 ? PARTS - 1 : 0][ni], acc[mi][ni], 0, 0, 0);
+    };
+    // One stage: S - 1 stages are in flight while it is multiplied; the operands
+    // of the next 16 indices are read while these are multiplied, over the
+    // barrier too.
+    auto step = [&](auto at, int t) {
+      constexpr int b = decltype(at)::value;
+      if (t + S - 1 < count) load(t + S - 1, ring((b + S - 1) % S));
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        if (kk + 1 < KK) {
+          read(ring(b), kk + 1, (kk + 1) & 1);
+        } else {  // behind the last stage this reads what nothing uses
+          stage_barrier<G::LOADS>(min(S - 2, count - t - 2));
+          read(ring((b + 1) % S), 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // the reads stay ahead of the products
+        multiply(kk & 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+      if (i < count) load(i, ring(i));
+    stage_barrier<G::LOADS>(min(S - 2, count - 1));
+    read(ring(0), 0, 0);
+    for (int t = 0; t < count; t += S) {
+      step(std::integral_constant<int, 0>{}, t);
+      if (B > 64 || t + 1 < count) step(std::integral_constant<int, 1>{}, t + 1);  // B > 64: count is even
+      if constexpr (S > 2) {
+        if (t + 2 < count) step(std::integral_constant<int, 2>{}, t + 2);
+        if (t + 3 < count) step(std::integral_constant<int, 3>{}, t + 3);
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const bool turned = SYM ? tm != tn : K == kLast ? a.tall != 0 : true;
-    if (turned) {
+    if (G::SHARE && count < nt) {
+      // Sums pass between workgroups at device scope (stores written through,
+      // loads that miss what a nearer cache holds), ordered by the counter.
+      constexpr int PAIRS = MI * NI * 8;
+      const int w0 = tile * nt / a.share, n = (tile * nt + nt - 1) / a.share - w0 + 1;
+      u32* arrived = a.arrived + tile;
+      auto slot = [&](int w) {  // a workgroup's only tile that it does not begin is its first one
+        const int64_t at = ((int64_t)w * 2 + (w == w0 ? 1 : 0)) * (B * B / 2);
+        return (u64*)a.sums + at + threadIdx.x;
+      };
+      auto pair = [&](int i) -> u64 {
+        const f16v& q = acc[i / 8 / NI][i / 8 % NI];
+        return (u64)__float_as_uint(q[i % 8 * 2 + 1]) << 32 | __float_as_uint(q[i % 8 * 2]);
+      };
+      if (threadIdx.x == 0)
+        s_state = __hip_atomic_load(arrived, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (u32)(n - 1);
+      __syncthreads();
+      if (!s_state) {
+        u64* to = slot(wg);
 #pragma unroll
-      for (int it = 0; it < 32 * VR / kWave; ++it) {
-        const int c = (it * kWave + lane) / 4, r = (it * kWave + lane) % 4 * 8;
+        for (int i = 0; i < PAIRS; ++i)
+          __hip_atomic_store(to + i * (WAVES * kWave), pair(i), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0)
+          s_state = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (u32)(n - 1);
+        __syncthreads();
+        if (!s_state) continue;
+      }
+      if (threadIdx.x == 0) __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      // s = sum over w0, w0 + 1, ...; this workgroup's own part from registers
+      constexpr int BATCH = 8;
+#pragma unroll
+      for (int i0 = 0; i0 < PAIRS; i0 += BATCH) {
+        u64 own[BATCH];
+        float lo[BATCH], up[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          own[i] = pair(i0 + i);
+          lo[i] = up[i] = 0.0f;
+        }
+        for (int w = w0; w < w0 + n; ++w) {
+          const u64* from = slot(w) + i0 * (WAVES * kWave);
+          u64 in[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i)
+            in[i] = w == wg ? own[i]
+                            : __hip_atomic_load(from + i * (WAVES * kWave), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            lo[i] += __uint_as_float((u32)in[i]);
+            up[i] += __uint_as_float((u32)(in[i] >> 32));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          f16v& q = acc[(i0 + i) / 8 / NI][(i0 + i) / 8 % NI];
+          q[(i0 + i) % 8 * 2] = lo[i];
+          q[(i0 + i) % 8 * 2 + 1] = up[i];
+        }
+      }
+    }
+    // Epilogue: every wave turns its tile in its own part of LDS, 32 rows at a
+    // time: once out in row order (16 bytes a lane), once transposed.  What it
+    // reads is fetched for 32 rows at once, where registers allow while the rows
+    // before are worked on.
+    constexpr int VR = WN / 8, ITS = 32 * VR / kWave, LD = WN + 2;  // vectors a row; of them a lane
+    constexpr int AHEAD = MI <= 2 ? 1 : 0;
+    static_assert(WAVES / 2 * 32 * LD * 4 <= 2 * B * kBK * 2, "a wave's strip fits its part of a stage");
+    float* strip = (float*)(wave < WAVES / 2 ? s_0 : s_1) + wave % (WAVES / 2) * 32 * LD;
+    const int64_t diag = (int64_t)batch * a.mp;
+    const int64_t plane_c = (int64_t)batch * a.mp * (SYM ? a.mp : a.np) * PARTS;
+    const int64_t plane_o = (int64_t)batch * a.rows * a.cols;
+    const int row0 = tm * B + l_row, col0 = tn * B + r_row;
+    auto strip_row = [&](int it) { return (it * kWave + lane) / VR; };
+    auto strip_col = [&](int it) { return (it * kWave + lane) % VR * 8; };
+    auto at_of = [&](int row, int col) { return plane_c + place_of<SPLIT>(row, col, SYM ? a.mp : a.np); };
+    Fetched<TW> f[AHEAD + 1][ITS];
+    auto fetch = [&](int mi, Fetched<TW>(&to)[ITS]) {
+#pragma unroll
+      for (int it = 0; it < ITS; ++it) {
+        const int row = row0 + mi * 32 + strip_row(it), col = col0 + strip_col(it);
+        if (row >= a.mp || col >= cols_c) continue;
+        if constexpr (K != kGram) {
+          const _Float16* from = (K == kSquare ? a.e : a.x) + at_of(row, col);
+          to[it].hi = *(const h8*)from;
+          if (SPLIT) to[it].lo = *(const h8*)(from + kSplitCols);
+          else if (K != kSquare) to[it].lo = *(const h8*)(from + a.x_low);
+          to[it].d_row = (K == kSquare ? a.diag_a : a.diag_p)[diag + row];
+        }
+        if constexpr (K == kLast && MUON) {
+          const int r = a.tall ? col0 + (it * kWave + lane) / 4 : row;
+          const int c = a.tall ? row0 + mi * 32 + lane % 4 * 8 : col;
+          if (r < a.rows && c + 8 <= a.cols) to[it].old = load_vec<TW, 8>((const TW*)a.out + plane_o + (int64_t)r * a.cols + c);
+        }
+      }
+    };
+    // one column for every it where VR divides the wave
+    constexpr int COLS = kWave % VR == 0 ? 1 : ITS;
+    float d_col[COLS][8];
+    if constexpr (K == kSquare) {
+#pragma unroll
+      for (int it = 0; it < COLS; ++it)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d_col[it][e] = a.diag_a[diag + min(col0 + strip_col(it) + e, a.mp - 1)];
+    }
+    fetch(0, f[0]);
+    __syncthreads();
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      if (AHEAD ? mi + 1 < MI : mi > 0) fetch(mi + AHEAD, f[(mi + AHEAD) & AHEAD]);
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          strip[(8 * (q / 4) + 4 * (lane >> 5) + q % 4) * LD + ni * 32 + (lane & 31)] = acc[mi][ni][q];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int it = 0; it < ITS; ++it) {
+        const int r = strip_row(it), c = strip_col(it);
+        float* s = strip + r * LD + c;
         float v[8];
-        h8 h, l;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] = strip[(r + e) * LD + c];
-          _Float16 p, q;
-          split_half(v[e], p, q);
-          h[e] = p;
-          l[e] = q;
-        }
+        for (int e = 0; e < 8; ++e) v[e] = s[e];
         const int row = row0 + mi * 32 + r, col = col0 + c;
-        if constexpr (K == kLast) {
-          put_result<TW, MUON>(a, plane_o, col, row, v);
+        if (row >= a.mp || col >= cols_c) continue;
+        finish_row<K, SPLIT, TW>(a, at_of(row, col), diag, row, col, v, f[mi & AHEAD][it], d_col[it % COLS]);
+        if (K == kLast && !a.tall) {
+          put_result<TW, MUON>(a, plane_o, row, col, v, f[mi & AHEAD][it].old);
         } else {
-          const int64_t at = plane_c + (int64_t)col * a.mp + row;
-          _Float16* to = K == kGram ? a.e : K == kSquare ? a.p : a.th;
-          *(h8*)(to + at) = h;
-          if (SPLIT) *(h8*)((K == kGram ? a.e + a.e_low : K == kSquare ? a.p + a.p_low : a.tl) + at) = l;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] = v[e];
         }
       }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const bool turned = SYM ? tm != tn : K == kLast ? a.tall != 0 : true;
+      if (turned) {
+#pragma unroll
+        for (int it = 0; it < ITS; ++it) {
+          const int c = (it * kWave + lane) / 4, r = lane % 4 * 8;
+          float v[8];
+          h8 h, l;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = strip[(r + e) * LD + c];
+            _Float16 p, q;
+            split_half(v[e], p, q);
+            h[e] = p;
+            l[e] = q;
+          }
+          const int row = row0 + mi * 32 + r, col = col0 + c;
+          if (row >= a.mp || col >= cols_c) continue;
+          if constexpr (K == kLast) {
+            put_result<TW, MUON>(a, plane_o, col, row, v, f[mi & AHEAD][it].old);
+          } else {
+            _Float16* to = (K == kGram ? a.e : K == kSquare ? a.p : a.t) + plane_c + place_of<SPLIT>(col, row, a.mp);
+            *(h8*)to = h;
+            if (SPLIT) *(h8*)(to + kSplitCols) = l;
+          }
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }    if (G::SHARE) __syncthreads();  // the next tile's stages overwrite the strips
   }
 }
 
@@ -516,11 +680,73 @@ static bool step_scales(int steps, double a, double b, double c, StepScales* s) 
 }
 
 struct NsPlan {
-  int m, n, mp, np, tall, tile, blocks;
+  int m, n, mp, np, tall, blocks;
+  int shape[3];  // of the gram, the square and the update
+  int share[2];  // stages of a workgroup in the gram and the square, where tiles are shared
+  int arrive;    // counters to clear
   bool split, small;
-  size_t part, diag_a, diag_p, x, t[2], e, p, total;  // byte offsets
-  int64_t x_low, t_low, e_low, p_low;                 // elements between high and low parts
+  size_t part, diag_a, diag_p, x, t[2], e, p, sums, arrived, total;  // byte offsets
+  int64_t x_low;  // elements between X's high and low parts (not split)
 };
+
+typedef Shape<64, 2, 2, 4> Tile64;
+typedef Shape<64, 2, 2, 4, true> Tile64Shared;
+typedef Shape<128, 2, 2, 2> Tile128;
+typedef Shape<128, 2, 2, 4> Tile128Deep;
+typedef Shape<192, 2, 2, 2> Tile192;
+typedef Shape<256, 2, 4, 2> Tile256;
+enum { k64, k128, k128Deep, k192, k256, k64Shared, kShapes };
+constexpr int kTile[kShapes] = {64, 128, 128, 192, 256, 64};
+
+// The shape of a product is the one with the least time by this model, fitted
+// to products of 128 to 8,192 a side: `fixed` us for the first stages' way and
+// the epilogue, and a time a stage, lower where every workgroup has a compute
+// unit of its own.  With more tiles than fit at once the last round costs about
+// a third of a round more than its share.
+struct ShapeTime {
+  int slots;          // workgroups that fit at once
+  float fixed, full, alone;  // us, and us a stage: all slots taken, one workgroup a compute unit
+  float full_split, alone_split;
+};
+constexpr ShapeTime kTime[kShapes] = {
+    {512, 4.5f, 0.55f, 0.21f, 0.65f, 0.27f},   {512, 8.0f, 1.05f, 0.75f, 1.3f, 0.95f},
+    {256, 8.0f, 0.55f, 0.55f, 0.85f, 0.85f},   {256, 11.0f, 1.05f, 1.05f, 1.45f, 1.45f},
+    {256, 14.0f, 1.75f, 1.75f, 2.8f, 2.8f},    {512, 12.5f, 0.3f, 0.25f, 0.4f, 0.3f},
+};
+
+static int64_t tiles_of(const NsPlan& p, int64_t batch, int shape, bool symmetric) {
+  const int64_t tm = (p.mp + kTile[shape] - 1) / kTile[shape], tn = (p.np + kTile[shape] - 1) / kTile[shape];
+  return batch * (symmetric ? tm * (tm + 1) / 2 : tm * tn);
+}
+
+// Stages a workgroup takes where tiles are shared: at most four workgroups a
+// tile, and eight stages at least.
+static int64_t pick_share(int64_t tiles, int64_t nt) {
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(512, std::min(tiles * 4, tiles * nt / 8)));
+  return ((tiles * nt + most - 1) / most + 1) / 2 * 2;
+}
+
+static int pick_shape(const NsPlan& p, int64_t batch, int64_t k, bool symmetric) {
+  const int64_t nt = k * (p.split ? 2 : 1) / kBK;
+  int best = k64;
+  double least = 1e30;
+  for (int i = 0; i < kShapes; ++i) {
+    if (i == k64Shared && !symmetric) continue;
+    const ShapeTime& t = kTime[i];
+    int64_t work = tiles_of(p, batch, i, symmetric), stages = nt;
+    if (i == k64Shared) {
+      stages = pick_share(work, nt);
+      if (stages >= nt) continue;
+      work = (work * nt + stages - 1) / stages;
+    }
+    const double full = p.split ? t.full_split : t.full, alone = p.split ? t.alone_split : t.alone;
+    const double us = t.fixed + stages * (work <= 256        ? alone
+                                          : work <= t.slots ? full
+                                                            : full * ((double)work / t.slots + 0.35));
+    if (us < least) least = us, best = i;
+  }
+  return best;
+}
 
 static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPlan* p) {
   if (batch < 1 || batch > 65535 || rows < 1 || cols < 1 || rows > 65536 || cols > 65536) return false;
@@ -533,15 +759,16 @@ static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPla
     p->total = small_workspace_bytes(batch, rows, cols);
     return true;
   }
-  p->tile = p->m > 512 ? 128 : 64;
   auto up = [](int64_t v, int64_t to) { return (v + to - 1) / to * to; };
-  p->mp = (int)up(p->m, p->tile);
-  p->np = (int)up(p->n, p->tile);
-  p->blocks = (int)std::min<int64_t>(kNormBlocks, up(rows * cols, 4096) / 4096);
+  // tiles may hang over, but shapes above 64 take stages in pairs
+  p->mp = (int)up(p->m, 128);
+  p->np = (int)up(p->n, 128);
+  p->shape[0] = pick_shape(*p, batch, p->np, true);
+  p->shape[1] = pick_shape(*p, batch, p->mp, true);
+  p->shape[2] = pick_shape(*p, batch, p->mp, false);
+  p->blocks = norm_blocks(batch, rows * cols);
   const int64_t xs = batch * p->mp * p->np, as = batch * p->mp * p->mp;
   p->x_low = xs;
-  p->t_low = xs;
-  p->e_low = p->p_low = as;
   size_t at = kWorkspaceHeader;
   auto take = [&](int64_t bytes) {
     const size_t here = at;
@@ -555,36 +782,65 @@ static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPla
   for (size_t& t : p->t) t = take(xs * (split ? 4 : 2));
   p->e = take(as * (split ? 4 : 2));
   p->p = take(as * (split ? 4 : 2));
+  int64_t runs = 0;
+  p->arrive = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (p->shape[i] != k64Shared) continue;
+    const int64_t tiles = tiles_of(*p, batch, k64Shared, true), nt = (int64_t)(i ? p->mp : p->np) * (split ? 2 : 1) / kBK;
+    p->share[i] = (int)pick_share(tiles, nt);
+    p->arrive = (int)tiles;
+    runs = std::max(runs, (tiles * nt + p->share[i] - 1) / p->share[i]);
+  }
+  p->sums = take(runs * 2 * 64 * 64 * 4);
+  p->arrived = take((int64_t)p->arrive * 4);
   p->total = at;
   return true;
 }
 
+template <Product K, bool SPLIT, class TW, bool MUON, class G>
+static void launch_tiles(const NsPlan& p, ProductArgs a, int64_t batch, hipStream_t stream) {
+  const int tm = (p.mp + G::B - 1) / G::B;
+  a.tiles_n = (p.np + G::B - 1) / G::B;
+  a.tiles = K == kGram || K == kSquare ? tm * (tm + 1) / 2 : tm * a.tiles_n;
+  int64_t blocks = a.tiles * batch;
+  if (G::SHARE) {
+    a.units = (int)(blocks * a.stages);
+    a.share = p.share[K == kSquare];
+    blocks = (a.units + a.share - 1) / a.share;
+  }
+  hipLaunchKernelGGL((k_ns_product<K, SPLIT, TW, MUON, G>), dim3((unsigned)blocks), dim3(G::WAVES * kWave), 0,
+                     stream, a);
+}
+
 template <Product K, bool SPLIT, class TW, bool MUON>
-static void launch_product(const NsPlan& p, const ProductArgs& a, int batch, hipStream_t stream) {
-  const bool sym = K == kGram || K == kSquare;
-  const int tm = p.mp / p.tile, tn = p.np / p.tile;
-  const dim3 grid(sym ? tm * (tm + 1) / 2 : tm * tn, batch);
-  if (p.tile == 128)
-    hipLaunchKernelGGL((k_ns_product<K, SPLIT, TW, MUON, 128, 128, 2, 2>), grid, dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL((k_ns_product<K, SPLIT, TW, MUON, 64, 64, 2, 2>), grid, dim3(256), 0, stream, a);
+static void launch_product(const NsPlan& p, const ProductArgs& a, int64_t batch, hipStream_t stream) {
+  constexpr bool SYM = K == kGram || K == kSquare;
+  switch (p.shape[K == kGram ? 0 : K == kSquare ? 1 : 2]) {
+    case k128: return launch_tiles<K, SPLIT, TW, MUON, Tile128>(p, a, batch, stream);
+    case k128Deep: return launch_tiles<K, SPLIT, TW, MUON, Tile128Deep>(p, a, batch, stream);
+    case k192: return launch_tiles<K, SPLIT, TW, MUON, Tile192>(p, a, batch, stream);
+    case k256: return launch_tiles<K, SPLIT, TW, MUON, Tile256>(p, a, batch, stream);
+    case k64Shared:
+      if constexpr (SYM) launch_tiles<K, SPLIT, TW, MUON, Tile64Shared>(p, a, batch, stream);
+      return;
+    default: return launch_tiles<K, SPLIT, TW, MUON, Tile64>(p, a, batch, stream);
+  }
 }
 
 template <bool SPLIT, class TW, bool MUON>
 static void run_steps(const NsCall& q, const NsPlan& p, const StepScales& s, char* ws, hipStream_t stream) {
-  const int batch = (int)q.batch;
+  constexpr int PARTS = SPLIT ? 2 : 1;
   ProductArgs a{};
   a.mp = p.mp;
   a.np = p.np;
-  a.tiles_n = p.np / p.tile;
   a.diag_a = (float*)(ws + p.diag_a);
   a.diag_p = (float*)(ws + p.diag_p);
   a.e = (_Float16*)(ws + p.e);
   a.p = (_Float16*)(ws + p.p);
-  a.e_low = p.e_low;
-  a.p_low = p.p_low;
-  a.xh = (_Float16*)(ws + p.x);
-  a.xl = a.xh + p.x_low;
+  a.x = (_Float16*)(ws + p.x);
+  a.x_low = p.x_low;
+  a.sums = (float*)(ws + p.sums);
+  a.arrived = (u32*)(ws + p.arrived);
   a.ca = (float)q.a;
   a.cb = (float)q.b;
   a.cc = (float)q.c;
@@ -594,40 +850,39 @@ static void run_steps(const NsCall& q, const NsPlan& p, const StepScales& s, cha
   a.tall = p.tall;
   a.keep = q.keep;
   a.gain = q.gain;
+  const int64_t x_size = (int64_t)p.mp * p.np * PARTS, a_size = (int64_t)p.mp * p.mp * PARTS;
   for (int t = 0; t < q.steps; ++t) {
     const float sx = s.x[t], sa = s.a[t], sp = s.p[t];
     ProductArgs g = a;
-    g.l = g.r = a.xh;
-    g.l_low = g.r_low = p.x_low;
-    g.l_batch = g.r_batch = (int64_t)p.mp * p.np;
-    g.ld = g.k = p.np;
+    g.l = g.r = a.x;
+    g.l_batch = g.r_batch = x_size;
+    g.stride = p.np * PARTS;
+    g.stages = g.stride / kBK;
     g.scale = 1.0f / (sx * sx);
     g.store = sa;
-    launch_product<kGram, SPLIT, float, false>(p, g, batch, stream);
+    launch_product<kGram, SPLIT, float, false>(p, g, q.batch, stream);
     g = a;
     g.l = g.r = a.e;
-    g.l_low = g.r_low = p.e_low;
-    g.l_batch = g.r_batch = (int64_t)p.mp * p.mp;
-    g.ld = g.k = p.mp;
+    g.l_batch = g.r_batch = a_size;
+    g.stride = p.mp * PARTS;
+    g.stages = g.stride / kBK;
     g.scale = 1.0f / (sa * sa);
     g.load = 1.0f / sa;
     g.store = sp;
-    launch_product<kSquare, SPLIT, float, false>(p, g, batch, stream);
+    launch_product<kSquare, SPLIT, float, false>(p, g, q.batch, stream);
     g = a;
     g.l = a.p;
-    g.l_low = p.p_low;
-    g.l_batch = (int64_t)p.mp * p.mp;
+    g.l_batch = a_size;
     g.r = (const _Float16*)(ws + p.t[t & 1]);
-    g.r_low = p.t_low;
-    g.r_batch = (int64_t)p.mp * p.np;
-    g.th = (_Float16*)(ws + p.t[(t & 1) ^ 1]);
-    g.tl = g.th + p.t_low;
-    g.ld = g.k = p.mp;
+    g.r_batch = x_size;
+    g.t = (_Float16*)(ws + p.t[(t & 1) ^ 1]);
+    g.stride = p.mp * PARTS;
+    g.stages = g.stride / kBK;
     g.scale = 1.0f / (sp * sx);
     g.load = 1.0f / sx;
     g.store = s.x[t + 1];
-    if (t + 1 < q.steps) launch_product<kUpdate, SPLIT, float, false>(p, g, batch, stream);
-    else launch_product<kLast, SPLIT, TW, MUON>(p, g, batch, stream);
+    if (t + 1 < q.steps) launch_product<kUpdate, SPLIT, float, false>(p, g, q.batch, stream);
+    else launch_product<kLast, SPLIT, TW, MUON>(p, g, q.batch, stream);
   }
 }
 
@@ -644,10 +899,12 @@ static tgs_status ns_run(const NsCall& q, const NsPlan& p, const StepScales& s, 
   k.x = q.x;
   k.momentum = q.momentum;
   k.part = (const double*)(ws + p.part);
-  k.xh = (_Float16*)(ws + p.x);
-  k.xl = k.xh + p.x_low;
-  k.th = (_Float16*)(ws + p.t[0]);
-  k.tl = p.split ? k.th + p.t_low : nullptr;
+  k.x_out = (_Float16*)(ws + p.x);
+  k.t_out = (_Float16*)(ws + p.t[0]);
+  k.x_low = p.x_low;
+  k.split = p.split;
+  k.arrived = (u32*)(ws + p.arrived);
+  k.arrive = p.arrive;
   k.count = q.rows * q.cols;
   k.rows = (int)q.rows;
   k.cols = (int)q.cols;

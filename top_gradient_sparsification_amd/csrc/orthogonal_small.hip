@@ -476,7 +476,7 @@ static SmallPlan small_plan(int64_t batch, int64_t rows, int64_t cols) {
   else
     while (p.cb < most && chunks(p.cb) * batch > 256) p.cb *= 2;
   p.chunks = (int)chunks(p.cb);
-  p.blocks = (int)std::min<int64_t>(kNormBlocks, (rows * cols + 4095) / 4096);
+  p.blocks = norm_blocks(batch, rows * cols);
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   size_t at = kWorkspaceHeader;
   p.part = at;

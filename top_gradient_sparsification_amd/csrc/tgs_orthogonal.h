@@ -2,6 +2,8 @@
 // a call, the scales of its steps, and the small route's entry.
 #pragma once
 
+#include <algorithm>
+
 #include "tgs_host.h"
 #include "tgs_types.h"
 
@@ -10,7 +12,6 @@ namespace tgs {
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxSteps = 64;
-constexpr int kNormBlocks = 128;  // partial sums of squares a matrix
 
 // Powers of two that X (before each step, 1 after the last), A and P are held at.
 struct StepScales {
@@ -42,6 +43,13 @@ __device__ __forceinline__ void split_half(float v, _Float16& h, _Float16& l) {
 __device__ __forceinline__ float new_momentum(float beta, float m, float g) { return fmaf(beta, m, g); }
 __device__ __forceinline__ float muon_u(int nesterov, float beta, float g, float m) {
   return nesterov ? fmaf(beta, m, g) : m;
+}
+
+// Partial sums of squares a matrix: 4,096 entries each, at most 1,024 and about
+// 2,048 for all matrices of a stack.
+inline int norm_blocks(int64_t batch, int64_t count) {
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(1024, 2048 / batch));
+  return (int)std::min(most, (count + 4095) / 4096);
 }
 
 // Sums of squares of what is orthogonalised (and the momentum's update): one
