@@ -304,9 +304,9 @@ tgs_status tgs_embedding_grad(const void* tokens, tgs_dtype tokens_dtype, int64_
                               int32_t accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace tgs_newton_schulz needs (0 if the sizes or the type are
-   invalid): 8 bytes an entry of x (padded to 128 a side) and 4 of the smaller
-   square with 16-bit types, twice that with fp32, and up to 17 MB for sums
-   that workgroups share. */
+   invalid): 10 bytes an entry of x (padded to 128 a side, 4 of them to the
+   update's tiles of up to 256) and 4 of the smaller square with 16-bit types,
+   16 and 8 with fp32, and up to 8 MB for sums that workgroups share. */
 size_t tgs_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, tgs_dtype dtype);
 
 /*

@@ -13,23 +13,24 @@
 //   update   P X = P (X^T)^T    operands P, X^T
 // X is kept in both orders; the update's epilogue writes both.
 //
-// A workgroup makes a tile of C: stages of 128 bytes a row of both operands go
-// from memory to a ring in LDS (asynchronous loads, one to three stages ahead),
-// the operands of the next 16 summation indices are read while these are
-// multiplied.  Square tiles of 64 to 256 a side, picked by a model of the time
-// (pick_shape).  256 tiles of 256 (4,096 square, update) take 141 us, as a library's
-// 4,096 product does (114 us without the epilogue); the symmetric products of
-// that size take 253 tiles of 192 rather than 136 of 256, which leave half the
-// device idle (four products of 4,096: 1,653 against 1,843 us for the whole
-// call).  Small matrices with a long side have few tiles with long sums, so
-// workgroups share them (gram of 200 x 8,000: 31 -> 12 us).
+// A workgroup makes a tile of C: stages of 128 or 256 bytes a row of both
+// operands go from memory to a ring in LDS by asynchronous loads, one to three
+// stages ahead, and the operands of the next 16 summation indices are read from
+// it while these are multiplied.  Tiles are 64 to 256 a side, whichever a model
+// of the time finds best (pick_shape): large ones read less from L2 and feed the
+// matrix cores better, small ones fill the device.  At 4,096 square the update
+// takes 256 tiles of 256 in 142 us (a library's product of that size takes 114),
+// at a clock that the power limit holds near 1.7 GHz; the symmetric products
+// take 253 tiles of 192 in 85 us rather than 136 of 256, which leave half the
+// device idle, in 120.  Few tiles with long sums are shared by workgroups (the
+// gram of 200 x 8,000 in fp32: 59 -> 28 us).
 //
 // What is rounded.  The diagonals of A and P are large against the rest near
 // the end (A tends to the identity), so they are held apart in fp32 and the
 // products see only the off-diagonal part E of A and of P:
 //   A = D + E:   A^2 = D^2 + (d_i + d_j) E + E^2,   P X = D_P X + E_P X.
-// X itself is held as fp16 high + low part (22 bits) and a + D_P multiplies
-// both.  With results of 16 bits the products read the high parts only: the
+// X itself is held in fp32, in the order of the update's registers, and a + D_P
+// multiplies that; the operands are fp16.  With results of 16 bits the products read the high parts only: the
 // result is then 2e-4 to 7e-4 (2-norm) off, below the 1.7e-3 of the final
 // rounding, where rounding X, A and P whole gives 1.6e-3 to 3e-3 (fp16) and
 // 1.3e-2 to 2.4e-2 (bf16).  With fp32 results every operand is high + low and
@@ -46,14 +47,16 @@
 
 namespace tgs {
 
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
-constexpr int kBK = 64;         // elements of a row a stage: rows of 128 bytes in LDS
 constexpr int kSplitCols = 32;  // columns of high parts, then as many of low parts, in a split row
 
 // Where a matrix of rows of ld elements holds (row, col).  Split matrices
-// interleave: 32 columns' high parts, then their low parts, so that a stage of
-// 128 bytes a row holds both.
+// interleave: 32 columns' high parts, then their low parts, so that a stage
+// holds both.
 template <bool SPLIT>
 __device__ __forceinline__ int64_t place_of(int row, int col, int ld) {
   return SPLIT ? (int64_t)row * 2 * ld + (col / kSplitCols) * 2 * kSplitCols + col % kSplitCols : (int64_t)row * ld + col;
@@ -73,9 +76,10 @@ struct PackArgs {
   const void* x;
   const float* momentum;
   const double* part;
-  _Float16* x_out;   // X, then low parts x_low behind
-  _Float16* t_out;   // the transpose; with split, low parts as X
-  int64_t x_low;
+  _Float16* x_out;   // X and its transpose, operands of the products
+  _Float16* t_out;
+  float* xf;         // X in fp32, in the order of the update's registers
+  int tile, tile_rows, tile_cols;  // of the update: a workgroup's, a wave's rows and columns
   int64_t count;     // rows * cols
   int rows, cols, mp, np, blocks;
   int split;
@@ -194,7 +198,6 @@ __global__ __launch_bounds__(256) void k_ns_pack(PackArgs a) {
                    (a.split ? place_of<true>(row, col, stride) : place_of<false>(row, col, stride));
     *(h8*)to = h;
     if (a.split) *(h8*)(to + kSplitCols) = l;
-    else if (is_x) *(h8*)(to + a.x_low) = l;
   };
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -213,17 +216,37 @@ __global__ __launch_bounds__(256) void k_ns_pack(PackArgs a) {
     put(r0 + i, c0 + vec * 8, ld, !a.tall, h, l);
     put(c0 + i, r0 + vec * 8, ldt, a.tall, hx, lx);
   }
+  // a wave writes one block of 32 x 32 of X as the update's wave will hold it
+  const int bi = threadIdx.x / 128 * 32, bj = threadIdx.x / 64 % 2 * 32;
+  const int row = (a.tall ? c0 : r0) + bi, col = (a.tall ? r0 : c0) + bj;
+  const int wr = a.tile / a.tile_rows, wc = a.tile / a.tile_cols;
+  const int tiles_m = (a.mp + a.tile - 1) / a.tile, tiles_n = (a.np + a.tile - 1) / a.tile;
+  const int wave = row % a.tile / a.tile_rows * wc + col % a.tile / a.tile_cols;
+  const int block = row % a.tile_rows / 32 * (a.tile_cols / 32) + col % a.tile_cols / 32;
+  const int64_t tile = ((int64_t)blockIdx.z * tiles_m + row / a.tile) * tiles_n + col / a.tile;
+  f4* to = (f4*)a.xf + ((tile * (wr * wc) + wave) * (a.tile_rows * a.tile_cols / 1024) + block) * 256 + tx;
+  const int h = tx >> 5, c32 = tx & 31;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    f4 v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = bi + 8 * g + 4 * h + r, j = bj + c32;
+      v[r] = a.tall ? s_t[j][i] : s_t[i][j];
+    }
+    to[g * kWave] = v;
+  }
 }
 
 // --------------------------------------------------------------- products --
 enum Product { kGram, kSquare, kUpdate, kLast };
 
 struct ProductArgs {
-  // operands of C = L R^T: rows `stride` elements apart, `stages` stages of 64 elements
+  // operands of C = L R^T: rows `stride` elements apart
   const _Float16* l;
   const _Float16* r;
   int64_t l_batch, r_batch;  // elements between matrices of a batch
-  int stride, stages;
+  int stride, stages;  // stages: of BK elements
   int mp, np;      // C is [mp][mp] (gram, square) or [mp][np]
   int tiles, tiles_n;  // tiles a matrix; of them in a row (update)
   int units, share;  // gram, square: stages of all tiles, and of them a workgroup's
@@ -235,9 +258,9 @@ struct ProductArgs {
   float* diag_p;   // [batch][mp] diagonal of P
   _Float16* e;     // gram: out, square: in; off-diagonal part of A
   _Float16* p;     // square: out
-  _Float16* x;     // update: X in and out
+  _Float16* x;     // update: X out
   _Float16* t;     // update: transpose out
-  int64_t x_low;   // X's low parts behind its high ones (not split)
+  float* xf;       // update: X in fp32, in and out, in the order of the registers
   float store;     // scale of what is stored
   float load;      // 1 / scale of X or E as read
   float ca, cb, cc;
@@ -250,18 +273,20 @@ struct ProductArgs {
 // A workgroup's share of a product: a B x B tile, WR x WC waves, a ring of S
 // stages in LDS.  SHARE: workgroups take equal runs of the list of all tiles'
 // stages (symmetric products).
-template <int B_, int WR_, int WC_, int S_, bool SHARE_ = false>
+template <int B_, int WR_, int WC_, int BK_, int S_, bool SHARE_ = false>
 struct Shape {
+  static constexpr int BK = BK_, CHUNKS = BK_ / 8, ROWS = 64 / CHUNKS;  // elements and chunks of a row a stage, rows a load
   static constexpr bool SHARE = SHARE_;
+  static constexpr int EU = 4 * B_ * BK_ * S_ > 80 * 1024 && WR_ * WC_ == 4 ? 1 : 2;  // waves a SIMD that LDS allows
   static constexpr int B = B_, WR = WR_, WC = WC_, S = S_, WAVES = WR_ * WC_;
   static constexpr int WM = B_ / WR_, WN = B_ / WC_, MI = WM / 32, NI = WN / 32;
-  static constexpr int LOADS = 2 * B_ / (8 * WAVES);  // 16-byte loads a lane and stage
+  static constexpr int LOADS = 2 * B_ / (ROWS * WAVES);  // 16-byte loads a lane and stage
 };
 
-// Stage layout: row r of a 64-element stage is 8 chunks of 16 bytes, chunk c at
-// place c ^ ((r >> 1) & 7): 16 lanes that read one chunk of 16 rows then cover
-// all 64 banks.
-__device__ __forceinline__ int chunk_place(int r, int c) { return c ^ ((r >> 1) & 7); }
+// Stage layout: a row is C chunks of 16 bytes, 8 or 16, turned by the row so that
+// 16 lanes that read one chunk of 16 rows cover all 64 banks.
+template <int C>
+__device__ __forceinline__ int chunk_place(int r, int c) { return c ^ (C == 8 ? (r >> 1) & 7 : r & 15); }
 
 // 16 bytes a lane from global memory to LDS (base + 16 * lane), asynchronously.
 __device__ __forceinline__ void load_to_lds(const char* from, _Float16* to) {
@@ -269,61 +294,12 @@ __device__ __forceinline__ void load_to_lds(const char* from, _Float16* to) {
                                    (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
-// Waits until at most `left` (0, 1 or 2) stages of N loads each are in flight
-// and every read of LDS is done, then meets the other waves: what they loaded
-// is there, and what they read may be overwritten.
-template <int N>
-__device__ __forceinline__ void stage_barrier(int left) {
-  if (left >= 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * N) : "memory");
-  else if (left == 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-  else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// What the epilogue reads for eight columns of one row, fetched ahead of the
-// stores before it (which the compiler must take for changing it).
-template <class TW>
-struct Fetched {
-  h8 hi, lo;       // X, or E
-  float d_row;     // of P's diagonal, or A's
-  Vec<TW, 8> old;  // weights
-};
-
-// Eight columns of one row of the result, in place in v: the epilogue's values
-// in the scale that is stored; written in row order.
-template <Product K, bool SPLIT, class TW>
-__device__ __forceinline__ void finish_row(const ProductArgs& a, int64_t at, int64_t diag, int row, int col,
-                                           float (&v)[8], const Fetched<TW>& f, const float (&d_col)[8]) {
-  const int64_t x_low = SPLIT ? kSplitCols : a.x_low;
-  h8 h, l;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if constexpr (K == kGram) {
-      const float t = v[e] * a.scale;
-      if (row == col + e) a.diag_a[diag + row] = t;
-      v[e] = row == col + e ? 0.0f : t * a.store;
-    } else if constexpr (K == kSquare) {
-      const float off = ((float)f.hi[e] + (SPLIT ? (float)f.lo[e] : 0.0f)) * a.load;
-      const float sq = v[e] * a.scale;
-      if (row == col + e) a.diag_p[diag + row] = fmaf(a.cc, fmaf(f.d_row, f.d_row, sq), a.cb * f.d_row);
-      const float t = fmaf(a.cc, sq, fmaf(a.cc, f.d_row + d_col[e], a.cb) * off);
-      v[e] = row == col + e ? 0.0f : t * a.store;
-    } else {
-      const float x = ((float)f.hi[e] + (float)f.lo[e]) * a.load;
-      v[e] = fmaf(a.ca + f.d_row, x, v[e] * a.scale) * a.store;
-    }
-    _Float16 p, q;
-    split_half(v[e], p, q);
-    h[e] = p;
-    l[e] = q;
-  }
-  if constexpr (K == kUpdate) {
-    *(h8*)(a.x + at) = h;
-    *(h8*)(a.x + at + x_low) = l;
-  } else if constexpr (K != kLast) {
-    _Float16* to = (K == kGram ? a.e : a.p) + at;
-    *(h8*)to = h;
-    if (SPLIT) *(h8*)(to + kSplitCols) = l;
-  }
+// Waits until at most LEFT loads are in flight and every read of LDS is done,
+// then meets the other waves: what they loaded is there, and what they read may
+// be overwritten.
+template <int LEFT>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
 // Eight consecutive results of the last step, to the caller's array.
@@ -344,14 +320,26 @@ __device__ __forceinline__ void put_result(const ProductArgs& a, int64_t plane_o
   }
 }
 
+// Eight columns of this lane's row, from columns `ld` apart, by two transposing reads.
+__device__ __forceinline__ h8 columns8(_Float16* from, int ld) {
+  typedef __attribute__((address_space(3))) s4* Lds;
+  union {
+    s4 s[2];
+    h8 h;
+  } u;
+  u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)from);
+  u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(from + 4 * ld));
+  return u.h;
+}
+
 template <Product K, bool SPLIT, class TW, bool MUON, class G>
-__global__ __launch_bounds__(G::WAVES* kWave, G::B == 192 ? 1 : 2) void k_ns_product(ProductArgs a) {
+__global__ __launch_bounds__(G::WAVES* kWave, G::EU) void k_ns_product(ProductArgs a) {
   constexpr int B = G::B, S = G::S, WAVES = G::WAVES, WC = G::WC, WM = G::WM, WN = G::WN, MI = G::MI, NI = G::NI;
   constexpr bool SYM = K == kGram || K == kSquare;
-  static_assert(S == 2 || S == 4, "ring");
+  static_assert(S >= 2 && S <= 4, "ring");
+  constexpr int BK = G::BK, STAGE = 2 * B * BK;
   // one array a stage, so that reads of one are seen not to depend on loads to another
-  __shared__ __align__(16) _Float16 s_0[2 * B * kBK], s_1[2 * B * kBK], s_2[S > 2 ? 2 * B * kBK : 8],
-      s_3[S > 2 ? 2 * B * kBK : 8];
+  __shared__ __align__(16) _Float16 s_0[STAGE], s_1[STAGE], s_2[S > 2 ? STAGE : 8], s_3[S > 3 ? STAGE : 8];
   __shared__ int s_state;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
   // Workgroups go to the 8 XCDs in turn: each XCD takes a run of neighbouring tiles.
@@ -396,35 +384,32 @@ __global__ __launch_bounds__(G::WAVES* kWave, G::B == 192 ? 1 : 2) void k_ns_pro
     const int cols_c = SYM ? a.mp : a.np;  // a tile may hang over: rows past the end are read as the last one
 #pragma unroll
     for (int i = 0; i < HALF; ++i) {
-      const int row = (i * WAVES + wave) * 8 + lane / 8;
-      off_l[i] = (u32)(min(row, a.mp - 1 - tm * B) * a.stride + chunk_place(row, lane % 8) * 8) * 2;
-      off_r[i] = (u32)(min(row, cols_c - 1 - tn * B) * a.stride + chunk_place(row, lane % 8) * 8) * 2;
+      const int row = (i * WAVES + wave) * G::ROWS + lane / G::CHUNKS;
+      const int chunk = chunk_place<G::CHUNKS>(row, lane % G::CHUNKS);
+      off_l[i] = (u32)(min(row, a.mp - 1 - tm * B) * a.stride + chunk * 8) * 2;
+      off_r[i] = (u32)(min(row, cols_c - 1 - tn * B) * a.stride + chunk * 8) * 2;
     }
-    const char* gl = (const char*)(a.l + batch * a.l_batch + (int64_t)tm * B * a.stride + (int64_t)first * kBK);
-    const char* gr = (const char*)(a.r + batch * a.r_batch + (int64_t)tn * B * a.stride + (int64_t)first * kBK);
+    const char* gl = (const char*)(a.l + batch * a.l_batch + (int64_t)tm * B * a.stride + (int64_t)first * BK);
+    const char* gr = (const char*)(a.r + batch * a.r_batch + (int64_t)tn * B * a.stride + (int64_t)first * BK);
     const int count = last - first;
     auto ring = [&](int i) -> _Float16* { return i == 0 ? s_0 : i == 1 ? s_1 : i == 2 ? s_2 : s_3; };
-    auto load = [&](int t, _Float16* to) {
-#pragma unroll
-      for (int i = 0; i < HALF; ++i) load_to_lds(gl + (int64_t)t * (kBK * 2) + off_l[i], to + (i * WAVES + wave) * 8 * kBK);
-#pragma unroll
-      for (int i = 0; i < HALF; ++i)
-        load_to_lds(gr + (int64_t)t * (kBK * 2) + off_r[i], to + B * kBK + (i * WAVES + wave) * 8 * kBK);
+    auto load = [&](int t, _Float16* to, int i) {  // the i-th of a stage's loads
+      const int j = i % HALF * WAVES + wave;
+      if (i < HALF) load_to_lds(gl + (int64_t)t * (BK * 2) + off_l[i], to + j * 512);
+      else load_to_lds(gr + (int64_t)t * (BK * 2) + off_r[i - HALF], to + B * BK + j * 512);
     };
     // Operands of 16 summation indices: [high, low parts][blocks of 32 rows]
-    constexpr int PARTS = SPLIT ? 2 : 1, KK = SPLIT ? 2 : 4;
+    constexpr int PARTS = SPLIT ? 2 : 1, KK = BK / 16 / PARTS;
     const int l_row = (wave / WC) * WM, r_row = (wave % WC) * WN;
     const int i32 = lane & 31, hi = lane >> 5;
     h8 x[2][PARTS][MI], y[2][PARTS][NI];
-    auto read = [&](const _Float16* from, int kk, int to) {
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p) {
-        const int place = chunk_place(i32, p * 4 + kk * 2 + hi) * 8;  // l_row, r_row: multiples of 32
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi) x[to][p][mi] = *(const h8*)(from + (l_row + mi * 32 + i32) * kBK + place);
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) y[to][p][ni] = *(const h8*)(from + (B + r_row + ni * 32 + i32) * kBK + place);
-      }
+    constexpr int READS = PARTS * (MI + NI), PRODUCTS = MI * NI * (SPLIT ? 3 : 1);
+    auto read = [&](const _Float16* from, int kk, int to, int i) {  // the i-th of the operands
+      const int p = i / (MI + NI), j = i % (MI + NI);
+      const int chunk = SPLIT ? kk / 2 * 8 + p * 4 + kk % 2 * 2 : kk * 2;
+      const int place = chunk_place<G::CHUNKS>(i32, chunk + hi) * 8;  // l_row, r_row: multiples of 32
+      if (j < MI) x[to][p][j] = *(const h8*)(from + (l_row + j * 32 + i32) * BK + place);
+      else y[to][p][j - MI] = *(const h8*)(from + (B + r_row + (j - MI) * 32 + i32) * BK + place);
     };
     f16v acc[MI][NI];
 #pragma unroll
@@ -433,48 +418,54 @@ __global__ __launch_bounds__(G::WAVES* kWave, G::B == 192 ? 1 : 2) void k_ns_pro
       for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[mi][ni][q] = 0.0f;
-    auto multiply = [&](int from) {
-#pragma unroll
-      for (int q = SPLIT ? 0 : 2; q < 3; ++q)  // high low, low high, high high
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-          for (int ni = 0; ni < NI; ++ni)
-            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[from][q == 1 ? PARTS - 1 : 0][mi],
-                                                                 y[from][q == 0 ? PARTS - 1 : 0][ni], acc[mi][ni], 0, 0, 0);
+    auto multiply = [&](int from, int i) {  // the i-th of the products: high low, low high, high high
+      const int q = SPLIT ? i / (MI * NI) : 2, mi = i % (MI * NI) / NI, ni = i % NI;
+      acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[from][q == 1 ? PARTS - 1 : 0][mi],
+                                                           y[from][q == 0 ? PARTS - 1 : 0][ni], acc[mi][ni], 0, 0, 0);
     };
     // One stage: S - 1 stages are in flight while it is multiplied; the operands
     // of the next 16 indices are read while these are multiplied, over the
-    // barrier too.
+    // barrier too.  Reads and loads stand between the products one by one: a row
+    // of them would hold the wave up at their queue with the matrix cores idle
+    // (8,192 x 2,048 in bf16: 1,036 -> 903 us).  Behind the last stage the loads
+    // repeat it and the reads give what nothing uses.
     auto step = [&](auto at, int t) {
       constexpr int b = decltype(at)::value;
-      if (t + S - 1 < count) load(t + S - 1, ring((b + S - 1) % S));
+      const int ahead = min(t + S - 1, count - 1);
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
-        if (kk + 1 < KK) {
-          read(ring(b), kk + 1, (kk + 1) & 1);
-        } else {  // behind the last stage this reads what nothing uses
-          stage_barrier<G::LOADS>(min(S - 2, count - t - 2));
-          read(ring((b + 1) % S), 0, 0);
+        const bool inside = kk + 1 < KK;
+        if (!inside) stage_barrier<(S - 2) * G::LOADS>();
+        const int l0 = inside ? G::LOADS * kk / (KK - 1) : 0, loads = inside ? G::LOADS * (kk + 1) / (KK - 1) - l0 : 0;
+        const int ops = READS + loads;
+#pragma unroll
+        for (int i = 0; i < PRODUCTS; ++i) {
+          multiply(kk & 1, i);
+#pragma unroll
+          for (int j = ops * i / PRODUCTS; j < ops * (i + 1) / PRODUCTS; ++j) {
+            if (j < READS) read(ring(inside ? b : (b + 1) % S), inside ? kk + 1 : 0, (kk + 1) & 1, j);
+            else load(ahead, ring((b + S - 1) % S), l0 + j - READS);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);  // the reads stay ahead of the products
-        multiply(kk & 1);
-        __builtin_amdgcn_sched_barrier(0);
       }
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
-      if (i < count) load(i, ring(i));
-    stage_barrier<G::LOADS>(min(S - 2, count - 1));
-    read(ring(0), 0, 0);
+#pragma unroll
+      for (int j = 0; j < G::LOADS; ++j) load(min(i, count - 1), ring(i), j);
+    stage_barrier<(S - 2) * G::LOADS>();
+#pragma unroll
+    for (int j = 0; j < READS; ++j) read(ring(0), 0, 0, j);
     for (int t = 0; t < count; t += S) {
       step(std::integral_constant<int, 0>{}, t);
-      if (B > 64 || t + 1 < count) step(std::integral_constant<int, 1>{}, t + 1);  // B > 64: count is even
-      if constexpr (S > 2) {
+      if ((S == 2 && B > 64) || t + 1 < count) step(std::integral_constant<int, 1>{}, t + 1);  // B > 64: count is even
+      if constexpr (S > 2)
         if (t + 2 < count) step(std::integral_constant<int, 2>{}, t + 2);
+      if constexpr (S > 3)
         if (t + 3 < count) step(std::integral_constant<int, 3>{}, t + 3);
-      }
     }
+    stage_barrier<0>();  // LDS is free for sums and strips
     if (G::SHARE && count < nt) {
       // Sums pass between workgroups at device scope (stores written through,
       // loads that miss what a nearer cache holds), ordered by the counter.
@@ -537,107 +528,169 @@ __global__ __launch_bounds__(G::WAVES* kWave, G::B == 192 ? 1 : 2) void k_ns_pro
         }
       }
     }
-    // Epilogue: every wave turns its tile in its own part of LDS, 32 rows at a
-    // time: once out in row order (16 bytes a lane), once transposed.  What it
-    // reads is fetched for 32 rows at once, where registers allow while the rows
-    // before are worked on.
-    constexpr int VR = WN / 8, ITS = 32 * VR / kWave, LD = WN + 2;  // vectors a row; of them a lane
-    constexpr int AHEAD = MI <= 2 ? 1 : 0;
-    static_assert(WAVES / 2 * 32 * LD * 4 <= 2 * B * kBK * 2, "a wave's strip fits its part of a stage");
-    float* strip = (float*)(wave < WAVES / 2 ? s_0 : s_1) + wave % (WAVES / 2) * 32 * LD;
-    const int64_t diag = (int64_t)batch * a.mp;
-    const int64_t plane_c = (int64_t)batch * a.mp * (SYM ? a.mp : a.np) * PARTS;
-    const int64_t plane_o = (int64_t)batch * a.rows * a.cols;
+    // Epilogue, 32 rows at a time, on the registers as the products leave them:
+    // lane (h, c) holds rows 8 g + 4 h + 0..3 of column c of a block.  Results go
+    // through the wave's own strip of LDS, column by column in fp16, and out in
+    // both orders: runs of 8 rows as they lie, runs of 8 columns by transposing
+    // reads.
+    constexpr int LDR = 40, LDF = WN + 2;  // a column of a strip, a row of the last step's fp32 strip
+    constexpr int STRIP = (32 * LDF * 4 > PARTS * WN * LDR * 2 ? 32 * LDF * 4 : PARTS * WN * LDR * 2) / 2;
+    constexpr int PER = WAVES / (S >= 4 ? 4 : 2);  // strips a stage
+    static_assert(PER * STRIP <= STAGE, "the waves' strips fit their stages");
+    _Float16* strip = ring(wave / PER) + wave % PER * STRIP;
+    const int h = hi, c32 = i32;
     const int row0 = tm * B + l_row, col0 = tn * B + r_row;
-    auto strip_row = [&](int it) { return (it * kWave + lane) / VR; };
-    auto strip_col = [&](int it) { return (it * kWave + lane) % VR * 8; };
-    auto at_of = [&](int row, int col) { return plane_c + place_of<SPLIT>(row, col, SYM ? a.mp : a.np); };
-    Fetched<TW> f[AHEAD + 1][ITS];
-    auto fetch = [&](int mi, Fetched<TW>(&to)[ITS]) {
+    const float* diag_in = (K == kSquare ? a.diag_a : a.diag_p) + (int64_t)batch * a.mp;
+    const int64_t plane = (int64_t)batch * a.mp * cols_c * PARTS;
+    _Float16* by_row = (K == kGram ? a.e : K == kSquare ? a.p : a.x) + plane;
+    _Float16* by_col = (K == kGram ? a.e : K == kSquare ? a.p : a.t) + plane;
+    f4* xf = (f4*)a.xf + (((int64_t)batch * a.tiles + tm * a.tiles_n + tn) * WAVES + wave) * (MI * NI * 4 * kWave) + lane;
+    // fetched for 32 rows at once, while the rows before are worked on
+    f4 x_in[2][NI][4], d_in[2][4];
+    h4 e_in[2][PARTS][NI][4];
+    auto fetch = [&](int mi, int to) {
+      if (K == kGram || row0 + mi * 32 >= a.mp) return;
 #pragma unroll
-      for (int it = 0; it < ITS; ++it) {
-        const int row = row0 + mi * 32 + strip_row(it), col = col0 + strip_col(it);
-        if (row >= a.mp || col >= cols_c) continue;
-        if constexpr (K != kGram) {
-          const _Float16* from = (K == kSquare ? a.e : a.x) + at_of(row, col);
-          to[it].hi = *(const h8*)from;
-          if (SPLIT) to[it].lo = *(const h8*)(from + kSplitCols);
-          else if (K != kSquare) to[it].lo = *(const h8*)(from + a.x_low);
-          to[it].d_row = (K == kSquare ? a.diag_a : a.diag_p)[diag + row];
-        }
-        if constexpr (K == kLast && MUON) {
-          const int r = a.tall ? col0 + (it * kWave + lane) / 4 : row;
-          const int c = a.tall ? row0 + mi * 32 + lane % 4 * 8 : col;
-          if (r < a.rows && c + 8 <= a.cols) to[it].old = load_vec<TW, 8>((const TW*)a.out + plane_o + (int64_t)r * a.cols + c);
+      for (int g = 0; g < 4; ++g) d_in[to][g] = *(const f4*)(diag_in + row0 + mi * 32 + 8 * g + 4 * h);
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        if (col0 + ni * 32 >= cols_c) continue;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if constexpr (K == kSquare) {  // E is symmetric: its row `col`
+            const _Float16* from = a.e + plane + place_of<SPLIT>(col0 + ni * 32 + c32, row0 + mi * 32 + 8 * g + 4 * h, a.mp);
+            e_in[to][0][ni][g] = *(const h4*)from;
+            if (SPLIT) e_in[to][PARTS - 1][ni][g] = *(const h4*)(from + kSplitCols);
+          } else {
+            x_in[to][ni][g] = xf[((mi * NI + ni) * 4 + g) * kWave];
+          }
         }
       }
     };
-    // one column for every it where VR divides the wave
-    constexpr int COLS = kWave % VR == 0 ? 1 : ITS;
-    float d_col[COLS][8];
+    float d_col[NI];
     if constexpr (K == kSquare) {
 #pragma unroll
-      for (int it = 0; it < COLS; ++it)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d_col[it][e] = a.diag_a[diag + min(col0 + strip_col(it) + e, a.mp - 1)];
+      for (int ni = 0; ni < NI; ++ni) {
+        const int col = col0 + ni * 32 + c32;
+        d_col[ni] = col < cols_c ? diag_in[col] : 0.0f;
+      }
     }
-    fetch(0, f[0]);
+    fetch(0, 0);
     __syncthreads();
+    const float to_stored = a.scale * a.store;  // powers of two
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
-      if (AHEAD ? mi + 1 < MI : mi > 0) fetch(mi + AHEAD, f[(mi + AHEAD) & AHEAD]);
+      if (row0 + mi * 32 >= a.mp) break;
+      if (mi + 1 < MI) fetch(mi + 1, (mi + 1) & 1);
 #pragma unroll
-      for (int ni = 0; ni < NI; ++ni)
+      for (int ni = 0; ni < NI; ++ni) {
+        if (col0 + ni * 32 >= cols_c) continue;
+        const bool on_diagonal = SYM && row0 + mi * 32 == col0 + ni * 32;
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
-          strip[(8 * (q / 4) + 4 * (lane >> 5) + q % 4) * LD + ni * 32 + (lane & 31)] = acc[mi][ni][q];
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int g = 0; g < 4; ++g) {
+          f4 v;
 #pragma unroll
-      for (int it = 0; it < ITS; ++it) {
-        const int r = strip_row(it), c = strip_col(it);
-        float* s = strip + r * LD + c;
-        float v[8];
+          for (int r = 0; r < 4; ++r) {
+            const float sum = acc[mi][ni][4 * g + r];
+            if constexpr (K == kGram) {
+              v[r] = sum * to_stored;
+            } else if constexpr (K == kSquare) {
+              const float e = (float)e_in[mi & 1][0][ni][g][r] + (SPLIT ? (float)e_in[mi & 1][PARTS - 1][ni][g][r] : 0.0f);
+              const float d = fmaf(a.cc, d_in[mi & 1][g][r] + d_col[ni], a.cb) * (a.load * a.store);
+              v[r] = fmaf(d, e, sum * (a.cc * to_stored));
+            } else {
+              v[r] = fmaf((a.ca + d_in[mi & 1][g][r]) * (a.load * a.store), x_in[mi & 1][ni][g][r], sum * to_stored);
+            }
+          }
+          if (on_diagonal && c32 / 8 == g && c32 / 4 % 2 == h) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = s[e];
-        const int row = row0 + mi * 32 + r, col = col0 + c;
-        if (row >= a.mp || col >= cols_c) continue;
-        finish_row<K, SPLIT, TW>(a, at_of(row, col), diag, row, col, v, f[mi & AHEAD][it], d_col[it % COLS]);
-        if (K == kLast && !a.tall) {
-          put_result<TW, MUON>(a, plane_o, row, col, v, f[mi & AHEAD][it].old);
-        } else {
+            for (int r = 0; r < 4; ++r) {
+              if (c32 % 4 != r) continue;
+              const float sum = acc[mi][ni][4 * g + r] * a.scale;
+              const int64_t at = (int64_t)batch * a.mp + row0 + mi * 32 + c32;
+              if constexpr (K == kGram) {
+                a.diag_a[at] = sum;
+              } else if constexpr (K == kSquare) {
+                const float d = d_in[mi & 1][g][r];
+                a.diag_p[at] = fmaf(a.cc, fmaf(d, d, sum), a.cb * d);
+              }
+              v[r] = 0.0f;
+            }
+          }
+          if constexpr (K == kLast) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[e] = v[e];
+            for (int r = 0; r < 4; ++r) ((float*)strip)[(8 * g + 4 * h + r) * LDF + ni * 32 + c32] = v[r];
+          } else {
+            if (K == kUpdate) xf[((mi * NI + ni) * 4 + g) * kWave] = v;
+            h4 p, q;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              _Float16 x1, x2;
+              split_half(v[r], x1, x2);
+              p[r] = x1;
+              q[r] = x2;
+            }
+            _Float16* to = strip + (ni * 32 + c32) * LDR + 8 * g + 4 * h;
+            *(h4*)to = p;
+            if (SPLIT) *(h4*)(to + WN * LDR) = q;
+          }
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      const bool turned = SYM ? tm != tn : K == kLast ? a.tall != 0 : true;
-      if (turned) {
+      constexpr int ITS = WN / 16;  // vectors of 8 a lane
+      if constexpr (K == kLast) {
+        const int64_t plane_o = (int64_t)batch * a.rows * a.cols;
+        const float* rows = (const float*)strip;
+        Vec<TW, 8> old[ITS];
+        int at_r[ITS], at_c[ITS], in[ITS];
 #pragma unroll
         for (int it = 0; it < ITS; ++it) {
-          const int c = (it * kWave + lane) / 4, r = lane % 4 * 8;
-          float v[8];
-          h8 h, l;
+          const int i = it * kWave + lane;
+          const int r = a.tall ? i % 4 * 8 : i / (WN / 8), c = a.tall ? i / 4 : i % (WN / 8) * 8;
+          at_r[it] = a.tall ? col0 + c : row0 + mi * 32 + r;
+          at_c[it] = a.tall ? row0 + mi * 32 + r : col0 + c;
+          in[it] = r * LDF + c;
+          if (MUON && at_r[it] < a.rows && at_c[it] + 8 <= a.cols)
+            old[it] = load_vec<TW, 8>((const TW*)a.out + plane_o + (int64_t)at_r[it] * a.cols + at_c[it]);
+        }
+        const int stride_v = a.tall ? LDF : 1;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] = strip[(r + e) * LD + c];
-            _Float16 p, q;
-            split_half(v[e], p, q);
-            h[e] = p;
-            l[e] = q;
-          }
-          const int row = row0 + mi * 32 + r, col = col0 + c;
-          if (row >= a.mp || col >= cols_c) continue;
-          if constexpr (K == kLast) {
-            put_result<TW, MUON>(a, plane_o, col, row, v, f[mi & AHEAD][it].old);
-          } else {
-            _Float16* to = (K == kGram ? a.e : K == kSquare ? a.p : a.t) + plane_c + place_of<SPLIT>(col, row, a.mp);
-            *(h8*)to = h;
-            if (SPLIT) *(h8*)(to + kSplitCols) = l;
+        for (int it = 0; it < ITS; ++it) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = rows[in[it] + e * stride_v];
+          put_result<TW, MUON>(a, plane_o, at_r[it], at_c[it], v, old[it]);
+        }
+      } else {
+#pragma unroll
+        for (int it = 0; it < ITS; ++it) {
+          const int i = it * kWave + lane, c = i / 4, r = i % 4 * 8;
+          if (col0 + c >= cols_c) continue;
+          _Float16* to = by_col + place_of<SPLIT>(col0 + c, row0 + mi * 32 + r, a.mp);
+          *(h8*)to = *(const h8*)(strip + c * LDR + r);
+          if (SPLIT) *(h8*)(to + kSplitCols) = *(const h8*)(strip + (WN + c) * LDR + r);
+        }
+        if (!SYM || tm != tn) {  // a tile on the diagonal is its own transpose
+          // 16 lanes transpose 16 rows x 4 columns: lane s reads rows 4 (s % 4).. of
+          // column s / 4 and gets row s
+          const int s = lane & 15;
+#pragma unroll
+          for (int it = 0; it < ITS; ++it) {
+            const int group = it * 4 + lane / 16, c = group % (WN / 8) * 8, r = group / (WN / 8) * 16;
+            _Float16* from = strip + (c + s / 4) * LDR + r + s % 4 * 4;
+            const h8 p = columns8(from, LDR);
+            h8 q;
+            if (SPLIT) q = columns8(from + WN * LDR, LDR);
+            if (col0 + c >= cols_c) continue;
+            _Float16* to = by_row + place_of<SPLIT>(row0 + mi * 32 + r + s, col0 + c, cols_c);
+            *(h8*)to = p;
+            if (SPLIT) *(h8*)(to + kSplitCols) = q;
           }
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }    if (G::SHARE) __syncthreads();  // the next tile's stages overwrite the strips
+    }
+    if (G::SHARE) __syncthreads();  // the next tile's stages overwrite the strips
   }
 }
 
@@ -685,33 +738,41 @@ struct NsPlan {
   int share[2];  // stages of a workgroup in the gram and the square, where tiles are shared
   int arrive;    // counters to clear
   bool split, small;
-  size_t part, diag_a, diag_p, x, t[2], e, p, sums, arrived, total;  // byte offsets
-  int64_t x_low;  // elements between X's high and low parts (not split)
+  size_t part, diag_a, diag_p, x, t[2], xf, e, p, sums, arrived, total;  // byte offsets
 };
 
-typedef Shape<64, 2, 2, 4> Tile64;
-typedef Shape<64, 2, 2, 4, true> Tile64Shared;
-typedef Shape<128, 2, 2, 2> Tile128;
-typedef Shape<128, 2, 2, 4> Tile128Deep;
-typedef Shape<192, 2, 2, 2> Tile192;
-typedef Shape<256, 2, 4, 2> Tile256;
-enum { k64, k128, k128Deep, k192, k256, k64Shared, kShapes };
-constexpr int kTile[kShapes] = {64, 128, 128, 192, 256, 64};
+typedef Shape<64, 2, 2, 64, 4> Tile64;
+typedef Shape<64, 2, 2, 128, 4> Tile64Deep;
+typedef Shape<64, 2, 2, 128, 4, true> Tile64Shared;
+typedef Shape<128, 2, 2, 64, 2> Tile128;
+typedef Shape<128, 2, 2, 64, 4> Tile128Deep;
+typedef Shape<192, 2, 2, 64, 2> Tile192;
+typedef Shape<256, 2, 4, 64, 2> Tile256;
+enum { k64, k64Deep, k128, k128Deep, k192, k256, k64Shared, kShapes };
+constexpr int kTile[kShapes] = {64, 64, 128, 128, 192, 256, 64};
+constexpr int kWaveRows[] = {Tile64::WM, Tile64Deep::WM, Tile128::WM, Tile128Deep::WM, Tile192::WM, Tile256::WM};
+constexpr int kWaveCols[] = {Tile64::WN, Tile64Deep::WN, Tile128::WN, Tile128Deep::WN, Tile192::WN, Tile256::WN};
 
 // The shape of a product is the one with the least time by this model, fitted
 // to products of 128 to 8,192 a side: `fixed` us for the first stages' way and
-// the epilogue, and a time a stage, lower where every workgroup has a compute
-// unit of its own.  With more tiles than fit at once the last round costs about
-// a third of a round more than its share.
+// the epilogue, and a time for 64 summation indices (for 32 with their low
+// parts in split products).  Shapes of which two workgroups fit a compute unit
+// take longer a stage where they do; then the last of several rounds costs a
+// third of a round more than its share, else a whole round.
 struct ShapeTime {
-  int slots;          // workgroups that fit at once
-  float fixed, full, alone;  // us, and us a stage: all slots taken, one workgroup a compute unit
-  float full_split, alone_split;
+  int slots;  // workgroups that fit at once
+  struct {
+    float fixed, alone, full;  // us, and us a stage: one workgroup a compute unit, all slots taken
+  } whole, split;
 };
 constexpr ShapeTime kTime[kShapes] = {
-    {512, 4.5f, 0.55f, 0.21f, 0.65f, 0.27f},   {512, 8.0f, 1.05f, 0.75f, 1.3f, 0.95f},
-    {256, 8.0f, 0.55f, 0.55f, 0.85f, 0.85f},   {256, 11.0f, 1.05f, 1.05f, 1.45f, 1.45f},
-    {256, 14.0f, 1.75f, 1.75f, 2.8f, 2.8f},    {512, 12.5f, 0.3f, 0.25f, 0.4f, 0.3f},
+    {512, {4.0f, 0.36f, 0.5f}, {4.5f, 0.29f, 0.5f}},     // 64
+    {256, {4.8f, 0.24f, 0.24f}, {4.8f, 0.22f, 0.22f}},   // 64 deep
+    {512, {6.8f, 0.61f, 0.8f}, {11.0f, 0.76f, 1.15f}},   // 128
+    {256, {6.0f, 0.48f, 0.48f}, {11.0f, 0.54f, 0.54f}},  // 128 deep
+    {256, {11.0f, 0.95f, 0.95f}, {18.0f, 1.2f, 1.2f}},   // 192
+    {256, {10.0f, 1.5f, 1.5f}, {17.0f, 2.0f, 2.0f}},     // 256
+    {256, {10.0f, 0.24f, 0.24f}, {10.0f, 0.22f, 0.22f}},  // 64 shared
 };
 
 static int64_t tiles_of(const NsPlan& p, int64_t batch, int shape, bool symmetric) {
@@ -719,30 +780,31 @@ static int64_t tiles_of(const NsPlan& p, int64_t batch, int shape, bool symmetri
   return batch * (symmetric ? tm * (tm + 1) / 2 : tm * tn);
 }
 
-// Stages a workgroup takes where tiles are shared: at most four workgroups a
-// tile, and eight stages at least.
+// Stages (of 128) a workgroup takes where tiles are shared: at most four
+// workgroups a tile, and four stages at least.
 static int64_t pick_share(int64_t tiles, int64_t nt) {
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(512, std::min(tiles * 4, tiles * nt / 8)));
-  return ((tiles * nt + most - 1) / most + 1) / 2 * 2;
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(256, std::min(tiles * 4, tiles * nt / 4)));
+  return (tiles * nt + most - 1) / most;
 }
 
 static int pick_shape(const NsPlan& p, int64_t batch, int64_t k, bool symmetric) {
-  const int64_t nt = k * (p.split ? 2 : 1) / kBK;
+  const int64_t nt = k * (p.split ? 2 : 1) / 64;
   int best = k64;
   double least = 1e30;
   for (int i = 0; i < kShapes; ++i) {
     if (i == k64Shared && !symmetric) continue;
-    const ShapeTime& t = kTime[i];
+    const auto& t = p.split ? kTime[i].split : kTime[i].whole;
+    const int slots = kTime[i].slots;
     int64_t work = tiles_of(p, batch, i, symmetric), stages = nt;
     if (i == k64Shared) {
-      stages = pick_share(work, nt);
+      stages = 2 * pick_share(work, nt / 2);
       if (stages >= nt) continue;
-      work = (work * nt + stages - 1) / stages;
+      work = 1;  // one round
     }
-    const double full = p.split ? t.full_split : t.full, alone = p.split ? t.alone_split : t.alone;
-    const double us = t.fixed + stages * (work <= 256        ? alone
-                                          : work <= t.slots ? full
-                                                            : full * ((double)work / t.slots + 0.35));
+    double us;
+    if (work <= 256) us = t.fixed + stages * t.alone;
+    else if (slots == 256) us = (t.fixed + stages * t.full) * ((work + 255) / 256);
+    else us = t.fixed + stages * t.full * (work <= slots ? 1.0 : (double)work / slots + 0.35);
     if (us < least) least = us, best = i;
   }
   return best;
@@ -768,7 +830,6 @@ static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPla
   p->shape[2] = pick_shape(*p, batch, p->mp, false);
   p->blocks = norm_blocks(batch, rows * cols);
   const int64_t xs = batch * p->mp * p->np, as = batch * p->mp * p->mp;
-  p->x_low = xs;
   size_t at = kWorkspaceHeader;
   auto take = [&](int64_t bytes) {
     const size_t here = at;
@@ -778,7 +839,8 @@ static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPla
   p->part = take(batch * p->blocks * 8);
   p->diag_a = take(batch * p->mp * 4);
   p->diag_p = take(batch * p->mp * 4);
-  p->x = take(xs * 4);
+  p->x = take(xs * (split ? 4 : 2));
+  p->xf = take(tiles_of(*p, batch, p->shape[2], false) * kTile[p->shape[2]] * kTile[p->shape[2]] * 4);
   for (size_t& t : p->t) t = take(xs * (split ? 4 : 2));
   p->e = take(as * (split ? 4 : 2));
   p->p = take(as * (split ? 4 : 2));
@@ -786,7 +848,7 @@ static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPla
   p->arrive = 0;
   for (int i = 0; i < 2; ++i) {
     if (p->shape[i] != k64Shared) continue;
-    const int64_t tiles = tiles_of(*p, batch, k64Shared, true), nt = (int64_t)(i ? p->mp : p->np) * (split ? 2 : 1) / kBK;
+    const int64_t tiles = tiles_of(*p, batch, k64Shared, true), nt = (int64_t)(i ? p->mp : p->np) * (split ? 2 : 1) / Tile64Shared::BK;
     p->share[i] = (int)pick_share(tiles, nt);
     p->arrive = (int)tiles;
     runs = std::max(runs, (tiles * nt + p->share[i] - 1) / p->share[i]);
@@ -801,6 +863,7 @@ template <Product K, bool SPLIT, class TW, bool MUON, class G>
 static void launch_tiles(const NsPlan& p, ProductArgs a, int64_t batch, hipStream_t stream) {
   const int tm = (p.mp + G::B - 1) / G::B;
   a.tiles_n = (p.np + G::B - 1) / G::B;
+  a.stages = a.stride / G::BK;
   a.tiles = K == kGram || K == kSquare ? tm * (tm + 1) / 2 : tm * a.tiles_n;
   int64_t blocks = a.tiles * batch;
   if (G::SHARE) {
@@ -816,6 +879,7 @@ template <Product K, bool SPLIT, class TW, bool MUON>
 static void launch_product(const NsPlan& p, const ProductArgs& a, int64_t batch, hipStream_t stream) {
   constexpr bool SYM = K == kGram || K == kSquare;
   switch (p.shape[K == kGram ? 0 : K == kSquare ? 1 : 2]) {
+    case k64Deep: return launch_tiles<K, SPLIT, TW, MUON, Tile64Deep>(p, a, batch, stream);
     case k128: return launch_tiles<K, SPLIT, TW, MUON, Tile128>(p, a, batch, stream);
     case k128Deep: return launch_tiles<K, SPLIT, TW, MUON, Tile128Deep>(p, a, batch, stream);
     case k192: return launch_tiles<K, SPLIT, TW, MUON, Tile192>(p, a, batch, stream);
@@ -838,7 +902,7 @@ static void run_steps(const NsCall& q, const NsPlan& p, const StepScales& s, cha
   a.e = (_Float16*)(ws + p.e);
   a.p = (_Float16*)(ws + p.p);
   a.x = (_Float16*)(ws + p.x);
-  a.x_low = p.x_low;
+  a.xf = (float*)(ws + p.xf);
   a.sums = (float*)(ws + p.sums);
   a.arrived = (u32*)(ws + p.arrived);
   a.ca = (float)q.a;
@@ -857,7 +921,6 @@ static void run_steps(const NsCall& q, const NsPlan& p, const StepScales& s, cha
     g.l = g.r = a.x;
     g.l_batch = g.r_batch = x_size;
     g.stride = p.np * PARTS;
-    g.stages = g.stride / kBK;
     g.scale = 1.0f / (sx * sx);
     g.store = sa;
     launch_product<kGram, SPLIT, float, false>(p, g, q.batch, stream);
@@ -865,7 +928,6 @@ static void run_steps(const NsCall& q, const NsPlan& p, const StepScales& s, cha
     g.l = g.r = a.e;
     g.l_batch = g.r_batch = a_size;
     g.stride = p.mp * PARTS;
-    g.stages = g.stride / kBK;
     g.scale = 1.0f / (sa * sa);
     g.load = 1.0f / sa;
     g.store = sp;
@@ -877,7 +939,6 @@ static void run_steps(const NsCall& q, const NsPlan& p, const StepScales& s, cha
     g.r_batch = x_size;
     g.t = (_Float16*)(ws + p.t[(t & 1) ^ 1]);
     g.stride = p.mp * PARTS;
-    g.stages = g.stride / kBK;
     g.scale = 1.0f / (sp * sx);
     g.load = 1.0f / sx;
     g.store = s.x[t + 1];
@@ -901,7 +962,10 @@ static tgs_status ns_run(const NsCall& q, const NsPlan& p, const StepScales& s, 
   k.part = (const double*)(ws + p.part);
   k.x_out = (_Float16*)(ws + p.x);
   k.t_out = (_Float16*)(ws + p.t[0]);
-  k.x_low = p.x_low;
+  k.xf = (float*)(ws + p.xf);
+  k.tile = kTile[p.shape[2]];
+  k.tile_rows = kWaveRows[p.shape[2]];
+  k.tile_cols = kWaveCols[p.shape[2]];
   k.split = p.split;
   k.arrived = (u32*)(ws + p.arrived);
   k.arrive = p.arrive;
