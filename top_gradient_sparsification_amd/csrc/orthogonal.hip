@@ -48,7 +48,6 @@
 namespace tgs {
 
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-typedef short s4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
@@ -249,8 +248,8 @@ struct ProductArgs {
   int stride, stages;  // stages: of BK elements
   int mp, np;      // C is [mp][mp] (gram, square) or [mp][np]
   int tiles, tiles_n;  // tiles a matrix; of them in a row (update)
-  int units, share;  // gram, square: stages of all tiles, and of them a workgroup's
-  float* sums;       // gram, square: [workgroups][2][B * B] partial sums of tiles that workgroups share
+  int units, share;  // gram, shared tiles: stages of all tiles, and of them a workgroup's
+  float* sums;       // [workgroups][2][B * B] partial sums of tiles that workgroups share
   u32* arrived;      // of their workgroups, per tile; zero between products
   float scale;     // accumulator to true value
   // in/out of the epilogues
@@ -272,7 +271,7 @@ struct ProductArgs {
 
 // A workgroup's share of a product: a B x B tile, WR x WC waves, a ring of S
 // stages in LDS.  SHARE: workgroups take equal runs of the list of all tiles'
-// stages (symmetric products).
+// stages (the gram).
 template <int B_, int WR_, int WC_, int BK_, int S_, bool SHARE_ = false>
 struct Shape {
   static constexpr int BK = BK_, CHUNKS = BK_ / 8, ROWS = 64 / CHUNKS;  // elements and chunks of a row a stage, rows a load
@@ -318,18 +317,6 @@ __device__ __forceinline__ void put_result(const ProductArgs& a, int64_t plane_o
     for (int e = 0; e < 7; ++e)
       if (c + e < a.cols) p[e] = from_f32<TW>(MUON ? fmaf(a.keep, to_f32(p[e]), a.gain * v[e]) : v[e]);
   }
-}
-
-// Eight columns of this lane's row, from columns `ld` apart, by two transposing reads.
-__device__ __forceinline__ h8 columns8(_Float16* from, int ld) {
-  typedef __attribute__((address_space(3))) s4* Lds;
-  union {
-    s4 s[2];
-    h8 h;
-  } u;
-  u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)from);
-  u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(from + 4 * ld));
-  return u.h;
 }
 
 template <Product K, bool SPLIT, class TW, bool MUON, class G>
@@ -678,9 +665,9 @@ __global__ __launch_bounds__(G::WAVES* kWave, G::EU) void k_ns_product(ProductAr
           for (int it = 0; it < ITS; ++it) {
             const int group = it * 4 + lane / 16, c = group % (WN / 8) * 8, r = group / (WN / 8) * 16;
             _Float16* from = strip + (c + s / 4) * LDR + r + s % 4 * 4;
-            const h8 p = columns8(from, LDR);
+            const h8 p = columns8(from, from + 4 * LDR);
             h8 q;
-            if (SPLIT) q = columns8(from + WN * LDR, LDR);
+            if (SPLIT) q = columns8(from + WN * LDR, from + (WN + 4) * LDR);
             if (col0 + c >= cols_c) continue;
             _Float16* to = by_row + place_of<SPLIT>(row0 + mi * 32 + r + s, col0 + c, cols_c);
             *(h8*)to = p;
@@ -735,9 +722,9 @@ static bool step_scales(int steps, double a, double b, double c, StepScales* s) 
 struct NsPlan {
   int m, n, mp, np, tall, blocks;
   int shape[3];  // of the gram, the square and the update
-  int share[2];  // stages of a workgroup in the gram and the square, where tiles are shared
+  int share;     // stages of a workgroup in the gram, where tiles are shared
   int arrive;    // counters to clear
-  bool split, small;
+  bool split, small, lds;
   size_t part, diag_a, diag_p, x, t[2], xf, e, p, sums, arrived, total;  // byte offsets
 };
 
@@ -787,12 +774,13 @@ static int64_t pick_share(int64_t tiles, int64_t nt) {
   return (tiles * nt + most - 1) / most;
 }
 
-static int pick_shape(const NsPlan& p, int64_t batch, int64_t k, bool symmetric) {
+static int pick_shape(const NsPlan& p, int64_t batch, int64_t k, Product product) {
+  const bool symmetric = product == kGram || product == kSquare;
   const int64_t nt = k * (p.split ? 2 : 1) / 64;
   int best = k64;
   double least = 1e30;
   for (int i = 0; i < kShapes; ++i) {
-    if (i == k64Shared && !symmetric) continue;
+    if (i == k64Shared && product != kGram) continue;  // a square's sums are too short
     const auto& t = p.split ? kTime[i].split : kTime[i].whole;
     const int slots = kTime[i].slots;
     int64_t work = tiles_of(p, batch, i, symmetric), stages = nt;
@@ -821,13 +809,18 @@ static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPla
     p->total = small_workspace_bytes(batch, rows, cols);
     return true;
   }
+  p->lds = lds_holds(rows, cols, split);
+  if (p->lds) {
+    p->total = kWorkspaceHeader;
+    return true;
+  }
   auto up = [](int64_t v, int64_t to) { return (v + to - 1) / to * to; };
   // tiles may hang over, but shapes above 64 take stages in pairs
   p->mp = (int)up(p->m, 128);
   p->np = (int)up(p->n, 128);
-  p->shape[0] = pick_shape(*p, batch, p->np, true);
-  p->shape[1] = pick_shape(*p, batch, p->mp, true);
-  p->shape[2] = pick_shape(*p, batch, p->mp, false);
+  p->shape[0] = pick_shape(*p, batch, p->np, kGram);
+  p->shape[1] = pick_shape(*p, batch, p->mp, kSquare);
+  p->shape[2] = pick_shape(*p, batch, p->mp, kUpdate);
   p->blocks = norm_blocks(batch, rows * cols);
   const int64_t xs = batch * p->mp * p->np, as = batch * p->mp * p->mp;
   size_t at = kWorkspaceHeader;
@@ -846,12 +839,11 @@ static bool ns_plan(int64_t batch, int64_t rows, int64_t cols, bool split, NsPla
   p->p = take(as * (split ? 4 : 2));
   int64_t runs = 0;
   p->arrive = 0;
-  for (int i = 0; i < 2; ++i) {
-    if (p->shape[i] != k64Shared) continue;
-    const int64_t tiles = tiles_of(*p, batch, k64Shared, true), nt = (int64_t)(i ? p->mp : p->np) * (split ? 2 : 1) / Tile64Shared::BK;
-    p->share[i] = (int)pick_share(tiles, nt);
+  if (p->shape[0] == k64Shared) {
+    const int64_t tiles = tiles_of(*p, batch, k64Shared, true), nt = (int64_t)p->np * (split ? 2 : 1) / Tile64Shared::BK;
+    p->share = (int)pick_share(tiles, nt);
     p->arrive = (int)tiles;
-    runs = std::max(runs, (tiles * nt + p->share[i] - 1) / p->share[i]);
+    runs = (tiles * nt + p->share - 1) / p->share;
   }
   p->sums = take(runs * 2 * 64 * 64 * 4);
   p->arrived = take((int64_t)p->arrive * 4);
@@ -868,7 +860,7 @@ static void launch_tiles(const NsPlan& p, ProductArgs a, int64_t batch, hipStrea
   int64_t blocks = a.tiles * batch;
   if (G::SHARE) {
     a.units = (int)(blocks * a.stages);
-    a.share = p.share[K == kSquare];
+    a.share = p.share;
     blocks = (a.units + a.share - 1) / a.share;
   }
   hipLaunchKernelGGL((k_ns_product<K, SPLIT, TW, MUON, G>), dim3((unsigned)blocks), dim3(G::WAVES * kWave), 0,
@@ -877,7 +869,6 @@ static void launch_tiles(const NsPlan& p, ProductArgs a, int64_t batch, hipStrea
 
 template <Product K, bool SPLIT, class TW, bool MUON>
 static void launch_product(const NsPlan& p, const ProductArgs& a, int64_t batch, hipStream_t stream) {
-  constexpr bool SYM = K == kGram || K == kSquare;
   switch (p.shape[K == kGram ? 0 : K == kSquare ? 1 : 2]) {
     case k64Deep: return launch_tiles<K, SPLIT, TW, MUON, Tile64Deep>(p, a, batch, stream);
     case k128: return launch_tiles<K, SPLIT, TW, MUON, Tile128>(p, a, batch, stream);
@@ -885,7 +876,7 @@ static void launch_product(const NsPlan& p, const ProductArgs& a, int64_t batch,
     case k192: return launch_tiles<K, SPLIT, TW, MUON, Tile192>(p, a, batch, stream);
     case k256: return launch_tiles<K, SPLIT, TW, MUON, Tile256>(p, a, batch, stream);
     case k64Shared:
-      if constexpr (SYM) launch_tiles<K, SPLIT, TW, MUON, Tile64Shared>(p, a, batch, stream);
+      if constexpr (K == kGram) launch_tiles<K, SPLIT, TW, MUON, Tile64Shared>(p, a, batch, stream);
       return;
     default: return launch_tiles<K, SPLIT, TW, MUON, Tile64>(p, a, batch, stream);
   }
@@ -949,8 +940,9 @@ static void run_steps(const NsCall& q, const NsPlan& p, const StepScales& s, cha
 
 template <bool MUON>
 static tgs_status ns_run(const NsCall& q, const NsPlan& p, const StepScales& s, void* workspace, hipStream_t stream) {
-  if (p.small) {
-    small_run(q, s, workspace, stream);
+  if (p.small || p.lds) {
+    if (p.small) small_run(q, s, workspace, stream);
+    else lds_run(q, s, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(TGS_EHIP, "%s: launch failed: %s", q.what, hipGetErrorString(e));
     return TGS_OK;

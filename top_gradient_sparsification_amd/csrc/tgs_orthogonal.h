@@ -10,6 +10,7 @@
 namespace tgs {
 
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxSteps = 64;
 
@@ -39,6 +40,19 @@ __device__ __forceinline__ void split_half(float v, _Float16& h, _Float16& l) {
   l = (_Float16)(v - (float)h);
 }
 
+// Eight columns of this lane's row by two transposing LDS reads of four: of 16
+// lanes, lane s addresses rows 4 (s % 4).. of column s / 4 and gets row s.
+__device__ __forceinline__ h8 columns8(const _Float16* first, const _Float16* second) {
+  typedef __attribute__((address_space(3))) s4* Lds;
+  union {
+    s4 s[2];
+    h8 h;
+  } u;
+  u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)first);
+  u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)second);
+  return u.h;
+}
+
 // The new momentum, and the value that is orthogonalised.
 __device__ __forceinline__ float new_momentum(float beta, float m, float g) { return fmaf(beta, m, g); }
 __device__ __forceinline__ float muon_u(int nesterov, float beta, float g, float m) {
@@ -60,5 +74,10 @@ void launch_norm(const NsCall& q, double* part, int blocks, hipStream_t stream);
 constexpr int kSmallSide = 64;
 size_t small_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
 void small_run(const NsCall& q, const StepScales& s, void* workspace, hipStream_t stream);
+
+
+// The route for matrices that one workgroup holds in LDS.
+bool lds_holds(int64_t rows, int64_t cols, bool split);
+void lds_run(const NsCall& q, const StepScales& s, hipStream_t stream);
 
 }  // namespace tgs
