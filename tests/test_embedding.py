@@ -121,7 +121,7 @@ def test_refusals_of_each():
     assert grad_call(lib, grad=None) == EINVAL
     assert grad_call(lib, gt=3) == EINVAL
     need = lib.tgs_embedding_grad_workspace_bytes(16, 100, 8, 0, 0)
-    assert need > 32768
+    assert need >= 32768
     assert grad_call(lib, wsn=need - 1) == EWORKSPACE
     assert grad_call(lib, out=0xA000000 + 64) == EINVAL
     for bad in ((-1, 10, 8, 0, 0), (10, 0, 8, 0, 0), (10, 10, 0, 0, 0), (10, 10, 8, 3, 0), (10, 10, 8, 0, 4),
@@ -279,6 +279,47 @@ def test_grad_sizes(tgs_gpu, T, V, D, masked):
     got = tgs_gpu.embedding_grad(tokens.cuda(), grad.cuda(), V, ws=ws)
     tgs_gpu.check_device_error(ws)
     assert_grad(got, tokens, grad, V, 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,D,masked", [
+    (33, 1, 5, 0.0), (32, 1, 64, 0.0), (2048, 1, 9, 0.3), (2048, 3, 300, 0.0),      # rows that one wave or eight add
+    (1024, 1001, 257, 0.05), (513, 2047, 4, 0.9), (2047, 10_000, 16, 0.1),          # one launch
+    (1024, 128_000, 16, 0.0), (512, 128_000, 130, 0.5),
+    (1025, 128_000, 130, 0.0), (2049, 100, 33, 0.1), (700, 1001, 4096, 0.1)])       # sorted
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grad_of_few_places(tgs_gpu, T, V, D, masked, accumulate):
+    rng = np.random.default_rng(T + V)
+    tokens = make_tokens(T, V, masked, torch.int32, rng)
+    grad = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).bfloat16()
+    base = torch.from_numpy(rng.standard_normal((V, D)).astype(np.float32)) if accumulate else None
+    out = base.cuda() if accumulate else torch.full((V, D), float("nan"), device="cuda")
+    dev = tokens.cuda()
+    assert tgs_gpu.embedding_grad(dev, grad.cuda(), V, scale=0.37, out=out, accumulate=accumulate) is out
+    assert_grad(out, tokens, grad, V, 0.37, base)
+    if not accumulate:
+        assert torch.equal(tgs_gpu.embedding_grad(dev, grad.cuda(), V, scale=0.37), out)
+
+
+@pytest.mark.gpu
+def test_wide_vectors_and_streaming_stores(tgs_gpu):
+    """Sizes that take eight 16-bit gradients a lane, and results larger than the caches; the oracle runs on the GPU."""
+    T, V, D = 70_001, 3_000, 2_003
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    tokens = torch.randint(-100, V, (T,), device="cuda", generator=gen)
+    grad = torch.randn(T, D, device="cuda", generator=gen).bfloat16()
+    real = tokens >= 0
+    total = torch.zeros(V, D, dtype=torch.float64, device="cuda")
+    size, count = torch.zeros_like(total), torch.bincount(tokens[real], minlength=V).double()[:, None]
+    total.index_add_(0, tokens[real], grad[real].double())
+    size.index_add_(0, tokens[real], grad[real].double().abs())
+    got = tgs_gpu.embedding_grad(tokens, grad, V)
+    assert ((got.double() - total).abs() <= size * (count + 8) * U * 1.01 + total.abs() * U).all()
+    for table_dtype in (torch.float32, torch.bfloat16):
+        table = torch.randn(V, D, device="cuda", generator=gen).to(table_dtype)
+        rows = tgs_gpu.embedding_lookup(tokens, table)
+        want = torch.where(real[:, None], table[tokens.clamp(min=0)], 0.0)
+        assert torch.equal(rows, want)
 
 
 @pytest.mark.gpu

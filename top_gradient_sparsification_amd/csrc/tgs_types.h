@@ -59,6 +59,23 @@ __device__ __forceinline__ Vec<T, E> load_vec(const T* p) { return *(const Vec<T
 template <class T, int E>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, E>& x) { *(Vec<T, E>*)p = x; }
 
+// The same store with the non-temporal hint, for arrays larger than the caches.
+template <class T, int E>
+struct VecWords {
+  typedef u32 type __attribute__((ext_vector_type(sizeof(T) * E / 4), aligned(sizeof(T))));
+};
+
+template <class T, int E>
+__device__ __forceinline__ void store_vec_streaming(T* p, const Vec<T, E>& x) {
+  if constexpr (sizeof(T) * E >= 8) {
+    typename VecWords<T, E>::type w;
+    __builtin_memcpy(&w, &x, sizeof(x));
+    __builtin_nontemporal_store(w, (typename VecWords<T, E>::type*)p);
+  } else {
+    store_vec<T, E>(p, x);
+  }
+}
+
 // Calls f with a null pointer of the element type for a dtype code.
 template <class F>
 inline void with_float_dtype(tgs_dtype t, F&& f) {
