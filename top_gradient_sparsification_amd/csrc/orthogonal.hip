@@ -163,6 +163,20 @@ __global__ __launch_bounds__(256) void k_ns_pack(PackArgs a) {
     const int64_t i = (((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
     if (i < a.arrive) a.arrived[i] = 0;
   }
+  // rows and columns of x's own order
+  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
+  // all of a thread's loads in flight at once: outside the matrix they read its
+  // first entry
+  T in[16];
+  float in_m[MUON ? 16 : 1];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = r0 + ty + 4 * i, c = c0 + tx;
+    const int64_t at = r < a.rows && c < a.cols ? (int64_t)r * a.cols + c : 0;
+    in[i] = x[at];
+    if (MUON) in_m[i] = mom[at];
+  }
   // every workgroup adds the partial sums itself, in the same order
   __shared__ double s_sum[4];
   double sum = 0.0;
@@ -173,19 +187,12 @@ __global__ __launch_bounds__(256) void k_ns_pack(PackArgs a) {
   __syncthreads();
   sum = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
   const double inv = 1.0 / (sqrt(sum) + a.eps);
-  // rows and columns of x's own order
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
-#pragma unroll 4
-  for (int i = ty; i < 64; i += 4) {
-    const int r = r0 + i, c = c0 + tx;
-    float v = 0.0f;
-    if (r < a.rows && c < a.cols) {
-      v = to_f32(x[(int64_t)r * a.cols + c]);
-      if (MUON) v = muon_u(a.nesterov, a.beta, v, mom[(int64_t)r * a.cols + c]);
-      v = (float)((double)v * inv) * a.sx;
-    }
-    s_t[i][tx] = v;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float v = to_f32(in[i]);
+    if (MUON) v = muon_u(a.nesterov, a.beta, v, in_m[i]);
+    v = (float)((double)v * inv) * a.sx;
+    s_t[ty + 4 * i][tx] = r0 + ty + 4 * i < a.rows && c0 + tx < a.cols ? v : 0.0f;
   }
   __syncthreads();
   // in x's order: X, or its transpose where x is tall
@@ -437,6 +444,47 @@ __global__ __launch_bounds__(G::WAVES* kWave, G::EU) void k_ns_product(ProductAr
         }
       }
     };
+    // What the epilogue reads: lane (h, c) holds rows 8 g + 4 h + 0..3 of column c of a
+    // block.  Fetched for 32 rows at once, while the rows before are worked on; for
+    // all rows ahead of the products where there are 32 only.
+    constexpr bool EARLY = MI == 1;
+    const int h = hi, c32 = i32;
+    const int row0 = tm * B + l_row, col0 = tn * B + r_row;
+    const float* diag_in = (K == kSquare ? a.diag_a : a.diag_p) + (int64_t)batch * a.mp;
+    const int64_t plane = (int64_t)batch * a.mp * cols_c * PARTS;
+    _Float16* by_row = (K == kGram ? a.e : K == kSquare ? a.p : a.x) + plane;
+    _Float16* by_col = (K == kGram ? a.e : K == kSquare ? a.p : a.t) + plane;
+    f4* xf = (f4*)a.xf + (((int64_t)batch * a.tiles + tm * a.tiles_n + tn) * WAVES + wave) * (MI * NI * 4 * kWave) + lane;
+    f4 x_in[2][NI][4], d_in[2][4];
+    h4 e_in[2][PARTS][NI][4];
+    auto fetch = [&](int mi, int to) {
+      if (K == kGram || row0 + mi * 32 >= a.mp) return;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) d_in[to][g] = *(const f4*)(diag_in + row0 + mi * 32 + 8 * g + 4 * h);
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        if (col0 + ni * 32 >= cols_c) continue;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if constexpr (K == kSquare) {  // E is symmetric: its row `col`
+            const _Float16* from = a.e + plane + place_of<SPLIT>(col0 + ni * 32 + c32, row0 + mi * 32 + 8 * g + 4 * h, a.mp);
+            e_in[to][0][ni][g] = *(const h4*)from;
+            if (SPLIT) e_in[to][PARTS - 1][ni][g] = *(const h4*)(from + kSplitCols);
+          } else {
+            x_in[to][ni][g] = xf[((mi * NI + ni) * 4 + g) * kWave];
+          }
+        }
+      }
+    };
+    float d_col[NI];
+    if constexpr (K == kSquare) {
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        const int col = col0 + ni * 32 + c32;
+        d_col[ni] = col < cols_c ? diag_in[col] : 0.0f;
+      }
+    }
+    if (EARLY) fetch(0, 0);
 #pragma unroll
     for (int i = 0; i < S - 1; ++i)
 #pragma unroll
@@ -525,44 +573,7 @@ __global__ __launch_bounds__(G::WAVES* kWave, G::EU) void k_ns_product(ProductAr
     constexpr int PER = WAVES / (S >= 4 ? 4 : 2);  // strips a stage
     static_assert(PER * STRIP <= STAGE, "the waves' strips fit their stages");
     _Float16* strip = ring(wave / PER) + wave % PER * STRIP;
-    const int h = hi, c32 = i32;
-    const int row0 = tm * B + l_row, col0 = tn * B + r_row;
-    const float* diag_in = (K == kSquare ? a.diag_a : a.diag_p) + (int64_t)batch * a.mp;
-    const int64_t plane = (int64_t)batch * a.mp * cols_c * PARTS;
-    _Float16* by_row = (K == kGram ? a.e : K == kSquare ? a.p : a.x) + plane;
-    _Float16* by_col = (K == kGram ? a.e : K == kSquare ? a.p : a.t) + plane;
-    f4* xf = (f4*)a.xf + (((int64_t)batch * a.tiles + tm * a.tiles_n + tn) * WAVES + wave) * (MI * NI * 4 * kWave) + lane;
-    // fetched for 32 rows at once, while the rows before are worked on
-    f4 x_in[2][NI][4], d_in[2][4];
-    h4 e_in[2][PARTS][NI][4];
-    auto fetch = [&](int mi, int to) {
-      if (K == kGram || row0 + mi * 32 >= a.mp) return;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) d_in[to][g] = *(const f4*)(diag_in + row0 + mi * 32 + 8 * g + 4 * h);
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        if (col0 + ni * 32 >= cols_c) continue;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          if constexpr (K == kSquare) {  // E is symmetric: its row `col`
-            const _Float16* from = a.e + plane + place_of<SPLIT>(col0 + ni * 32 + c32, row0 + mi * 32 + 8 * g + 4 * h, a.mp);
-            e_in[to][0][ni][g] = *(const h4*)from;
-            if (SPLIT) e_in[to][PARTS - 1][ni][g] = *(const h4*)(from + kSplitCols);
-          } else {
-            x_in[to][ni][g] = xf[((mi * NI + ni) * 4 + g) * kWave];
-          }
-        }
-      }
-    };
-    float d_col[NI];
-    if constexpr (K == kSquare) {
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        const int col = col0 + ni * 32 + c32;
-        d_col[ni] = col < cols_c ? diag_in[col] : 0.0f;
-      }
-    }
-    fetch(0, 0);
+    if (!EARLY) fetch(0, 0);
     __syncthreads();
     const float to_stored = a.scale * a.store;  // powers of two
 #pragma unroll
