@@ -287,7 +287,7 @@ tgs_status tgs_embedding_lookup(const void* tokens, tgs_dtype tokens_dtype, int6
 
 /* Bytes of workspace tgs_embedding_grad needs (0 if the sizes or types are
    invalid): 16 bytes a place for the sort, and two partial rows for every 8
-   to 64 places. */
+   to 64 places; the header alone for few places of a small table. */
 size_t tgs_embedding_grad_workspace_bytes(int64_t T, int64_t V, int64_t D, tgs_dtype grad_dtype, tgs_dtype out_dtype);
 
 /*

@@ -19,6 +19,7 @@
 //      binary search in the sorted tokens finds them);
 //   3. k_grad_join: partial rows of tokens that span chunks are added in chunk
 //      order.
+// Few places of a small table take one launch instead (k_grad_few).
 // The order of every sum is fixed by the tokens alone, so results are the same
 // bits on every run.  Sums are fp32.
 #include <type_traits>
