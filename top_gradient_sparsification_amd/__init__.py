@@ -215,6 +215,12 @@ def workspace(kind: str, nbytes: int, device) -> torch.Tensor:
         return buf
 
 
+def _scratch(kind: str, nbytes: int, dev: torch.device, stream: int) -> torch.Tensor:
+    """``workspace`` for a tensor's device and its current stream, without the lock where it is there."""
+    buf = _ws_cache.get((dev.index, stream, kind))
+    return buf if buf is not None and buf.numel() >= nbytes else workspace(kind, nbytes, dev)
+
+
 # --------------------------------------------------------------- operations --
 def topk_workspace_bytes(n: int, k: int) -> int:
     return int(_load().tgs_topk_workspace_bytes(n, k))
@@ -653,16 +659,17 @@ def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1
         out_dtype = out_dtype or table.dtype
         if out_dtype not in _FLOATS:
             raise TypeError("out_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
-        out = torch.empty((*tokens.shape, D), dtype=out_dtype, device=dev)
+        out = table.new_empty((*tokens.shape, D), dtype=out_dtype)
     else:
         _require_any(out, _FLOATS if out_dtype is None else (out_dtype,), "out", dev)
         if out.shape != (*tokens.shape, D):
             raise ValueError("out must have shape %s" % ((*tokens.shape, D),))
+    stream = _stream_handle(dev)
     if ws is None:
-        ws = workspace("embedding", 32768, dev)
+        ws = _scratch("embedding", 32768, dev, stream)
     st = _load().tgs_embedding_lookup(_ptr(tokens), _DTYPES[tokens.dtype], tokens.numel(), _ptr(table),
                                       _DTYPES[table.dtype], V, D, scale, _ptr(out), _DTYPES[out.dtype],
-                                      ws.data_ptr(), ws.numel(), _stream_handle(dev))
+                                      ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_embedding_lookup")
     return out
@@ -696,20 +703,21 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, scal
         out_dtype = out_dtype or torch.float32
         if out_dtype not in _FLOATS:
             raise TypeError("out_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
-        out = torch.empty((V, D), dtype=out_dtype, device=dev)
+        out = grad.new_empty((V, D), dtype=out_dtype)
     else:
         _require_any(out, _FLOATS if out_dtype is None else (out_dtype,), "out", dev)
         if out.shape != (V, D):
             raise ValueError("out must have shape %s" % ((V, D),))
+    stream = _stream_handle(dev)
     lib = _load()
     T, gt, ot = tokens.numel(), _DTYPES[grad.dtype], _DTYPES[out.dtype]
     if ws is None:
         need = lib.tgs_embedding_grad_workspace_bytes(T, V, D, gt, ot)
         if need == 0:
             raise ValueError("invalid sizes T=%d num_rows=%d D=%d" % (T, V, D))
-        ws = workspace("embedding", need, dev)
+        ws = _scratch("embedding", need, dev, stream)
     st = lib.tgs_embedding_grad(_ptr(tokens), _DTYPES[tokens.dtype], T, _ptr(grad), gt, V, D, scale, _ptr(out), ot,
-                                bool(accumulate), ws.data_ptr(), ws.numel(), _stream_handle(dev))
+                                bool(accumulate), ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_embedding_grad")
     return out
@@ -748,16 +756,17 @@ def newton_schulz(x: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ_CO
             raise ValueError("out must have x's shape")
     if x.numel() == 0:
         return out
+    stream = _stream_handle(dev)
     lib = _load()
     dt = _DTYPES[x.dtype]
     if ws is None:
         need = lib.tgs_newton_schulz_workspace_bytes(b, m, n, dt)
         if need == 0:
             raise ValueError("invalid sizes batch=%d rows=%d cols=%d" % (b, m, n))
-        ws = workspace("muon", need, dev)
+        ws = _scratch("muon", need, dev, stream)
     ca, cb, cc = coefficients
     st = lib.tgs_newton_schulz(x.data_ptr(), dt, b, m, n, steps, ca, cb, cc, eps, out.data_ptr(), ws.data_ptr(),
-                               ws.numel(), _stream_handle(dev))
+                               ws.numel(), stream)
     if st:
         _check(st, "tgs_newton_schulz")
     return out
@@ -785,17 +794,18 @@ def muon_step(weight: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, 
         raise ValueError("weight, grad and momentum must have one shape")
     if weight.numel() == 0:
         return weight
+    stream = _stream_handle(dev)
     lib = _load()
     wt = _DTYPES[weight.dtype]
     if ws is None:
         need = lib.tgs_muon_workspace_bytes(b, m, n, wt)
         if need == 0:
             raise ValueError("invalid sizes batch=%d rows=%d cols=%d" % (b, m, n))
-        ws = workspace("muon", need, dev)
+        ws = _scratch("muon", need, dev, stream)
     ca, cb, cc = coefficients
     st = lib.tgs_muon_step(weight.data_ptr(), wt, grad.data_ptr(), _DTYPES[grad.dtype], momentum.data_ptr(), b, m, n,
                            lr, beta, bool(nesterov), weight_decay, steps, ca, cb, cc, eps, ws.data_ptr(), ws.numel(),
-                           _stream_handle(dev))
+                           stream)
     if st:
         _check(st, "tgs_muon_step")
     return weight
