@@ -24,18 +24,20 @@
 // take 253 tiles of 192 in 85 us rather than 136 of 256, which leave half the
 // device idle, in 120.  Few tiles with long sums are shared by workgroups (the
 // gram of 200 x 8,000 in fp32: 59 -> 28 us).
+// Tiles of 64 and 128 are bound by the rate at which a compute unit fills its
+// LDS, about 65 GB/s: 1,000 x 1,533 in fp32 takes 13 to 21 us a product.
 //
 // What is rounded.  The diagonals of A and P are large against the rest near
 // the end (A tends to the identity), so they are held apart in fp32 and the
 // products see only the off-diagonal part E of A and of P:
 //   A = D + E:   A^2 = D^2 + (d_i + d_j) E + E^2,   P X = D_P X + E_P X.
 // X itself is held in fp32, in the order of the update's registers, and a + D_P
-// multiplies that; the operands are fp16.  With results of 16 bits the products read the high parts only: the
-// result is then 2e-4 to 7e-4 (2-norm) off, below the 1.7e-3 of the final
-// rounding, where rounding X, A and P whole gives 1.6e-3 to 3e-3 (fp16) and
-// 1.3e-2 to 2.4e-2 (bf16).  With fp32 results every operand is high + low and
-// a product is three (high low + low high + high high): as exact as fp32
-// products (1.4e-6 to 2.3e-6 against 1.3e-6 to 2.0e-6).
+// multiplies that; the operands are fp16.  With results of 16 bits the products
+// read high parts only: the result is then 2e-4 to 7e-4 (2-norm) off, below the
+// 1.7e-3 of the final rounding, where rounding X, A and P whole gives 1.6e-3 to
+// 3e-3 (fp16) and 1.3e-2 to 2.4e-2 (bf16).  With fp32 results every operand is
+// high + low and a product is three (high low + low high + high high): as exact
+// as fp32 products (1.4e-6 to 2.3e-6 against 1.3e-6 to 2.0e-6).
 //
 // Range.  The singular values of X start in [0, 1]; the host bounds them after
 // every step by the polynomial's extrema, and scales X, A and P by powers of
