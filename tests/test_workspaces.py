@@ -1,0 +1,79 @@
+"""The binding's own workspaces: which calls share one."""
+import threading
+
+import pytest
+import torch
+
+
+def in_threads(n, f):
+    """[f(0), .., f(n - 1)], each in a thread of its own, all alive at once."""
+    out, errors = [None] * n, []
+    gate = threading.Barrier(n)
+
+    def run(i):
+        try:
+            gate.wait(60)
+            out[i] = f(i)
+            gate.wait(60)
+        except Exception as e:  # noqa: BLE001 - reported below
+            errors.append(e)
+            gate.abort()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    return out
+
+
+# ------------------------------------------------------------------- CPU --
+@pytest.fixture
+def tgs_cpu(monkeypatch):
+    """The binding with every tensor's stream taken to be one and the same."""
+    import top_gradient_sparsification_amd as tgs
+    monkeypatch.setattr(tgs, "_stream_handle", lambda device: 7)
+    return tgs
+
+
+def test_threads_on_one_stream_have_workspaces_of_their_own(tgs_cpu):
+    cpu = torch.device("cpu")
+    for get in (lambda i: tgs_cpu.workspace("threads", 1000, cpu),
+                lambda i: tgs_cpu._scratch("threads", 1000, cpu, 7)):
+        a, b = in_threads(2, get)
+        assert a.numel() >= 1000 and b.numel() >= 1000 and a.data_ptr() != b.data_ptr()
+    here = tgs_cpu.workspace("threads", 1000, cpu)
+    assert tgs_cpu._scratch("threads", 900, cpu, 7) is here and tgs_cpu.workspace("threads", 1000, cpu) is here
+    assert tgs_cpu.workspace("threads", 2000, cpu) is not here  # it grows
+    assert not here.any()
+
+
+# ------------------------------------------------------------------- GPU --
+@pytest.mark.gpu
+def test_two_threads_on_one_stream_get_what_one_gets(tgs_gpu):
+    """Sequences of launches, enqueued by two threads at once on the stream they share."""
+    T, V, D, rounds = 20_000, 3_000, 64, 25
+
+    def inputs(i):
+        gen = torch.Generator(device="cuda").manual_seed(i)
+        return (torch.randint(-1, V, (T,), device="cuda", generator=gen), torch.randn(T, D, device="cuda", generator=gen),
+                torch.randn(200, 300, device="cuda", generator=gen), torch.randn(60, 700, device="cuda", generator=gen))
+
+    def work(given):
+        tokens, grad, wide, small = given
+        weight, momentum = wide.clone(), torch.zeros_like(wide)
+        for _ in range(rounds):
+            tgs_gpu.muon_step(weight, wide, momentum, lr=0.1)
+            g = tgs_gpu.embedding_grad(tokens, grad, V)
+            o = tgs_gpu.newton_schulz(small)
+        return weight, momentum, g, o
+
+    given = [inputs(i) for i in range(2)]
+    want = [work(x) for x in given]
+    torch.cuda.synchronize()
+    got = in_threads(2, lambda i: work(given[i]))
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)

@@ -197,27 +197,34 @@ def _require(t, dtype, name, device=None, min_numel=None):
 
 
 # --------------------------------------------------------------- workspaces --
-_ws_cache: dict = {}
-_ws_lock = threading.Lock()
+class _Workspaces(threading.local):
+    """Each thread's own: a call enqueues a sequence of launches with the
+    interpreter's lock let go, so what two threads enqueue on one stream can
+    stand there mixed, and stream order alone does not keep them apart."""
+
+    def __init__(self):
+        self.buffers: dict = {}
+
+
+_ws_cache = _Workspaces()
 
 
 def workspace(kind: str, nbytes: int, device) -> torch.Tensor:
     """A zero-initialised (hence ready) uint8 device buffer of at least
-    ``nbytes``, cached per (device, current stream, kind).  Calls that share it
-    are ordered on that stream."""
+    ``nbytes``, cached per (thread, device, current stream, kind).  Calls that
+    share it come from one thread and are ordered on that stream."""
     dev = torch.device(device)
     key = (dev.index, _stream_handle(dev), kind)
-    with _ws_lock:
-        buf = _ws_cache.get(key)
-        if buf is None or buf.numel() < nbytes:
-            buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
-            _ws_cache[key] = buf
-        return buf
+    buf = _ws_cache.buffers.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        _ws_cache.buffers[key] = buf
+    return buf
 
 
 def _scratch(kind: str, nbytes: int, dev: torch.device, stream: int) -> torch.Tensor:
-    """``workspace`` for a tensor's device and its current stream, without the lock where it is there."""
-    buf = _ws_cache.get((dev.index, stream, kind))
+    """``workspace`` for a tensor's device and its current stream."""
+    buf = _ws_cache.buffers.get((dev.index, stream, kind))
     return buf if buf is not None and buf.numel() >= nbytes else workspace(kind, nbytes, dev)
 
 
