@@ -31,9 +31,10 @@ def in_threads(n, f):
 # ------------------------------------------------------------------- CPU --
 @pytest.fixture
 def tgs_cpu(monkeypatch):
-    """The binding with every tensor's stream taken to be one and the same."""
+    """The binding with every tensor's stream taken to be one and the same, and not captured."""
     import top_gradient_sparsification_amd as tgs
     monkeypatch.setattr(tgs, "_stream_handle", lambda device: 7)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return tgs
 
 
@@ -47,6 +48,20 @@ def test_threads_on_one_stream_have_workspaces_of_their_own(tgs_cpu):
     assert tgs_cpu._scratch("threads", 900, cpu, 7) is here and tgs_cpu.workspace("threads", 1000, cpu) is here
     assert tgs_cpu.workspace("threads", 2000, cpu) is not here  # it grows
     assert not here.any()
+
+
+def test_a_call_under_capture_leaves_the_kept_workspace_alone(tgs_cpu, monkeypatch):
+    """A graph writes to its workspace at every replay: one that a larger call
+    later replaces, and frees, must not be it."""
+    cpu = torch.device("cpu")
+    kept = tgs_cpu.workspace("capture", 40_000, cpu)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    for get in (lambda: tgs_cpu.workspace("capture", 40_000, cpu), lambda: tgs_cpu._scratch("capture", 40_000, cpu, 7)):
+        buf = get()
+        assert buf.data_ptr() != kept.data_ptr() and buf.numel() >= 40_000 and not buf[:32768].any()
+        assert get() is not buf
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    assert tgs_cpu.workspace("capture", 40_000, cpu) is kept
 
 
 # ------------------------------------------------------------------- GPU --
@@ -77,3 +92,37 @@ def test_two_threads_on_one_stream_get_what_one_gets(tgs_gpu):
     for a, b in zip(want, got):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_a_graph_outlives_the_workspace_of_its_stream(tgs_gpu):
+    """Captured on the stream that was warmed up, without a workspace of the
+    caller's; then a larger call there replaces the stream's own."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(300, 400, device="cuda", generator=gen)
+    tokens = torch.randint(0, 900, (9_000,), device="cuda", generator=gen)
+    grad = torch.randn(9_000, 40, device="cuda", generator=gen)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        o, g = tgs_gpu.newton_schulz(x), tgs_gpu.embedding_grad(tokens, grad, 900)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        tgs_gpu.newton_schulz(x, out=o)
+        tgs_gpu.embedding_grad(tokens, grad, 900, out=g)
+    with torch.cuda.stream(stream):
+        tgs_gpu.newton_schulz(torch.randn(900, 1300, device="cuda", generator=gen))
+        tgs_gpu.embedding_grad(torch.randint(0, 900, (200_000,), device="cuda", generator=gen),
+                               torch.randn(200_000, 40, device="cuda", generator=gen), 900)
+        others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in [1 << 16, 1 << 20, 1 << 22] * 20]
+    stream.synchronize()
+    for seed in (4, 5, 6):
+        gen.manual_seed(seed)
+        x.normal_(generator=gen)
+        grad.normal_(generator=gen)
+        with torch.cuda.stream(stream):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, tgs_gpu.newton_schulz(x)) and torch.equal(g, tgs_gpu.embedding_grad(tokens, grad, 900))
+        assert all(bool((t == 7).all()) for t in others)

@@ -209,11 +209,22 @@ class _Workspaces(threading.local):
 _ws_cache = _Workspaces()
 
 
+_HEADER_BYTES = 32768  # of a workspace; the rest is scratch
+
+
 def workspace(kind: str, nbytes: int, device) -> torch.Tensor:
     """A zero-initialised (hence ready) uint8 device buffer of at least
     ``nbytes``, cached per (thread, device, current stream, kind).  Calls that
-    share it come from one thread and are ordered on that stream."""
+    share it come from one thread and are ordered on that stream.
+
+    While the current stream is being captured it is a buffer of its own, of
+    the graph's memory, its header cleared by the graph: a cached one may be
+    replaced by a larger one, and the graph would write to freed memory."""
     dev = torch.device(device)
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        buf[:_HEADER_BYTES].zero_()
+        return buf
     key = (dev.index, _stream_handle(dev), kind)
     buf = _ws_cache.buffers.get(key)
     if buf is None or buf.numel() < nbytes:
@@ -225,7 +236,9 @@ def workspace(kind: str, nbytes: int, device) -> torch.Tensor:
 def _scratch(kind: str, nbytes: int, dev: torch.device, stream: int) -> torch.Tensor:
     """``workspace`` for a tensor's device and its current stream."""
     buf = _ws_cache.buffers.get((dev.index, stream, kind))
-    return buf if buf is not None and buf.numel() >= nbytes else workspace(kind, nbytes, dev)
+    if buf is None or buf.numel() < nbytes or torch.cuda.is_current_stream_capturing():
+        return workspace(kind, nbytes, dev)
+    return buf
 
 
 # --------------------------------------------------------------- operations --
