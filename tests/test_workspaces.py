@@ -64,6 +64,15 @@ def test_a_call_under_capture_leaves_the_kept_workspace_alone(tgs_cpu, monkeypat
     assert tgs_cpu.workspace("capture", 40_000, cpu) is kept
 
 
+def test_a_workspace_on_another_device_is_refused(tgs_cpu):
+    with pytest.raises(ValueError, match="ws is on cpu, expected cuda:0"):
+        tgs_cpu._require_ws(torch.zeros(32768, dtype=torch.uint8), torch.device("cuda", 0))
+    with pytest.raises(TypeError, match="ws"):
+        tgs_cpu._require_ws(b"0" * 32768, torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="contiguous"):
+        tgs_cpu._require_ws(torch.zeros(9, 9)[:, 0], torch.device("cpu"))
+
+
 # ------------------------------------------------------------------- GPU --
 @pytest.mark.gpu
 def test_two_threads_on_one_stream_get_what_one_gets(tgs_gpu):
@@ -126,3 +135,23 @@ def test_a_graph_outlives_the_workspace_of_its_stream(tgs_gpu):
         torch.cuda.synchronize()
         assert torch.equal(o, tgs_gpu.newton_schulz(x)) and torch.equal(g, tgs_gpu.embedding_grad(tokens, grad, 900))
         assert all(bool((t == 7).all()) for t in others)
+
+
+@pytest.mark.gpu
+def test_every_call_refuses_a_workspace_in_host_memory(tgs_gpu):
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    ids, x, v = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.ones(4, 8, device="cuda"), torch.ones(64, device="cuda")
+    lam = torch.ones(1, device="cuda")
+    for call in (lambda: tgs_gpu.embedding_lookup(ids, x, ws=ws), lambda: tgs_gpu.embedding_grad(ids, x, 4, ws=ws),
+                 lambda: tgs_gpu.newton_schulz(x, ws=ws), lambda: tgs_gpu.muon_step(x, x.clone(), x.clone(), lr=0.1, ws=ws),
+                 lambda: tgs_gpu.topk_ef_step(v, v.clone(), 3, ws=ws),
+                 lambda: tgs_gpu.topk_ef_step_segmented(v, v.clone(), [0, 64], [3], ws=ws),
+                 lambda: tgs_gpu.threshold_ef_step(v, v.clone(), 0.5, 64, ws=ws),
+                 lambda: tgs_gpu.threshold_ef_step_dev(v, v.clone(), lam, 64, ws=ws),
+                 lambda: tgs_gpu.threshold_estimate(v, v.clone(), ids, 1, ws=ws),
+                 lambda: tgs_gpu.estimated_threshold_ef_step(v, v.clone(), ids, 1, 64, ws=ws),
+                 lambda: tgs_gpu.rtopk_ef_step(v, v.clone(), 8, 3, 1, 1, ws=ws),
+                 lambda: tgs_gpu.gtopk_merge(ids[:3].view(1, 3), v[:3].view(1, 3), 64, ws=ws)):
+        with pytest.raises(ValueError, match="ws is on cpu"):
+            call()
+    assert x.eq(1).all() and v.eq(1).all()

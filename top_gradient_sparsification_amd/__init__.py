@@ -196,6 +196,16 @@ def _require(t, dtype, name, device=None, min_numel=None):
         raise ValueError("%s holds %d entries, needs %d" % (name, t.numel(), min_numel))
 
 
+def _require_ws(ws, dev):
+    """A workspace of the caller's: kernels write to it, so host memory or another device's is refused."""
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a torch.Tensor")
+    if ws.device != dev:
+        raise ValueError("ws is on %s, expected %s" % (ws.device, dev))
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+
+
 # --------------------------------------------------------------- workspaces --
 class _Workspaces(threading.local):
     """Each thread's own: a call enqueues a sequence of launches with the
@@ -275,6 +285,8 @@ def topk_ef_step(grad: torch.Tensor, residual: torch.Tensor, k: int, out_idx=Non
         raise ValueError("invalid sizes n=%d k=%d" % (n, k))
     if ws is None:
         ws = workspace("topk", need, dev)
+    else:
+        _require_ws(ws, dev)
     st = lib.tgs_topk_ef_step(_ptr(grad), _ptr(residual), n, k, _ptr(out_idx), _ptr(out_val), ws.data_ptr(),
                               ws.numel(), _stream_handle(dev))
     _check(st, "tgs_topk_ef_step")
@@ -389,6 +401,8 @@ def topk_ef_step_segmented(grad: torch.Tensor, residual: torch.Tensor, offsets, 
         raise ValueError("invalid segment table")
     if ws is None:
         ws = workspace("topk", need, dev)
+    else:
+        _require_ws(ws, dev)
     st = lib.tgs_topk_ef_step_segmented(_ptr(grad), _ptr(residual), nseg, offs.ctypes.data, kk.ctypes.data,
                                         _ptr(out_idx), _ptr(out_val), ws.data_ptr(), ws.numel(), _stream_handle(dev))
     _check(st, "tgs_topk_ef_step_segmented")
@@ -476,6 +490,8 @@ def threshold_ef_step(grad: torch.Tensor, residual: torch.Tensor, lam: float, ca
         raise ValueError("invalid size n=%d" % n)
     if ws is None:
         ws = workspace("threshold", need, dev)
+    else:
+        _require_ws(ws, dev)
     st = lib.tgs_threshold_ef_step(_ptr(grad), _ptr(residual), n, ctypes.c_float(lam), _ptr(out_idx),
                                    _ptr(out_val), capacity, count.data_ptr(), ws.data_ptr(), ws.numel(),
                                    _stream_handle(dev))
@@ -508,6 +524,8 @@ def threshold_estimate(grad: torch.Tensor, residual: torch.Tensor, sample_idx: t
         raise ValueError("invalid sample count m=%d" % m)
     if ws is None:
         ws = workspace("estimate", need, dev)
+    else:
+        _require_ws(ws, dev)
     st = lib.tgs_threshold_estimate(_ptr(grad), _ptr(residual), n, _ptr(sample_idx), m, int(q), d_lambda.data_ptr(),
                                     ws.data_ptr(), ws.numel(), _stream_handle(dev))
     _check(st, "tgs_threshold_estimate")
@@ -543,6 +561,8 @@ def threshold_ef_step_dev(grad: torch.Tensor, residual: torch.Tensor, d_lambda: 
         raise ValueError("invalid size n=%d" % n)
     if ws is None:
         ws = workspace("threshold", need, dev)
+    else:
+        _require_ws(ws, dev)
     st = lib.tgs_threshold_ef_step_dev(_ptr(grad), _ptr(residual), n, d_lambda.data_ptr(), _ptr(out_idx),
                                        _ptr(out_val), capacity, count.data_ptr(), ws.data_ptr(), ws.numel(),
                                        _stream_handle(dev))
@@ -561,6 +581,8 @@ def estimated_threshold_ef_step(grad: torch.Tensor, residual: torch.Tensor, samp
     if ws is None:
         need = max(threshold_estimate_workspace_bytes(m), threshold_workspace_bytes(n))
         ws = workspace("threshold", need, grad.device)
+    else:
+        _require_ws(ws, grad.device)
     d_lambda = threshold_estimate(grad, residual, sample_idx, q, d_lambda=d_lambda, ws=ws)
     idx, val, cnt = threshold_ef_step_dev(grad, residual, d_lambda, capacity, out_idx=out_idx, out_val=out_val,
                                           count=count, ws=ws)
@@ -596,6 +618,8 @@ def rtopk_ef_step(grad: torch.Tensor, residual: torch.Tensor, r: int, k: int, se
         raise ValueError("invalid sizes n=%d r=%d k=%d" % (n, r, k))
     if ws is None:
         ws = workspace("rtopk", need, dev)
+    else:
+        _require_ws(ws, dev)
     st = lib.tgs_rtopk_ef_step(_ptr(grad), _ptr(residual), n, r, k, int(seed) & (2**64 - 1), int(step) & (2**64 - 1),
                                _ptr(out_idx), _ptr(out_val), ws.data_ptr(), ws.numel(), _stream_handle(dev))
     _check(st, "tgs_rtopk_ef_step")
@@ -629,6 +653,8 @@ def gtopk_merge(idx: torch.Tensor, val: torch.Tensor, n: int, ws: torch.Tensor |
         raise ValueError("invalid sizes P=%d k=%d n=%d" % (P, k, n))
     if ws is None:
         ws = workspace("gtopk", need, dev)
+    else:
+        _require_ws(ws, dev)
     st = lib.tgs_gtopk_merge(_ptr(idx), _ptr(val), P, k, n, _ptr(out_idx), _ptr(out_val), _ptr(mask),
                              ws.data_ptr(), ws.numel(), _stream_handle(dev))
     _check(st, "tgs_gtopk_merge")
@@ -687,6 +713,8 @@ def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1
     stream = _stream_handle(dev)
     if ws is None:
         ws = _scratch("embedding", 32768, dev, stream)
+    else:
+        _require_ws(ws, dev)
     st = _load().tgs_embedding_lookup(_ptr(tokens), _DTYPES[tokens.dtype], tokens.numel(), _ptr(table),
                                       _DTYPES[table.dtype], V, D, scale, _ptr(out), _DTYPES[out.dtype],
                                       ws.data_ptr(), ws.numel(), stream)
@@ -736,6 +764,8 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, scal
         if need == 0:
             raise ValueError("invalid sizes T=%d num_rows=%d D=%d" % (T, V, D))
         ws = _scratch("embedding", need, dev, stream)
+    else:
+        _require_ws(ws, dev)
     st = lib.tgs_embedding_grad(_ptr(tokens), _DTYPES[tokens.dtype], T, _ptr(grad), gt, V, D, scale, _ptr(out), ot,
                                 bool(accumulate), ws.data_ptr(), ws.numel(), stream)
     if st:
@@ -784,6 +814,8 @@ def newton_schulz(x: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ_CO
         if need == 0:
             raise ValueError("invalid sizes batch=%d rows=%d cols=%d" % (b, m, n))
         ws = _scratch("muon", need, dev, stream)
+    else:
+        _require_ws(ws, dev)
     ca, cb, cc = coefficients
     st = lib.tgs_newton_schulz(x.data_ptr(), dt, b, m, n, steps, ca, cb, cc, eps, out.data_ptr(), ws.data_ptr(),
                                ws.numel(), stream)
@@ -822,6 +854,8 @@ def muon_step(weight: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, 
         if need == 0:
             raise ValueError("invalid sizes batch=%d rows=%d cols=%d" % (b, m, n))
         ws = _scratch("muon", need, dev, stream)
+    else:
+        _require_ws(ws, dev)
     ca, cb, cc = coefficients
     st = lib.tgs_muon_step(weight.data_ptr(), wt, grad.data_ptr(), _DTYPES[grad.dtype], momentum.data_ptr(), b, m, n,
                            lr, beta, bool(nesterov), weight_decay, steps, ca, cb, cc, eps, ws.data_ptr(), ws.numel(),
