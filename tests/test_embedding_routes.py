@@ -1,0 +1,34 @@
+"""The embedding gradient's two routes, few places in one launch and many by a
+sort, held to the same results."""
+import pytest
+import torch
+
+from test_embedding import EINVAL, abi, grad_call, lookup_call
+
+def needs(tgs, T, V, D, grad_dtype, out_dtype):
+    return tgs.embedding_grad_workspace_bytes(T, V, D, grad_dtype, out_dtype)
+
+
+def test_more_threads_than_a_launch_may_have_are_refused():
+    """2^24 workgroups of 256 make 2^32 threads: refused before anything is enqueued."""
+    lib, far = abi(), dict(tokens=1 << 44, out=3 << 44, ws=5 << 44, wsn=1 << 50)
+    assert lookup_call(lib, table=2 << 44, T=2**31 - 1, D=64, **far) == EINVAL
+    assert b"too large" in lib.tgs_last_error()
+    assert grad_call(lib, grad=2 << 44, T=2**31 - 1, D=1024, **far) == EINVAL
+    assert b"too large" in lib.tgs_last_error()
+
+
+@pytest.mark.gpu
+def test_more_sums_to_join_than_workgroups(tgs_gpu):
+    """Over 2^30 places of one column: the kernel that joins partial sums has more of them than a launch has
+    workgroups of 256.  All sums are counts below 2^24, so exact."""
+    T, V, part = (1 << 30) + 12_345, 1 << 20, 1 << 26
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    tokens = torch.randint(0, V, (T,), device="cuda", dtype=torch.int32, generator=gen)
+    want = torch.zeros(V, dtype=torch.int64, device="cuda")
+    for t in tokens.split(part):
+        want += torch.bincount(t, minlength=V)
+    grad = torch.ones(T, 1, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(needs(tgs_gpu, T, V, 1, torch.bfloat16, torch.float32), dtype=torch.uint8, device="cuda")
+    got = tgs_gpu.embedding_grad(tokens, grad, V, ws=ws)
+    assert torch.equal(got[:, 0].long(), want)

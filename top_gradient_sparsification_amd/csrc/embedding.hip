@@ -313,6 +313,7 @@ struct GradArgs {
   u32 chunk;  // places a chunk
   u32 chunks;
   u64 waves;       // chunks * slabs
+  u32 join0;       // first of a launch's (chunk, slab) pairs to join
   u32 fill_rows;   // rows a zero-filling wave looks at
   float scale;
   int accumulate;
@@ -450,7 +451,7 @@ __global__ __launch_bounds__(kGradThreads) void k_grad_chunks(GradArgs a) {
 template <class TO, int E>
 __global__ __launch_bounds__(kGradThreads) void k_grad_join(GradArgs a) {
   __shared__ float s_sum[kGradWaves][kWave][E];
-  const u32 slab = blockIdx.x % a.slabs, chunk = blockIdx.x / a.slabs;
+  const u32 id = a.join0 + blockIdx.x, slab = id % a.slabs, chunk = id / a.slabs;
   const u64 end = (u64)(chunk + 1) * a.chunk;  // chunk + 1 < chunks, so end < T
   const u32 key = a.keys[end - 1];
   if (key == a.V || a.keys[end] != key) return;
@@ -624,6 +625,10 @@ __global__ __launch_bounds__(kFewThreads) void k_grad_few(FewArgs a) {
 }
 
 // ------------------------------------------------------------------ host --
+// A launch of 2^32 threads or more is refused by the runtime, after what came
+// before it is enqueued.
+static u64 most_blocks(int threads) { return 0xFFFFFFFFull / threads; }
+
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Elements a lane moves at once: 16 bytes of the wider type; single elements
@@ -767,7 +772,7 @@ extern "C" tgs_status tgs_embedding_lookup(const void* tokens, tgs_dtype tokens_
   a.total = (u64)T * a.nv;
   a.scale = scale;
   const u64 blocks = (a.total + kLookupThreads * kLookupUnroll - 1) / (kLookupThreads * kLookupUnroll);
-  if (blocks > INT32_MAX) return fail(TGS_EINVAL, "%s: T * D too large", what);
+  if (blocks > most_blocks(kLookupThreads)) return fail(TGS_EINVAL, "%s: T * D too large", what);
   with_token_dtype(tokens_dtype, [&](auto* i) {
     with_float_dtype(table_dtype, [&](auto* ti) {
       with_float_dtype(out_dtype, [&](auto* to) {
@@ -865,8 +870,9 @@ extern "C" tgs_status tgs_embedding_grad(const void* tokens, tgs_dtype tokens_dt
   a.accumulate = accumulate != 0;
   const u64 fill = accumulate ? 0 : ((u64)V + a.fill_rows - 1) / a.fill_rows;
   const u64 blocks = (a.waves + fill + kGradWaves - 1) / kGradWaves;
-  const u64 joins = p.chunks > 1 ? (u64)(p.chunks - 1) * p.slabs : 0;
-  if (blocks > INT32_MAX || joins > INT32_MAX) return fail(TGS_EINVAL, "%s: T * D or V * D too large", what);
+  if (blocks > most_blocks(kGradThreads)) return fail(TGS_EINVAL, "%s: T * D or V * D too large", what);
+  // a workgroup each, four times as many as chunk workgroups: past 2^30 places in several launches
+  const u32 joins = p.chunks > 1 ? (p.chunks - 1) * p.slabs : 0;
   SortArgs s{};
   s.tokens = tokens;
   s.hist = (u32*)(ws + p.hist);
@@ -912,7 +918,11 @@ extern "C" tgs_status tgs_embedding_grad(const void* tokens, tgs_dtype tokens_dt
       auto launch = [&](auto width) {
         constexpr int E = decltype(width)::value;
         hipLaunchKernelGGL((k_grad_chunks<TG, TO, E>), dim3((u32)blocks), dim3(kGradThreads), 0, stream, a);
-        if (joins) hipLaunchKernelGGL((k_grad_join<TO, E>), dim3((u32)joins), dim3(kGradThreads), 0, stream, a);
+        for (a.join0 = 0; a.join0 < joins;) {
+          const u32 n = (u32)std::min<u64>(joins - a.join0, most_blocks(kGradThreads));
+          hipLaunchKernelGGL((k_grad_join<TO, E>), dim3(n), dim3(kGradThreads), 0, stream, a);
+          a.join0 += n;
+        }
       };
       if (p.E == 1) launch(std::integral_constant<int, 1>{});
       else if constexpr (sizeof(TG) == 4) launch(std::integral_constant<int, 4>{});
