@@ -1,9 +1,13 @@
 """The embedding gradient's two routes, few places in one launch and many by a
 sort, held to the same results."""
+import numpy as np
 import pytest
 import torch
 
-from test_embedding import EINVAL, abi, grad_call, lookup_call
+from test_embedding import EINVAL, FLOATS, abi, assert_grad, grad_call, lookup_call, make_tokens
+
+ONE_LAUNCH = 32768  # bytes of workspace: the header alone
+
 
 def needs(tgs, T, V, D, grad_dtype, out_dtype):
     return tgs.embedding_grad_workspace_bytes(T, V, D, grad_dtype, out_dtype)
@@ -32,3 +36,23 @@ def test_more_sums_to_join_than_workgroups(tgs_gpu):
     ws = torch.zeros(needs(tgs_gpu, T, V, 1, torch.bfloat16, torch.float32), dtype=torch.uint8, device="cuda")
     got = tgs_gpu.embedding_grad(tokens, grad, V, ws=ws)
     assert torch.equal(got[:, 0].long(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,one", [(300, True), (5_000, False)])
+@pytest.mark.parametrize("out_dtype", FLOATS)
+def test_rows_without_places_are_plus_zero(tgs_gpu, T, one, out_dtype):
+    V, D = 700, 33
+    assert (needs(tgs_gpu, T, V, D, torch.float32, out_dtype) == ONE_LAUNCH) == one
+    rng = np.random.default_rng(T)
+    tokens = make_tokens(T, V, 0.1, torch.int64, rng)
+    grad = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32))
+    got = tgs_gpu.embedding_grad(tokens.cuda(), grad.cuda(), V, scale=-0.37, out_dtype=out_dtype).cpu()
+    assert_grad(got, tokens, grad, V, -0.37)
+    empty = torch.ones(V, dtype=torch.bool)
+    empty[tokens[tokens >= 0]] = False
+    assert empty.any() and not torch.signbit(got[empty]).any()
+    # masked places only, and no places
+    for t in (torch.full((T,), -1), torch.empty(0, dtype=torch.int64)):
+        none = tgs_gpu.embedding_grad(t.cuda(), grad[:t.numel()].cuda(), V, scale=-2.0, out_dtype=out_dtype)
+        assert not none.any() and not torch.signbit(none).any()

@@ -601,7 +601,8 @@ __global__ __launch_bounds__(kFewThreads) void k_grad_few(FewArgs a) {
     if (i1 - i0 > kFewHot || (i1 == i0 && a.accumulate)) continue;
     float s[E] = {};
     add(i0, i1, s);
-    if (here) put_row<TO, E>(out + (int64_t)r * a.D, s, a.scale, a.accumulate, skip);
+    // a row without places is +0, whatever the scale's sign
+    if (here) put_row<TO, E>(out + (int64_t)r * a.D, s, i1 == i0 ? 1.0f : a.scale, a.accumulate, skip);
   }
   if (s_start[kWave] <= kFewHot) return;
   for (u32 r = 0; r < rows; ++r) {  // rows of many places: an eighth of them a wave
