@@ -2,9 +2,9 @@
 // formulas, and what is rounded, as in orthogonal.hip).
 //
 // Such a step has little to compute: what costs is the launches and the
-// barriers.  Here X stays in registers.  A wave owns 16 CB columns of the
-// padded MP x n matrix (MP = 32 or 64 rows) in both orders that the 16 x 16 x
-// 32 matrix instruction takes an operand in:
+// barriers.  Here X stays in registers, in fp32.  A wave owns 16 CB columns of
+// the padded MP x n matrix (MP = 32 or 64 rows) in both orders that the 16 x 16
+// x 32 matrix instruction takes an operand in, rounded to fp16 parts as it does:
 //   rows    lane = row of X, 8 columns      for the gram product X X^T
 //   columns lane = column of X, 8 rows      for the update P X
 // The instruction's result comes in the layout "lane = column, 4 rows", so its
@@ -12,9 +12,8 @@
 // summation index in another order (slot (g, 4 b + r) holds index 16 b + 4 g +
 // r; both operands use the same order).  P X with P as left operand gives the
 // column order; the same registers with the operands exchanged give (P X)^T,
-// the row order.  The update is computed both ways and nothing of X passes
-// through LDS.  Once, at the start, the order that memory does not have is
-// made by a product with the identity (exact: the parts are fp16).
+// the row order.  The update is computed both ways and X passes through LDS
+// once, at the start, for the order that memory does not have.
 //
 // Per step: the waves' gram products are added through LDS (lower blocks
 // only), E and D are made, the waves share the blocks of E^2, P is written to
@@ -46,7 +45,7 @@ struct SmallArgs {
   void* out;
   const double* part;  // partial sums of squares (chunks > 1)
   f4* gram;            // [2][batch][chunks][lower blocks][64]
-  h8* state;           // [batch][chunks][registers][threads]
+  f4* state;           // [batch][chunks][registers][threads]
   int64_t count;       // rows * cols
   tgs_dtype x_dtype, out_dtype;
   int rows, cols, n, tall, nesterov, steps, step, chunks, part_blocks;
@@ -120,8 +119,9 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
   const int64_t base = (int64_t)batch * a.count;
   const f4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
-  // X: [..][0] columns order, [..][1] rows order; high and low parts
-  h8 ch[KB][CB], cl[KB][CB], rh[RB][CP], rl[RB][CP];
+  // X, times the step's scale, block by block: this lane's column and four rows,
+  // and its row and four columns
+  f4 xc[RB][CB], xr[RB][CB];
   // the place of this lane's four values of block (rb, c) in memory order
   auto place = [&](int rb, int c, int64_t& at, int& left) {
     const int line = a.tall ? j0 + 16 * c + l16 : 16 * rb + l16;
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
     left = line < a.rows ? a.cols - off : 0;
   };
 
-  h8* state = a.state + ((int64_t)batch * a.chunks + chunk) * (2 * (KB * CB + RB * CP)) * kSmThreads + tid;
+  f4* state = a.state + ((int64_t)batch * a.chunks + chunk) * (2 * RB * CB) * kSmThreads + tid;
 
   if constexpr (STAGE == kWhole || STAGE == kFirst) {
     f4 v[RB][CB];
@@ -176,73 +176,48 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
     }
     const double inv = 1.0 / (sqrt(sum) + a.eps);
     const float sx = sc.x[0];
-    h8 id[2];  // slot (g, 4 b' + r) of column l16 of the identity's block b
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) id[b][e] = (_Float16)(e / 4 == b && 4 * g + e % 4 == l16 ? 1.0f : 0.0f);
+    // the other order: block by block through the wave's own LDS, in lines of 20 so
+    // that neither order's accesses meet in a bank
+    constexpr int LINE = 20;
+    static_assert(2 * 16 * LINE * sizeof(float) <= sizeof(s_gram[0]), "two blocks fit");
+    float* turn = (float*)s_gram[w];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-      for (int c = 0; c < CB; ++c)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          _Float16 h, l;
-          split_half((float)((double)v[rb][c][r] * inv) * sx, h, l);
-          ch[rb / 2][c][4 * (rb & 1) + r] = h;
-          cl[rb / 2][c][4 * (rb & 1) + r] = l;
-        }
-    if (!a.tall) {  // memory order is rows order: those are row operands, the columns follow from them
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int c = 0; c < CB; ++c)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            rh[rb][c / 2][4 * (c & 1) + r] = ch[rb / 2][c][4 * (rb & 1) + r];
-            rl[rb][c / 2][4 * (c & 1) + r] = cl[rb / 2][c][4 * (rb & 1) + r];
-          }
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          const f4 h = mfma(rh[rb][c / 2], id[c & 1], zero), l = mfma(rl[rb][c / 2], id[c & 1], zero);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            ch[rb / 2][c][4 * (rb & 1) + r] = (_Float16)h[r];
-            cl[rb / 2][c][4 * (rb & 1) + r] = (_Float16)l[r];
-          }
-        }
-    } else {
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int c = 0; c < CB; ++c) {
-          const f4 h = mfma(ch[rb / 2][c], id[rb & 1], zero), l = mfma(cl[rb / 2][c], id[rb & 1], zero);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            rh[rb][c / 2][4 * (c & 1) + r] = (_Float16)h[r];
-            rl[rb][c / 2][4 * (c & 1) + r] = (_Float16)l[r];
-          }
-        }
-    }
-  } else {
-    h8* p = state;
-#pragma unroll
-    for (int k = 0; k < KB; ++k)
 #pragma unroll
       for (int c = 0; c < CB; ++c) {
-        ch[k][c] = *p, p += kSmThreads;
-        cl[k][c] = *p, p += kSmThreads;
+        f4 x, y;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = (float)((double)v[rb][c][r] * inv) * sx;
+        float* block = turn + (rb * CB + c) % 2 * (16 * LINE);
+        *(f4*)(block + l16 * LINE + 4 * g) = x;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = block[(4 * g + r) * LINE + l16];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        xc[rb][c] = a.tall ? x : y;
+        xr[rb][c] = a.tall ? y : x;
       }
+  } else {
+    const f4* p = state;
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int c = 0; c < CP; ++c) {
-        rh[rb][c] = *p, p += kSmThreads;
-        rl[rb][c] = *p, p += kSmThreads;
+      for (int c = 0; c < CB; ++c) {
+        xc[rb][c] = *p, p += kSmThreads;
+        xr[rb][c] = *p, p += kSmThreads;
       }
   }
+
+  // An operand of two neighbouring blocks: high parts, low parts.
+  auto operand = [&](f4 first, f4 second, h8& high, h8& low) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      _Float16 h, l;
+      split_half(e < 4 ? first[e] : second[e - 4], h, l);
+      high[e] = h;
+      low[e] = l;
+    }
+  };
 
   // The sums of X X^T's lower blocks over this workgroup's columns; `take` gets
   // four rows of one column each.
@@ -252,15 +227,19 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
     for (int t = 0; t < NBLK; ++t) acc[t] = zero;
     if (w < waves) {
 #pragma unroll
-      for (int c = 0; c < CP; ++c)
+      for (int c = 0; c < CP; ++c) {
+        h8 rh[RB], rl[RB];
 #pragma unroll
-        for (int I = 0; I < RB; ++I)
+        for (int I = 0; I < RB; ++I) {
+          operand(xr[I][2 * c], xr[I][2 * c + 1], rh[I], rl[I]);
 #pragma unroll
           for (int J = 0; J <= I; ++J) {
             f4& q = acc[I * (I + 1) / 2 + J];
-            if (SPLIT) q = mfma(rl[I][c], rh[J][c], mfma(rh[I][c], rl[J][c], q));
-            q = mfma(rh[I][c], rh[J][c], q);
+            if (SPLIT) q = mfma(rl[I], rh[J], mfma(rh[I], rl[J], q));
+            q = mfma(rh[I], rh[J], q);
           }
+        }
+      }
 #pragma unroll
       for (int t = 0; t < NBLK; ++t) s_gram[w][t][lane] = acc[t];
     }
@@ -338,10 +317,13 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
   // X <- (a + D_P) X + E_P X in both orders, or the result in memory's order.
   auto update = [&](float sx, float sp, float next, auto last) {
     constexpr bool LAST = decltype(last)::value;
-    const float from_x = 1.0f / sx, from_acc = 1.0f / (sp * sx);
+    const float to_x = next / sx, to_acc = next / (sp * sx);  // powers of two
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
       f4 nc[RB], nr[RB];
+      h8 ch[KB], cl[KB];
+#pragma unroll
+      for (int k = 0; k < KB; ++k) operand(xc[2 * k][c], xc[2 * k + 1][c], ch[k], cl[k]);
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         f4 qc = zero, qr = zero;
@@ -351,23 +333,20 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
           h8 pl;
           if (SPLIT) pl = p_operand(ND - 1, rb, k);
           if (!LAST || a.tall) {
-            if (SPLIT) qc = mfma(pl, ch[k][c], mfma(ph, cl[k][c], qc));
-            qc = mfma(ph, ch[k][c], qc);
+            if (SPLIT) qc = mfma(pl, ch[k], mfma(ph, cl[k], qc));
+            qc = mfma(ph, ch[k], qc);
           }
           if (!LAST || !a.tall) {
-            if (SPLIT) qr = mfma(ch[k][c], pl, mfma(cl[k][c], ph, qr));
-            qr = mfma(ch[k][c], ph, qr);
+            if (SPLIT) qr = mfma(ch[k], pl, mfma(cl[k], ph, qr));
+            qr = mfma(ch[k], ph, qr);
           }
         }
         const f4 dc = *(const f4*)&s_dp[16 * rb + 4 * g];
         const float dr = s_dp[16 * rb + l16];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int ec = 4 * (rb & 1) + r, er = 4 * (c & 1) + r;
-          const float xc = ((float)ch[rb / 2][c][ec] + (float)cl[rb / 2][c][ec]) * from_x;
-          const float xr = ((float)rh[rb][c / 2][er] + (float)rl[rb][c / 2][er]) * from_x;
-          nc[rb][r] = fmaf(a.ca + dc[r], xc, qc[r] * from_acc) * next;
-          nr[rb][r] = fmaf(a.ca + dr, xr, qr[r] * from_acc) * next;
+          nc[rb][r] = fmaf((a.ca + dc[r]) * to_x, xc[rb][c][r], qc[r] * to_acc);
+          nr[rb][r] = fmaf((a.ca + dr) * to_x, xr[rb][c][r], qr[r] * to_acc);
         }
       }
 #pragma unroll
@@ -384,16 +363,8 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
           }
           store4(a.out, a.out_dtype, at, left, v);
         } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            _Float16 h, l;
-            split_half(nc[rb][r], h, l);
-            ch[rb / 2][c][4 * (rb & 1) + r] = h;
-            cl[rb / 2][c][4 * (rb & 1) + r] = l;
-            split_half(nr[rb][r], h, l);
-            rh[rb][c / 2][4 * (c & 1) + r] = h;
-            rl[rb][c / 2][4 * (c & 1) + r] = l;
-          }
+xc[rb][c] = nc[rb];
+          xr[rb][c] = nr[rb];
         }
       }
     }
@@ -403,20 +374,13 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
     return a.gram + ((int64_t)(s & 1) * gridDim.y + batch) * a.chunks * (NBLK * kWave);
   };
   auto save = [&]() {
-    h8* p = state;
-#pragma unroll
-    for (int k = 0; k < KB; ++k)
-#pragma unroll
-      for (int c = 0; c < CB; ++c) {
-        *p = ch[k][c], p += kSmThreads;
-        *p = cl[k][c], p += kSmThreads;
-      }
+    f4* p = state;
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int c = 0; c < CP; ++c) {
-        *p = rh[rb][c], p += kSmThreads;
-        *p = rl[rb][c], p += kSmThreads;
+      for (int c = 0; c < CB; ++c) {
+        *p = xc[rb][c], p += kSmThreads;
+        *p = xr[rb][c], p += kSmThreads;
       }
   };
 
@@ -486,7 +450,7 @@ static SmallPlan small_plan(int64_t batch, int64_t rows, int64_t cols) {
     p.gram = at;
     at += up((size_t)2 * batch * p.chunks * (p.rb * (p.rb + 1) / 2) * kWave * sizeof(f4));
     p.state = at;
-    at += up((size_t)batch * p.chunks * (2 * p.rb * p.cb) * kSmThreads * sizeof(h8));
+    at += up((size_t)batch * p.chunks * (2 * p.rb * p.cb) * kSmThreads * sizeof(f4));
   }
   p.total = at;
   return p;
@@ -528,7 +492,7 @@ void small_run(const NsCall& q, const StepScales& s, void* workspace, hipStream_
   a.out = q.out;
   a.part = (const double*)(ws + p.part);
   a.gram = (f4*)(ws + p.gram);
-  a.state = (h8*)(ws + p.state);
+  a.state = (f4*)(ws + p.state);
   a.count = q.rows * q.cols;
   a.x_dtype = q.x_dtype;
   a.out_dtype = q.out_dtype;
