@@ -305,8 +305,8 @@ tgs_status tgs_embedding_grad(const void* tokens, tgs_dtype tokens_dtype, int64_
 
 /* Bytes of workspace tgs_newton_schulz needs (0 if the sizes or the type are
    invalid): 10 bytes an entry of x (padded to 128 a side, 4 of them to the
-   update's tiles of up to 256) and 4 of the smaller square with 16-bit types,
-   16 and 8 with fp32, and up to 8 MB for sums that workgroups share. */
+   update's tiles of up to 256) and 4 of the smaller square with bf16, 16 and 8
+   with fp32 and fp16, and up to 8 MB for sums that workgroups share. */
 size_t tgs_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, tgs_dtype dtype);
 
 /*
@@ -318,9 +318,12 @@ size_t tgs_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t co
  * 1 <= batch <= 65535, 1 <= rows, cols <= 65536, 1 <= steps <= 64, eps >= 0.
  * Coefficients with which a singular value that starts in [0, 1] could pass
  * 2^30 are refused.  The products use fp16 operands scaled by powers of two
- * and fp32 sums: fp32 results are as exact as with fp32 products (three fp16
- * products each), 16-bit results are within half the error of their final
- * rounding for matrices like gradients.  A NaN or infinity in x makes its
+ * and fp32 sums.  fp32 and fp16 results are as exact as with fp32 products
+ * (three fp16 products each).  bf16 results take single products: before the
+ * final rounding (1.7e-3 of the 2-norm) they are off by at most half of that for
+ * matrices like gradients, whose singular values fall off into noise.  Matrices
+ * of low rank come out up to 2.8e-3 off where the shorter side is 65 to 128,
+ * 1.6e-3 at 256, 0.9e-3 at 512.  A NaN or infinity in x makes its
  * matrix's result NaN.  Equal inputs give equal bits.
  */
 tgs_status tgs_newton_schulz(const void* x, tgs_dtype dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps,

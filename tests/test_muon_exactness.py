@@ -1,7 +1,73 @@
-"""How exact the Newton-Schulz products are, type by type."""
-import pytest
+"""How exact the Newton-Schulz products are, type by type.
 
-from test_muon import distance, exact, matrices
+r is the 2-norm error of the exact result rounded to the type, taken from the
+oracle itself; a result whose error before the rounding is d r is off by
+sqrt(1 + d^2) r, and r varies by some per cent over the few entries of a small
+matrix.
+* fp16 and fp32 results: operands of 22 bits, 2^-18 in all before the rounding.
+* bf16 results: single fp16 operands, diagonals apart, d <= 1/2 for matrices like
+  gradients: 1.12 r, here 1.15 r.  Rounding X, A and P whole to fp16 gives 1.24 r
+  and more.
+"""
+import pytest
+import torch
+
+from test_muon import QUINTIC, distance, exact, matrices
+
+SHAPES = [(64, 64), (40, 700), (128, 128), (96, 160), (300, 200), (530, 600)]
+
+
+def rounding(want, dtype):
+    return distance(want.to(dtype), want)
+
+
+def bound(want, dtype):
+    return 1.15 * rounding(want, dtype) if dtype == torch.bfloat16 else 1.05 * rounding(want, dtype) + 2.0**-18
+
+
+def rounded(v, scale):
+    return (v * scale).half().float() / scale
+
+
+def half_products(x, apart, steps=5):
+    """The iteration with fp16 operands: diagonals of A and P and X held apart in fp32, or all rounded whole."""
+    a, b, c = QUINTIC
+    y = (x.double() / (x.double().norm() + 1e-7)).float()
+    y = y.T.contiguous() if y.shape[0] > y.shape[1] else y
+    for _ in range(steps):
+        h = rounded(y, 8192.0)
+        g = h @ h.T
+        d = g.diagonal().clone() if apart else torch.zeros(len(g))
+        e = rounded(g - d.diag(), 8192.0)
+        square = e @ e
+        p = (c * (d[:, None] + d[None, :]) + b) * e + c * square
+        dp = c * (d * d + square.diagonal()) + b * d if apart else torch.zeros(len(g))
+        p = rounded(p - p.diagonal().diag() if apart else p, 2048.0)
+        y = (a + dp)[:, None] * (y if apart else h) + p @ h
+    return y.T if x.shape[0] > x.shape[1] else y
+
+
+@pytest.mark.parametrize("shape", [(64, 64), (128, 128), (300, 200)])
+@pytest.mark.parametrize("noise", [0.1, 0.3, 1.0])
+def test_the_bounds_tell_the_schemes_apart(shape, noise):
+    x = matrices(shape, seed=sum(shape), noise=noise)
+    for dtype in (torch.bfloat16, torch.float16):
+        want = exact(x.to(dtype))
+        apart, whole = (half_products(x.to(dtype), s).to(dtype) for s in (True, False))
+        assert distance(whole, want) > bound(want, dtype)
+        # single products with the diagonals apart are enough for bf16, not for fp16
+        assert (distance(apart, want) <= bound(want, dtype)) == (dtype == torch.bfloat16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("noise", [0.1, 0.3, 1.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rounding_is_what_16_bit_results_lose(tgs_gpu, shape, noise, dtype):
+    for s in (shape, shape[::-1]):
+        x = matrices(s, seed=sum(s), noise=noise, dtype=dtype)
+        want = exact(x)
+        assert distance(tgs_gpu.newton_schulz(x.cuda()), want) <= bound(want, dtype)
 
 
 @pytest.mark.gpu

@@ -32,12 +32,16 @@
 // products see only the off-diagonal part E of A and of P:
 //   A = D + E:   A^2 = D^2 + (d_i + d_j) E + E^2,   P X = D_P X + E_P X.
 // X itself is held in fp32, in the order of the update's registers, and a + D_P
-// multiplies that; the operands are fp16.  With results of 16 bits the products
-// read high parts only: the result is then 2e-4 to 7e-4 (2-norm) off, below the
-// 1.7e-3 of the final rounding, where rounding X, A and P whole gives 1.6e-3 to
-// 3e-3 (fp16) and 1.3e-2 to 2.4e-2 (bf16).  With fp32 results every operand is
-// high + low and a product is three (high low + low high + high high): as exact
-// as fp32 products (1.4e-6 to 2.3e-6 against 1.3e-6 to 2.0e-6).
+// multiplies that; the operands are fp16.  With bf16 results the products read
+// high parts only: for matrices like gradients the result is then 2e-4 to 8e-4
+// (2-norm) off, below the 1.7e-3 of the final rounding, where rounding X, A and P
+// whole to fp16 gives 1.2e-3 to 4.3e-3 and to bf16 1.3e-2 to 2.4e-2.  What X's
+// rounding puts into directions in which a matrix of low rank is empty grows by
+// the first coefficient a step: such a matrix comes out up to 2.8e-3 off with a
+// shorter side of 128, 1.6e-3 with 256, 0.9e-3 with 512.  With fp32 and fp16
+// results every operand is high + low and a product is three (high low + low high
+// + high high): as exact as fp32 products (1.4e-6 to 2.3e-6 against 1.3e-6 to
+// 2.0e-6).  fp16 rounds at 2.1e-4, which single products' 2e-4 to 8e-4 would pass.
 //
 // Range.  The singular values of X start in [0, 1]; the host bounds them after
 // every step by the polynomial's extrema, and scales X, A and P by powers of
@@ -993,7 +997,7 @@ static tgs_status ns_run(const NsCall& q, const NsPlan& p, const StepScales& s, 
   });
   with_float_dtype(q.out_dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    run_steps<sizeof(T) == 4, T, MUON>(q, p, s, ws, stream);
+    run_steps<kSplitProducts<T>, T, MUON>(q, p, s, ws, stream);
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(TGS_EHIP, "%s: launch failed: %s", q.what, hipGetErrorString(e));
@@ -1004,7 +1008,7 @@ static tgs_status ns_run(const NsCall& q, const NsPlan& p, const StepScales& s, 
 static tgs_status ns_check(const NsCall& q, NsPlan* p, StepScales* s, const void* workspace, size_t workspace_bytes) {
   if (!is_float_dtype(q.x_dtype) || !is_float_dtype(q.out_dtype))
     return fail(TGS_EINVAL, "%s: values must be fp32, bf16 or fp16", q.what);
-  if (!ns_plan(q.batch, q.rows, q.cols, q.out_dtype == TGS_FP32, p))
+  if (!ns_plan(q.batch, q.rows, q.cols, split_products(q.out_dtype), p))
     return fail(TGS_EINVAL, "%s: batch=%lld rows=%lld cols=%lld outside [1, 65535], [1, 65536], [1, 65536]", q.what,
                 (long long)q.batch, (long long)q.rows, (long long)q.cols);
   if (q.steps < 1 || q.steps > kMaxSteps)
@@ -1034,7 +1038,7 @@ using namespace tgs;
 
 extern "C" size_t tgs_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, tgs_dtype dtype) {
   NsPlan p;
-  return is_float_dtype(dtype) && ns_plan(batch, rows, cols, dtype == TGS_FP32, &p) ? p.total : 0;
+  return is_float_dtype(dtype) && ns_plan(batch, rows, cols, split_products(dtype), &p) ? p.total : 0;
 }
 
 extern "C" tgs_status tgs_newton_schulz(const void* x, tgs_dtype dtype, int64_t batch, int64_t rows, int64_t cols,

@@ -1,10 +1,10 @@
 // Newton-Schulz products of matrices that one workgroup holds in LDS (the
 // formulas, and what is rounded, as in orthogonal.hip): a shorter side of 65 to
-// 128, and a longer one of up to 384 in 16 bits, 128 in fp32.
+// 128, and a longer one of up to 384 for bf16 results, 128 for fp32 and fp16.
 //
 // Such a matrix has 17 launches' worth of steps and little to compute in each:
 // one launch does it all, the norm and the momentum included.  X lies in LDS
-// column by column (fp16; high and low parts for fp32 results) and, in fp32, in
+// column by column (fp16; high and low parts for fp32 and fp16 results) and, in fp32, in
 // registers in the layout that the matrix instructions leave: the wave that
 // makes a block of the update owns it throughout.  The update reads X as it lies,
 // the gram by transposing reads.  Eight waves take the products' blocks of 32 x 32;
@@ -329,7 +329,7 @@ void lds_run(const NsCall& q, const StepScales& s, hipStream_t stream) {
   a.eps = q.eps;
   with_float_dtype(q.out_dtype, [&](auto* o) {
     using TW = std::remove_pointer_t<decltype(o)>;
-    constexpr bool SPLIT = sizeof(TW) == 4;
+    constexpr bool SPLIT = kSplitProducts<TW>;
     if (q.momentum)
       with_float_dtype(q.x_dtype, [&](auto* x) {
         launch_lds<SPLIT, std::remove_pointer_t<decltype(x)>, TW, true>(a, s, (int)q.batch, stream);

@@ -512,7 +512,7 @@ void small_run(const NsCall& q, const StepScales& s, void* workspace, hipStream_
   a.cc = (float)q.c;
   a.eps = q.eps;
   if (p.chunks > 1) launch_norm(q, (double*)(ws + p.part), p.blocks, stream);
-  if (q.out_dtype == TGS_FP32) launch_small_any<true>(p, a, s, (int)q.batch, stream);
+  if (split_products(q.out_dtype)) launch_small_any<true>(p, a, s, (int)q.batch, stream);
   else launch_small_any<false>(p, a, s, (int)q.batch, stream);
 }
 

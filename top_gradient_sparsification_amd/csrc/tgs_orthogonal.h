@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tgs_host.h"
 #include "tgs_types.h"
@@ -13,6 +14,12 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxSteps = 64;
+
+// Operands are high + low fp16 parts and a product is three where the result is
+// fp32 or fp16, whose roundings (2^-24, 2^-11) a single fp16 operand's would pass.
+inline bool split_products(tgs_dtype t) { return t != TGS_BF16; }
+template <class T>
+constexpr bool kSplitProducts = !std::is_same<T, bf16_t>::value;
 
 // Powers of two that X (before each step, 1 after the last), A and P are held at.
 struct StepScales {
