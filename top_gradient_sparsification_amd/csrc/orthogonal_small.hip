@@ -1,5 +1,6 @@
 // Newton-Schulz products of matrices whose shorter side is at most 64 (the
-// formulas, and what is rounded, as in orthogonal.hip).
+// formulas, and what is rounded, as in orthogonal.hip, but that the update takes
+// X's low parts for every type).
 //
 // Such a step has little to compute: what costs is the launches and the
 // barriers.  Here X stays in registers, in fp32.  A wave owns 16 CB columns of
@@ -314,7 +315,12 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
     const h4 y = *(const h4*)&s_p[d][16 * rb + l16][32 * k + 16 + 4 * g];
     return (h8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
   };
-  // X <- (a + D_P) X + E_P X in both orders, or the result in memory's order.
+  // X <- (a + D_P) X + E_P X in both orders, or the result in memory's order.  X's
+  // low parts are multiplied for bf16 results too: what its rounding puts into
+  // directions in which a matrix of low rank is empty grows by the first coefficient
+  // a step, and the more the smaller the matrix (8 x 8 of rank 1: 1.6e-2 off, with
+  // them 7e-4; 64 x 64 of rank 8: 3.0e-3 and 7e-4).  64 x 512 takes 46 us with
+  // them, 39 without, 63 with all three products; 64 x 64 takes 23, 20 and 27.
   auto update = [&](float sx, float sp, float next, auto last) {
     constexpr bool LAST = decltype(last)::value;
     const float to_x = next / sx, to_acc = next / (sp * sx);  // powers of two
@@ -333,12 +339,12 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
           h8 pl;
           if (SPLIT) pl = p_operand(ND - 1, rb, k);
           if (!LAST || a.tall) {
-            if (SPLIT) qc = mfma(pl, ch[k], mfma(ph, cl[k], qc));
-            qc = mfma(ph, ch[k], qc);
+            if (SPLIT) qc = mfma(pl, ch[k], qc);
+            qc = mfma(ph, ch[k], mfma(ph, cl[k], qc));
           }
           if (!LAST || !a.tall) {
-            if (SPLIT) qr = mfma(ch[k], pl, mfma(cl[k], ph, qr));
-            qr = mfma(ch[k], ph, qr);
+            if (SPLIT) qr = mfma(ch[k], pl, qr);
+            qr = mfma(ch[k], ph, mfma(cl[k], ph, qr));
           }
         }
         const f4 dc = *(const f4*)&s_dp[16 * rb + 4 * g];
