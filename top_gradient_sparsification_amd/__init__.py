@@ -682,6 +682,51 @@ def _require_any(t, dtypes, name, device=None):
         raise ValueError("%s must be contiguous" % name)
 
 
+def _differentiable(t, name, out) -> bool:
+    """Whether a graph is to be kept of a call on ``t``; ``out`` takes none."""
+    if not (t.requires_grad and torch.is_grad_enabled()):
+        return False
+    if out is not None:
+        raise RuntimeError("%s requires a gradient, which a call with out= has not" % name)
+    return True
+
+
+class _Lookup(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, table, scale, out_dtype, ws):
+        ctx.save_for_backward(tokens)
+        ctx.rows, ctx.scale, ctx.dtype = table.shape[0], scale, table.dtype
+        return embedding_lookup(tokens, table, scale, out_dtype, ws=ws)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (tokens,) = ctx.saved_tensors
+        return None, embedding_grad(tokens, grad.contiguous(), ctx.rows, ctx.scale, ctx.dtype), None, None, None
+
+
+class _LookupGrad(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, grad, num_rows, scale, out_dtype, ws):
+        ctx.save_for_backward(tokens)
+        ctx.scale, ctx.dtype = scale, grad.dtype
+        return embedding_grad(tokens, grad, num_rows, scale, out_dtype, ws=ws)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (tokens,) = ctx.saved_tensors
+        return None, embedding_lookup(tokens, grad.contiguous(), ctx.scale, ctx.dtype), None, None, None, None
+
+
+class _NewtonSchulz(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, steps, coefficients, eps, ws):
+        return newton_schulz(x, steps, coefficients, eps, ws=ws)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise NotImplementedError("newton_schulz has no gradient: detach its input")
+
+
 def embedding_lookup_workspace_bytes(T: int) -> int:
     return int(_load().tgs_embedding_lookup_workspace_bytes(T))
 
@@ -694,13 +739,18 @@ def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1
     fp16, ``[V, D]``); a negative token is a masked place and gives a row of
     zeros.  ``out`` has the shape ``tokens.shape + (D,)`` and the type
     ``out_dtype`` (the table's if not given).  A token >= V gives zeros and
-    sets the bad-input bit that ``check_device_error(ws)`` reports."""
+    sets the bad-input bit that ``check_device_error(ws)`` reports.
+
+    Differentiable in the table, whose gradient is ``embedding_grad``'s, in the
+    table's type; not with ``out``."""
     _require_any(table, _FLOATS, "table")
     dev = table.device
     _require_any(tokens, _TOKENS, "tokens", dev)
     if table.dim() != 2:
         raise ValueError("table must have shape [V, D]")
     V, D = table.shape
+    if _differentiable(table, "table", out):
+        return _Lookup.apply(tokens, table, scale, out_dtype, ws)
     if out is None:
         out_dtype = out_dtype or table.dtype
         if out_dtype not in _FLOATS:
@@ -738,13 +788,18 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, scal
     feeds the sparsifier's steps).  Sums are fp32 in a fixed order: equal
     inputs give equal bits.  Masked places (negative tokens) add to nothing;
     tokens >= num_rows neither, and set the bad-input bit that
-    ``check_device_error(ws)`` reports."""
+    ``check_device_error(ws)`` reports.  Differentiable in ``grad``, without
+    ``out``."""
     _require_any(grad, _FLOATS, "grad")
     dev = grad.device
     _require_any(tokens, _TOKENS, "tokens", dev)
     if grad.dim() < 1 or grad.shape[:-1] != tokens.shape:
         raise ValueError("grad must have the shape of tokens and one dimension more")
     V, D = int(num_rows), grad.shape[-1]
+    if _differentiable(grad, "grad", out):
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        return _LookupGrad.apply(tokens, grad, V, scale, out_dtype, ws)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
@@ -794,10 +849,13 @@ def newton_schulz(x: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ_CO
     """Orthogonalises a matrix, or each of a stack of matrices: ``X = x /
     (|x|_F + eps)``, then ``steps`` times ``X <- a X + (b A + c A^2) X`` with
     ``A = X X^T`` (over the shorter side).  ``out`` has ``x``'s shape and type
-    (fp32, bf16, fp16) and may be ``x`` itself."""
+    (fp32, bf16, fp16) and may be ``x`` itself.  Going back through it raises:
+    it has no gradient."""
     _require_any(x, _FLOATS, "x")
     dev = x.device
     b, m, n = _matrices(x, "x")
+    if _differentiable(x, "x", out):
+        return _NewtonSchulz.apply(x, steps, coefficients, eps, ws)
     if out is None:
         out = torch.empty_like(x)
     else:
