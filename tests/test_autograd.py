@@ -95,3 +95,25 @@ def test_what_has_no_gradient_says_so(tgs_gpu):
         want = tgs_gpu.newton_schulz(table.detach())
         assert not tgs_gpu.newton_schulz(table).requires_grad and torch.equal(o.detach(), want)
         assert not tgs_gpu.embedding_lookup(tokens, table, out=torch.empty(5, 6, device="cuda")).requires_grad
+
+
+@pytest.mark.gpu
+def test_what_is_written_in_place_is_seen(tgs_gpu):
+    """A graph that saved a tensor must not go back through values that a later call has overwritten."""
+    x, g, w = normal(4, 6, seed=1), normal(6, 5, seed=2), normal(6, 5, seed=3).requires_grad_()
+    loss = (x.requires_grad_() @ w).sum()
+    with torch.no_grad():
+        tgs_gpu.muon_step(w, g, torch.zeros_like(g), lr=0.1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    for write in (lambda t: tgs_gpu.newton_schulz(g, out=t),
+                  lambda t: tgs_gpu.embedding_lookup(torch.arange(6, device="cuda"), g, out=t),
+                  lambda t: tgs_gpu.embedding_grad(torch.arange(6, device="cuda"), g, 6, out=t),
+                  lambda t: tgs_gpu.muon_step(torch.ones_like(g), g, t, lr=0.1)):
+        t = normal(6, 5, seed=4)
+        before = t._version
+        write(t)
+        assert t._version > before
+    with torch.inference_mode():
+        t = normal(6, 5, seed=4)
+        tgs_gpu.muon_step(t, g, torch.zeros_like(g), lr=0.1)

@@ -691,6 +691,12 @@ def _differentiable(t, name, out) -> bool:
     return True
 
 
+def _written(t):
+    """Tells autograd, which cannot see it, that a call has overwritten ``t``."""
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 class _Lookup(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, table, scale, out_dtype, ws):
@@ -751,7 +757,8 @@ def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1
     V, D = table.shape
     if _differentiable(table, "table", out):
         return _Lookup.apply(tokens, table, scale, out_dtype, ws)
-    if out is None:
+    given = out is not None
+    if not given:
         out_dtype = out_dtype or table.dtype
         if out_dtype not in _FLOATS:
             raise TypeError("out_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
@@ -770,6 +777,8 @@ def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1
                                       ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_embedding_lookup")
+    if given:
+        _written(out)
     return out
 
 
@@ -800,7 +809,8 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, scal
         if accumulate:
             raise ValueError("accumulate needs out")
         return _LookupGrad.apply(tokens, grad, V, scale, out_dtype, ws)
-    if out is None:
+    given = out is not None
+    if not given:
         if accumulate:
             raise ValueError("accumulate needs out")
         out_dtype = out_dtype or torch.float32
@@ -825,6 +835,8 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, scal
                                 bool(accumulate), ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_embedding_grad")
+    if given:
+        _written(out)
     return out
 
 
@@ -856,7 +868,8 @@ def newton_schulz(x: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ_CO
     b, m, n = _matrices(x, "x")
     if _differentiable(x, "x", out):
         return _NewtonSchulz.apply(x, steps, coefficients, eps, ws)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty_like(x)
     else:
         _require_any(out, (x.dtype,), "out", dev)
@@ -879,6 +892,8 @@ def newton_schulz(x: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ_CO
                                ws.numel(), stream)
     if st:
         _check(st, "tgs_newton_schulz")
+    if given:
+        _written(out)
     return out
 
 
@@ -920,6 +935,8 @@ def muon_step(weight: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, 
                            stream)
     if st:
         _check(st, "tgs_muon_step")
+    _written(weight)
+    _written(momentum)
     return weight
 
 
