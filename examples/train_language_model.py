@@ -5,8 +5,8 @@
 Each step looks the tokens' rows up in an embedding table (``embedding_lookup``),
 takes two weight matrices of torch over them, and on the way back
 
-* sums the table's gradient by sorted tokens (``embedding_grad``), dense and
-  fp32, as the sparsifier takes it;
+* sums the table's gradient by sorted tokens (the lookup's own gradient,
+  ``embedding_grad``), dense and fp32, as the sparsifier takes it;
 * sends the largest 1% of it after error feedback (``TopkStep``): here the
   worker applies its own pairs, where many would merge theirs;
 * updates the matrices by Muon (``muon_step``), whose Newton-Schulz products
@@ -27,21 +27,6 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import top_gradient_sparsification_amd as tgs
 
 
-class Lookup(torch.autograd.Function):
-    """The table's rows; its gradient by sorted tokens."""
-
-    @staticmethod
-    def forward(ctx, tokens, table, scale):
-        ctx.save_for_backward(tokens)
-        ctx.rows, ctx.scale = table.shape[0], scale
-        return tgs.embedding_lookup(tokens, table, scale=scale)
-
-    @staticmethod
-    def backward(ctx, grad):
-        (tokens,) = ctx.saved_tensors
-        return None, tgs.embedding_grad(tokens, grad.contiguous(), ctx.rows, scale=ctx.scale), None
-
-
 class Model:
     def __init__(self, vocab, dim, density, seed=0):
         gen = torch.Generator(device="cuda").manual_seed(seed)
@@ -59,7 +44,7 @@ class Model:
         self.topk = tgs.TopkStep(n, max(1, int(density * n)))
 
     def loss(self, tokens, targets):
-        x = Lookup.apply(tokens, self.table, self.scale)
+        x = tgs.embedding_lookup(tokens, self.table, scale=self.scale)
         h = torch.tanh(x.flatten(0, 1) @ self.hidden)
         real = targets.flatten() >= 0
         return torch.nn.functional.cross_entropy(h[real] @ self.output, targets.flatten()[real])
@@ -73,7 +58,11 @@ class Model:
             idx, val = self.topk(self.table.grad.view(-1), self.residual)
             self.table.view(-1).index_add_(0, idx, val, alpha=-lr_table)
             for w, momentum in self.matrices:
-                tgs.muon_step(w, w.grad, momentum, lr=lr_matrices)
+                # Muon scales a step by sqrt(max(1, out / in)), muon_step by sqrt(max(1, rows / cols)):
+                # these matrices are [in, out]
+                n_in, n_out = w.shape
+                scale = math.sqrt(max(1, n_out / n_in) / max(1, n_in / n_out))
+                tgs.muon_step(w, w.grad, momentum, lr=lr_matrices * scale)
         return loss.detach()
 
 
@@ -95,7 +84,7 @@ def batches(vocab, sequences, length, seed=1):
 def train(steps=60, vocab=4096, dim=256, density=0.01, sequences=64, length=128, report=10):
     model, losses = Model(vocab, dim, density), []
     for i, (tokens, targets) in zip(range(steps), batches(vocab, sequences, length)):
-        losses.append(model.step(tokens, targets, lr_table=2.0, lr_matrices=0.05))
+        losses.append(model.step(tokens, targets, lr_table=2.0, lr_matrices=0.02))
         if report and (i % report == 0 or i == steps - 1):
             print("step %3d  loss %.3f" % (i, losses[-1].item()), flush=True)
     model.topk.check()

@@ -340,7 +340,8 @@ size_t tgs_muon_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, tgs_d
  *   u = grad + beta momentum (nesterov != 0), or momentum
  *   O = u orthogonalised as tgs_newton_schulz does
  *   weight <- (1 - lr weight_decay) weight - lr sqrt(max(1, rows / cols)) O
- *   weight    [batch][rows][cols] fp32, bf16 or fp16, in/out.
+ *   weight    [batch][rows][cols] fp32, bf16 or fp16, in/out; rows are taken
+ *             to be a layer's outputs.
  *   grad      [batch][rows][cols] fp32, bf16 or fp16, read only.
  *   momentum  [batch][rows][cols] fp32, in/out.
  * The arrays must not overlap.  Sizes, coefficients, exactness (by the

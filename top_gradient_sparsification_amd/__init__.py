@@ -909,7 +909,9 @@ def muon_step(weight: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, 
     without ``nesterov``), ``O = newton_schulz(u)``, ``weight <- (1 - lr
     weight_decay) weight - lr sqrt(max(1, rows / cols)) O``.  ``weight`` and
     ``grad`` are fp32, bf16 or fp16, ``momentum`` is fp32; weight and momentum
-    are updated in place.  Returns ``weight``."""
+    are updated in place.  Rows are taken to be a layer's outputs: for a matrix
+    kept as ``[in, out]`` the factor is the caller's, through ``lr``.  Returns
+    ``weight``."""
     _require_any(weight, _FLOATS, "weight")
     dev = weight.device
     _require_any(grad, _FLOATS, "grad", dev)
