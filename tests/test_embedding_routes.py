@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_embedding import EINVAL, FLOATS, abi, assert_grad, grad_call, lookup_call, make_tokens
+from test_embedding import EINVAL, FLOATS, U, abi, assert_grad, grad_call, lookup_call, make_tokens
 
 ONE_LAUNCH = 32768  # bytes of workspace: the header alone
 
@@ -56,3 +56,56 @@ def test_rows_without_places_are_plus_zero(tgs_gpu, T, one, out_dtype):
     for t in (torch.full((T,), -1), torch.empty(0, dtype=torch.int64)):
         none = tgs_gpu.embedding_grad(t.cuda(), grad[:t.numel()].cuda(), V, scale=-2.0, out_dtype=out_dtype)
         assert not none.any() and not torch.signbit(none).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("grad_dtype", FLOATS)
+@pytest.mark.parametrize("out_dtype", FLOATS)
+@pytest.mark.parametrize("D", [1, 5, 130, 264])
+def test_sorted_types_and_widths(tgs_gpu, grad_dtype, out_dtype, D):
+    """Every type, written and accumulated: masked places, tokens within a chunk and over many."""
+    T, V = 5_003, 311
+    assert needs(tgs_gpu, T, V, D, grad_dtype, out_dtype) > ONE_LAUNCH
+    rng = np.random.default_rng(D)
+    for ids, scale, acc in ((torch.int32, -0.37, False), (torch.int64, 1.0, True)):
+        tokens = make_tokens(T, V, 0.1, ids, rng)
+        grad = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).to(grad_dtype)
+        base = torch.from_numpy(rng.standard_normal((V, D)).astype(np.float32)).to(out_dtype) if acc else None
+        out = base.cuda() if acc else None
+        got = tgs_gpu.embedding_grad(tokens.cuda(), grad.cuda(), V, scale=scale, out_dtype=out_dtype, out=out,
+                                     accumulate=acc)
+        assert got.dtype == out_dtype
+        assert_grad(got, tokens, grad, V, scale, base)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,D,one", [(1025, 128_000, 130, True), (1_100, 128_000, 130, False), (2_048, 1_000, 33, True),
+                                       (2_049, 1_000, 33, False), (1, 300_000, 3, False), (700, 64, 4_099, True)])
+@pytest.mark.parametrize("out_dtype", FLOATS)
+def test_either_side_of_the_rule(tgs_gpu, T, V, D, one, out_dtype):
+    assert (needs(tgs_gpu, T, V, D, torch.bfloat16, out_dtype) == ONE_LAUNCH) == one
+    rng = np.random.default_rng(T)
+    tokens = make_tokens(T, V, 0.05, torch.int64, rng)
+    grad = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).bfloat16()
+    got = tgs_gpu.embedding_grad(tokens.cuda(), grad.cuda(), V, scale=0.5, out_dtype=out_dtype)
+    assert_grad(got, tokens, grad, V, 0.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("D", [2_003, 2_048])
+def test_eight_fp16_gradients_a_lane(tgs_gpu, D, accumulate):
+    """Sizes that take eight 16-bit gradients a lane into fp32 rows; the oracle runs on the GPU."""
+    T, V = 70_001, 3_000
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    tokens = torch.randint(-100, V, (T,), device="cuda", generator=gen)
+    grad = torch.randn(T, D, device="cuda", generator=gen).half()
+    base = torch.randn(V, D, device="cuda", generator=gen) if accumulate else torch.zeros(V, D, device="cuda")
+    real = tokens >= 0
+    total, size = (torch.zeros(V, D, dtype=torch.float64, device="cuda") for _ in range(2))
+    total.index_add_(0, tokens[real], grad[real].double())
+    size.index_add_(0, tokens[real], grad[real].double().abs())
+    count = torch.bincount(tokens[real], minlength=V).double()[:, None]
+    got = tgs_gpu.embedding_grad(tokens, grad, V, out=base.clone(), accumulate=accumulate)
+    want = total + base.double()
+    assert ((got.double() - want).abs() <= size * (count + 8) * U * 1.01 + want.abs() * 2 * U).all()
