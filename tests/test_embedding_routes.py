@@ -93,10 +93,10 @@ def test_either_side_of_the_rule(tgs_gpu, T, V, D, one, out_dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("accumulate", [False, True])
-@pytest.mark.parametrize("D", [2_003, 2_048])
-def test_eight_fp16_gradients_a_lane(tgs_gpu, D, accumulate):
-    """Sizes that take eight 16-bit gradients a lane into fp32 rows; the oracle runs on the GPU."""
-    T, V = 70_001, 3_000
+@pytest.mark.parametrize("T,D", [(70_001, 2_003), (70_001, 2_048), (262_147, 257), (262_147, 256)])
+def test_eight_fp16_gradients_a_lane(tgs_gpu, T, D, accumulate):
+    """Sizes that take eight 16-bit gradients a lane into fp32 rows, and one that does not; the oracle runs on the GPU."""
+    V = 3_000
     gen = torch.Generator(device="cuda").manual_seed(D)
     tokens = torch.randint(-100, V, (T,), device="cuda", generator=gen)
     grad = torch.randn(T, D, device="cuda", generator=gen).half()

@@ -658,9 +658,12 @@ struct GradPlan {
 static bool grad_plan(int64_t T, int64_t V, int64_t D, tgs_dtype tg, tgs_dtype to, GradPlan* p) {
   if (T < 0 || T > INT32_MAX || V < 1 || V > INT32_MAX || D < 1 || D > INT32_MAX) return false;
   p->E = vector_of(D, tg, to);
-  // 16-bit gradients to fp32 rows: eight a lane where there are waves enough (131,072 places of 2,048: 325 -> 299 us;
-  // 16,384 of 1,024, where it would halve the chunks: 54 -> 62)
-  if (p->E == 4 && dtype_bytes(tg) == 2 && D >= 8 && T > kFewMaxT && T >= ((int64_t)1 << 27) / D) p->E = 8;
+  // 16-bit gradients to fp32 rows: eight a lane where that leaves fewer groups of 64 lanes a row, and waves
+  // enough.  With 25,000 rows, accumulated, four against eight: 2^26 values in rows of 512 103 and 86 us, of 2,048
+  // 103 and 81; 2^28 in rows of 2,048 284 and 251.  At 2^25 they are within a tenth of each other (rows of 768 76
+  // and 77, written 73 and 75), at 2^24, where eight halves the chunks, written 53 and 61.  Rows of up to 256 would
+  // leave half the lanes idle: 2^26 in rows of 64 204 and 215, 2^27 in rows of 256 163 and 171.
+  if (p->E == 4 && dtype_bytes(tg) == 2 && D > 256 && T > kFewMaxT && T >= ((int64_t)1 << 26) / D) p->E = 8;
   p->nv = (u32)((D + p->E - 1) / p->E);
   p->slabs = (p->nv + kWave - 1) / kWave;
   // chunks: long enough that partial rows are few, short enough that about
