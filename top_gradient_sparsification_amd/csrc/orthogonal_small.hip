@@ -20,9 +20,9 @@
 // only), E and D are made, the waves share the blocks of E^2, P is written to
 // LDS, every wave updates its columns.
 //
-// Up to 128 CB columns one workgroup holds a whole matrix and one launch does
-// everything, the norm and the momentum included.  Longer ones are cut into
-// chunks of that many columns, a workgroup each, and the sum over chunks is
+// Up to 512 columns of 64, or 1,024 of 32, one workgroup holds a whole matrix and
+// one launch does everything, the norm and the momentum included.  Longer ones are
+// cut into chunks of 256 columns, a workgroup each, and the sum over chunks is
 // where a launch ends: norm, first gram, then one launch a step, in which every
 // workgroup adds the chunks' gram products itself; X is kept in memory between
 // them as the registers' dump.
@@ -432,8 +432,12 @@ struct SmallPlan {
   size_t part, gram, state, total;
 };
 
-// Columns a wave: the fewest with which one workgroup holds the matrix; else
-// the fewest with which every workgroup has a compute unit of its own.
+// Columns a wave: the fewest with which one workgroup holds the matrix and one
+// launch does (30 x 512 in bf16 21 us, 35 in chunks; 300 of 64 x 512 99 and 228;
+// one of 64 x 512 in fp32 65 and 60 is the exception); else 32, the fewest there
+// are, for any batch: with 64, 16 of 64 x 4,096 take 139 us instead of 108, 300
+// of 64 x 2,048 966 instead of 895, 1,000 of 30 x 1,100 885 instead of 765, though
+// 1,000 of 64 x 1,024 1,452 instead of 1,585.
 static SmallPlan small_plan(int64_t batch, int64_t rows, int64_t cols) {
   SmallPlan p{};
   const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
@@ -443,8 +447,6 @@ static SmallPlan small_plan(int64_t batch, int64_t rows, int64_t cols) {
   p.cb = 2;
   if (chunks(most) == 1)
     while (chunks(p.cb) > 1) p.cb *= 2;
-  else
-    while (p.cb < most && chunks(p.cb) * batch > 256) p.cb *= 2;
   p.chunks = (int)chunks(p.cb);
   p.blocks = norm_blocks(batch, rows * cols);
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
@@ -471,10 +473,12 @@ static void launch_small(const SmallPlan& p, SmallArgs a, const StepScales& s, i
     hipLaunchKernelGGL((k_ns_small<RB, CB, SPLIT, kWhole>), grid, block, 0, stream, a, s);
     return;
   }
-  hipLaunchKernelGGL((k_ns_small<RB, CB, SPLIT, kFirst>), grid, block, 0, stream, a, s);
-  for (a.step = 0; a.step + 1 < a.steps; ++a.step)
-    hipLaunchKernelGGL((k_ns_small<RB, CB, SPLIT, kMiddle>), grid, block, 0, stream, a, s);
-  hipLaunchKernelGGL((k_ns_small<RB, CB, SPLIT, kEnd>), grid, block, 0, stream, a, s);
+  if constexpr (CB == 2) {  // chunks are of 32 columns a wave
+    hipLaunchKernelGGL((k_ns_small<RB, CB, SPLIT, kFirst>), grid, block, 0, stream, a, s);
+    for (a.step = 0; a.step + 1 < a.steps; ++a.step)
+      hipLaunchKernelGGL((k_ns_small<RB, CB, SPLIT, kMiddle>), grid, block, 0, stream, a, s);
+    hipLaunchKernelGGL((k_ns_small<RB, CB, SPLIT, kEnd>), grid, block, 0, stream, a, s);
+  }
 }
 
 template <bool SPLIT>
