@@ -164,7 +164,7 @@ def _check(status: int, what: str):
 
 
 def _stream_handle(device) -> int:
-    index = torch.device(device).index
+    index = (device if isinstance(device, torch.device) else torch.device(device)).index
     # the handle alone: a torch.cuda.Stream object costs 2 us a call
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
@@ -682,9 +682,9 @@ def _require_any(t, dtypes, name, device=None):
         raise ValueError("%s must be contiguous" % name)
 
 
-def _differentiable(t, name, out) -> bool:
-    """Whether a graph is to be kept of a call on ``t``; ``out`` takes none."""
-    if not (t.requires_grad and torch.is_grad_enabled()):
+def _differentiable(name, out) -> bool:
+    """Whether a graph is to be kept of a call on a tensor that requires a gradient; ``out`` takes none."""
+    if not torch.is_grad_enabled():
         return False
     if out is not None:
         raise RuntimeError("%s requires a gradient, which a call with out= has not" % name)
@@ -755,7 +755,7 @@ def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1
     if table.dim() != 2:
         raise ValueError("table must have shape [V, D]")
     V, D = table.shape
-    if _differentiable(table, "table", out):
+    if table.requires_grad and _differentiable("table", out):
         return _Lookup.apply(tokens, table, scale, out_dtype, ws)
     given = out is not None
     if not given:
@@ -772,8 +772,8 @@ def embedding_lookup(tokens: torch.Tensor, table: torch.Tensor, scale: float = 1
         ws = _scratch("embedding", 32768, dev, stream)
     else:
         _require_ws(ws, dev)
-    st = _load().tgs_embedding_lookup(_ptr(tokens), _DTYPES[tokens.dtype], tokens.numel(), _ptr(table),
-                                      _DTYPES[table.dtype], V, D, scale, _ptr(out), _DTYPES[out.dtype],
+    st = _load().tgs_embedding_lookup(tokens.data_ptr(), _DTYPES[tokens.dtype], tokens.numel(), table.data_ptr(),
+                                      _DTYPES[table.dtype], V, D, scale, out.data_ptr(), _DTYPES[out.dtype],
                                       ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_embedding_lookup")
@@ -805,7 +805,7 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, scal
     if grad.dim() < 1 or grad.shape[:-1] != tokens.shape:
         raise ValueError("grad must have the shape of tokens and one dimension more")
     V, D = int(num_rows), grad.shape[-1]
-    if _differentiable(grad, "grad", out):
+    if grad.requires_grad and _differentiable("grad", out):
         if accumulate:
             raise ValueError("accumulate needs out")
         return _LookupGrad.apply(tokens, grad, V, scale, out_dtype, ws)
@@ -831,8 +831,8 @@ def embedding_grad(tokens: torch.Tensor, grad: torch.Tensor, num_rows: int, scal
         ws = _scratch("embedding", need, dev, stream)
     else:
         _require_ws(ws, dev)
-    st = lib.tgs_embedding_grad(_ptr(tokens), _DTYPES[tokens.dtype], T, _ptr(grad), gt, V, D, scale, _ptr(out), ot,
-                                bool(accumulate), ws.data_ptr(), ws.numel(), stream)
+    st = lib.tgs_embedding_grad(tokens.data_ptr(), _DTYPES[tokens.dtype], T, grad.data_ptr(), gt, V, D, scale,
+                                out.data_ptr(), ot, bool(accumulate), ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_embedding_grad")
     if given:
@@ -866,7 +866,7 @@ def newton_schulz(x: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ_CO
     _require_any(x, _FLOATS, "x")
     dev = x.device
     b, m, n = _matrices(x, "x")
-    if _differentiable(x, "x", out):
+    if x.requires_grad and _differentiable("x", out):
         return _NewtonSchulz.apply(x, steps, coefficients, eps, ws)
     given = out is not None
     if not given:
