@@ -3,8 +3,10 @@
 // Lookup: out[t] = scale * table[token[t]], a row of zeros where token[t] < 0.
 // One pass, bound by HBM: every thread moves four vectors of 16 bytes (of the
 // wider of the two types), all four rows' loads in flight before the first
-// store.  131,072 rows of 2,048 in bf16 from a table of 128,000: 184 us, 3.6 TB/s
-// of a copy's 5.2; one row: 3 us of a call's 8.
+// store.  131,072 rows of 2,048 in bf16 from a table of 128,000: 184 us.  Its
+// 32,600 distinct rows are 134 MB, but each of the eight L2s fetches for itself,
+// 225 MB if it kept all and 301 as counted: with the 537 MB written 4.6 TB/s of a
+// copy's 5.2.  One row: 3 us of a call's 8.
 //
 // Gradient: out[v] (+)= scale * sum of grad[t] over the places with
 // token[t] == v.  Atomic adds would make the sums depend on their order, and a
@@ -50,9 +52,12 @@ struct LookupArgs {
 
 constexpr int kLookupThreads = 256;
 constexpr int kLookupUnroll = 4;
-// Out of this size on, stores pass the caches by, so that these keep the table's
-// frequent rows (537 MB from 128,000 rows of 2,048 in bf16: 206 -> 141 us; 34 MB:
-// 12.8 plain, 13.9 past the caches).
+// Above this size stores pass the caches by, so that these keep the table's
+// frequent rows.  From 128,000 rows of 2,048 in bf16, inputs changing, plain and
+// past the caches: 8 MB 8.9 and 9.1 us, 34 MB 14.7 and 12.3, 134 MB 52 and 36, 537
+// MB 197 and 185.  What reads a smaller result next still finds it in the caches:
+// with an addition over the result 50 MB take 36.3 and 37.6, 67 MB 47.1 and 48.6,
+// 100 MB 69.7 and 68.4, 537 MB 374 and 362.
 constexpr size_t kStreamingBytes = (size_t)64 << 20;
 
 template <class TI, class TO, class I, int E, bool STREAMING>
@@ -99,10 +104,16 @@ __global__ __launch_bounds__(kLookupThreads) void k_lookup(LookupArgs a) {
 constexpr int kTokenThreads = 512;
 constexpr int kTokenWaves = kTokenThreads / kWave;
 constexpr int kDigitBits = 10;
+// Sorting workgroups, one for 2,048 places.  131,072 places of 16 columns take 64
+// us with 32 of them, 55 with 64, 56 with 128; 1,000,000 238 with 64, 199 with 128,
+// 189 with 256, which double the counts that each reads.  Of 1,024 places each
+// 16,384 take 36 us instead of 40, 131,072 56 instead of 55.
 constexpr int kTokenBlocks = 128;
 constexpr int kOneThreads = 1024;
 constexpr int kOneWaves = kOneThreads / kWave;
-constexpr int kOneMaxT = 4096;  // places that one workgroup sorts in LDS
+// Places that one workgroup sorts, in one launch: what LDS holds (4,096 of 64
+// columns in 25,000 rows: 31 us, 37 by several; 2,500: 27 and 34).
+constexpr int kOneMaxT = 4096;
 
 struct SortArgs {
   const void* tokens;
@@ -398,7 +409,7 @@ __global__ __launch_bounds__(kGradThreads) void k_grad_chunks(GradArgs a) {
   const u32 n = (u32)min((u64)a.chunk, (u64)a.T - first);
   const u32* keys = a.keys + first;
   const u32* places = a.places + first;
-  if (keys[0] == a.V) return;  // masked places only
+  if (keys[0] == a.V) return;  // masked places only; behind others their rows may be loaded, and are never added
   const u32 vec = slab * kWave + lane_id();
   const bool here = vec < a.nv;
   int skip;
@@ -667,7 +678,10 @@ static bool grad_plan(int64_t T, int64_t V, int64_t D, tgs_dtype tg, tgs_dtype t
   p->nv = (u32)((D + p->E - 1) / p->E);
   p->slabs = (p->nv + kWave - 1) / kWave;
   // chunks: long enough that partial rows are few, short enough that about
-  // 4096 waves (two a SIMD) have work
+  // 4096 waves (four a SIMD) have work.  For 1,024, 2,048, 4,096, 8,192 and 16,384
+  // 16,384 places of 1,024 take 85, 62, 50, 48 and 48 us, 131,072 of 256 103, 103,
+  // 78, 69 and 79, of 2,048 302, 303, 302, 302 and 330; each doubling doubles the
+  // partial rows' memory too
   p->chunk = 64;
   while (p->chunk > 8 && (u64)T / p->chunk * p->slabs < 4096) p->chunk >>= 1;
   p->chunks = (u32)(((u64)T + p->chunk - 1) / p->chunk);

@@ -19,11 +19,12 @@
 // it while these are multiplied.  Tiles are 64 to 256 a side, whichever a model
 // of the time finds best (pick_shape): large ones read less from L2 and feed the
 // matrix cores better, small ones fill the device.  At 4,096 square the update
-// takes 256 tiles of 256 in 142 us (a library's product of that size takes 114),
-// at a clock that the power limit holds near 1.7 GHz; the symmetric products
-// take 253 tiles of 192 in 85 us rather than 136 of 256, which leave half the
-// device idle, in 120.  Few tiles with long sums are shared by workgroups (the
-// gram of 200 x 8,000 in fp32: 59 -> 28 us).
+// takes 256 tiles of 256 in 142 us; a library's product of that size, which writes
+// 2 bytes an entry of its result where this reads and writes 12, takes 114.  The
+// clock falls to about 1.7 GHz under it, and fewer cycles no longer shortened it.
+// The symmetric products take 253 tiles of 192 in 85 us rather than 136 of 256,
+// which leave half the device idle, in 120.  Few tiles with long sums are shared
+// by workgroups (the gram of 200 x 8,000 in fp32: 59 -> 28 us).
 // Tiles of 64 and 128 are bound by the rate at which a compute unit fills its
 // LDS, about 65 GB/s: 1,000 x 1,533 in fp32 takes 13 to 21 us a product.
 //
@@ -784,8 +785,12 @@ static int64_t tiles_of(const NsPlan& p, int64_t batch, int shape, bool symmetri
   return batch * (symmetric ? tm * (tm + 1) / 2 : tm * tn);
 }
 
-// Stages (of 128) a workgroup takes where tiles are shared: at most four
-// workgroups a tile, and four stages at least.
+// Stages (of 128) a workgroup takes where tiles are shared: as many workgroups as
+// make about four a tile, runs of four stages or more.  With one, two, four, eight
+// and sixteen a tile the gram lets 256 x 4,096 in bf16 take 169, 146, 132, 135 and
+// 135 us, 512 x 8,192 289, 235, 214, 241 and 241, two of 256 x 4,096 in fp32 263,
+// 212, 187, 190 and 223, 129 x 2,029 171, 153, 142, 147 and 147, and 200 x 8,000
+// 401, 281, 229, 208 and 219.  Runs of two or eight stages and more change nothing.
 static int64_t pick_share(int64_t tiles, int64_t nt) {
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(256, std::min(tiles * 4, tiles * nt / 4)));
   return (tiles * nt + most - 1) / most;
