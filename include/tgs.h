@@ -318,13 +318,14 @@ size_t tgs_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t co
  * 1 <= batch <= 65535, 1 <= rows, cols <= 65536, 1 <= steps <= 64, eps >= 0.
  * Coefficients with which a singular value that starts in [0, 1] could pass
  * 2^30 are refused.  The products use fp16 operands scaled by powers of two
- * and fp32 sums.  fp32 and fp16 results are as exact as with fp32 products
- * (three fp16 products each).  bf16 results take single products: before the
- * final rounding (1.7e-3 of the 2-norm) they are off by at most half of that for
- * matrices like gradients, whose singular values fall off into noise.  Matrices
- * of low rank come out up to 2.8e-3 off where the shorter side is 65 to 128,
- * 1.6e-3 at 256, 0.9e-3 at 512, and 1.1e-3 from 33 to 64, 1.7e-3 below.  A NaN
- * or infinity in x makes its matrix's result NaN.  Equal inputs give equal bits.
+ * and fp32 sums.  fp32 and fp16 results, and bf16 ones whose shorter side is at
+ * most 32, are as exact as with fp32 products (three fp16 products each).  Other
+ * bf16 results take single products: before the final rounding (1.7e-3 of the
+ * 2-norm) they are off by at most half of that for matrices like gradients, whose
+ * singular values fall off into noise.  Matrices of low rank come out up to 1.6e-3
+ * off where the shorter side is 33 to 64, 5e-3 at 65, 3e-3 at 128, 2e-3 at 256 and
+ * 1.4e-3 at 512.  A NaN or infinity in x makes its matrix's result NaN.  Equal
+ * inputs give equal bits.
  */
 tgs_status tgs_newton_schulz(const void* x, tgs_dtype dtype, int64_t batch, int64_t rows, int64_t cols, int32_t steps,
                              float a, float b, float c, float eps, void* out, void* workspace, size_t workspace_bytes,

@@ -38,11 +38,12 @@
 // (2-norm) off, below the 1.7e-3 of the final rounding, where rounding X, A and P
 // whole to fp16 gives 1.2e-3 to 4.3e-3 and to bf16 1.3e-2 to 2.4e-2.  What X's
 // rounding puts into directions in which a matrix of low rank is empty grows by
-// the first coefficient a step: such a matrix comes out up to 2.8e-3 off with a
-// shorter side of 128, 1.6e-3 with 256, 0.9e-3 with 512.  With fp32 and fp16
-// results every operand is high + low and a product is three (high low + low high
-// + high high): as exact as fp32 products (1.4e-6 to 2.3e-6 against 1.3e-6 to
-// 2.0e-6).  fp16 rounds at 2.1e-4, which single products' 2e-4 to 8e-4 would pass.
+// the first coefficient a step: such a matrix comes out up to 5e-3 off with a
+// shorter side of 65, 3e-3 with 128, 2e-3 with 256, 1.4e-3 with 512.  With fp32
+// and fp16 results every operand is high + low and a product is three (high low +
+// low high + high high): as exact as fp32 products (1.4e-6 to 2.3e-6 against
+// 1.3e-6 to 2.0e-6).  fp16 rounds at 2.1e-4, which single products' 2e-4 to 8e-4
+// would pass.
 //
 // Range.  The singular values of X start in [0, 1]; the host bounds them after
 // every step by the polynomial's extrema, and scales X, A and P by powers of

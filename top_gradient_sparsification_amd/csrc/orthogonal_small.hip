@@ -1,6 +1,7 @@
 // Newton-Schulz products of matrices whose shorter side is at most 64 (the
-// formulas, and what is rounded, as in orthogonal.hip, but that the update takes
-// X's low parts for every type).
+// formulas, and what is rounded, as in orthogonal.hip, but that with a shorter side
+// of up to 32 every type takes the three products, and above the update takes X's
+// low parts for every type).
 //
 // Such a step has little to compute: what costs is the launches and the
 // barriers.  Here X stays in registers, in fp32.  A wave owns 16 CB columns of
@@ -318,9 +319,9 @@ __global__ __launch_bounds__(kSmThreads) void k_ns_small(SmallArgs a, StepScales
   // X <- (a + D_P) X + E_P X in both orders, or the result in memory's order.  X's
   // low parts are multiplied for bf16 results too: what its rounding puts into
   // directions in which a matrix of low rank is empty grows by the first coefficient
-  // a step, and the more the smaller the matrix (8 x 8 of rank 1: 1.6e-2 off, with
-  // them 7e-4; 64 x 64 of rank 8: 3.0e-3 and 7e-4).  64 x 512 takes 46 us with
-  // them, 39 without, 63 with all three products; 64 x 64 takes 23, 20 and 27.
+  // a step, and the more the smaller the matrix (64 x 64 of rank 8: 3.0e-3 off, with
+  // them 7e-4).  64 x 512 takes 46 us with them, 39 without, 63 with all three
+  // products; 64 x 64 takes 23, 20 and 27.
   auto update = [&](float sx, float sp, float next, auto last) {
     constexpr bool LAST = decltype(last)::value;
     const float to_x = next / sx, to_acc = next / (sp * sx);  // powers of two
@@ -484,9 +485,12 @@ static void launch_small(const SmallPlan& p, SmallArgs a, const StepScales& s, i
 template <bool SPLIT>
 static void launch_small_any(const SmallPlan& p, const SmallArgs& a, const StepScales& s, int batch, hipStream_t stream) {
   if (p.rb == 2) {
-    if (p.cb == 2) launch_small<2, 2, SPLIT>(p, a, s, batch, stream);
-    else if (p.cb == 4) launch_small<2, 4, SPLIT>(p, a, s, batch, stream);
-    else launch_small<2, 8, SPLIT>(p, a, s, batch, stream);
+    // three products for bf16 results too: single ones, even with X's low parts in the
+    // update, leave up to 3.7e-3 of matrices so small, twice the result's rounding (30 x
+    // 1,024 takes 42 us instead of 36, 32 x 32 11.9 instead of 10.5)
+    if (p.cb == 2) launch_small<2, 2, true>(p, a, s, batch, stream);
+    else if (p.cb == 4) launch_small<2, 4, true>(p, a, s, batch, stream);
+    else launch_small<2, 8, true>(p, a, s, batch, stream);
   } else {
     if (p.cb == 2) launch_small<4, 2, SPLIT>(p, a, s, batch, stream);
     else launch_small<4, 4, SPLIT>(p, a, s, batch, stream);
