@@ -279,7 +279,8 @@ size_t tgs_embedding_lookup_workspace_bytes(int64_t T);
  *             error word, and its row is +0.
  *   table     [V][D] fp32, bf16 or fp16, row-major.
  *   out       [T][D] fp32, bf16 or fp16: fp32(table) * scale, rounded once.
- * 0 <= T, 1 <= V, 1 <= D, each at most 2^31 - 1; scale is finite.
+ * 0 <= T, 1 <= V, 1 <= D, each at most 2^31 - 1; scale is finite.  Sizes that
+ * would take a launch of 2^32 threads (2^34 16-byte vectors of out) are refused.
  */
 tgs_status tgs_embedding_lookup(const void* tokens, tgs_dtype tokens_dtype, int64_t T, const void* table,
                                 tgs_dtype table_dtype, int64_t V, int64_t D, float scale, void* out,
@@ -297,7 +298,8 @@ size_t tgs_embedding_grad_workspace_bytes(int64_t T, int64_t V, int64_t D, tgs_d
  *   accumulate != 0: out = out + S, rows that no token names are not touched
  * The sums are fp32, in an order that depends on the tokens alone, so equal
  * inputs give equal bits.  Masked places (negative tokens) and tokens >= V
- * (bad-input bit) add to nothing: their rows of grad may hold anything.
+ * (bad-input bit) add to nothing: their rows of grad may hold anything.  Sizes
+ * that would take a launch of 2^32 threads are refused, as the lookup's are.
  */
 tgs_status tgs_embedding_grad(const void* tokens, tgs_dtype tokens_dtype, int64_t T, const void* grad,
                               tgs_dtype grad_dtype, int64_t V, int64_t D, float scale, void* out, tgs_dtype out_dtype,
