@@ -67,7 +67,9 @@ __device__ __forceinline__ float muon_u(int nesterov, float beta, float g, float
 }
 
 // Partial sums of squares a matrix: 4,096 entries each, at most 1,024 and about
-// 2,048 for all matrices of a stack.
+// 2,048 for all matrices of a stack.  2,048 to 16,384 entries, and at most 256 to
+// 2,048, change a call by 2% at most (4,096 square 1,574 to 1,580 us, eight of 1,024
+// 396 to 405).
 inline int norm_blocks(int64_t batch, int64_t count) {
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(1024, 2048 / batch));
   return (int)std::min(most, (count + 4095) / 4096);
