@@ -355,6 +355,142 @@ tgs_status tgs_muon_step(void* weight, tgs_dtype weight_dtype, const void* grad,
                          float weight_decay, int32_t steps, float a, float b, float c, float eps, void* workspace,
                          size_t workspace_bytes, hipStream_t stream);
 
+/* -------------------------------------------------------------------------
+ * Operators over rows, between a model's hidden states and its losses.  The
+ * conventions of the section above hold.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Layer norm of each row: out = (x - mean) rstd weight + bias with mean = sum x
+ * / D and rstd = 1 / sqrt(sum (x - mean)^2 / D + eps).
+ *   x         [T][D] fp32, bf16 or fp16; out [T][D] of any of them, x itself
+ *             included where the types agree.
+ *   weight, bias  [D] of one type, fp32, bf16 or fp16; either may be null (1, 0).
+ *   mean, rstd    [T] float, out, for the gradients; either may be null.
+ * 0 <= T <= 2^31 - 1, 1 <= D <= 2^24, eps >= 0.  The mean is known before the
+ * squares are summed, so a large mean costs no more than x's own rounding.
+ */
+tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T, int64_t D, const void* weight, const void* bias,
+                          tgs_dtype weight_dtype, float eps, void* out, tgs_dtype out_dtype, float* mean, float* rstd,
+                          hipStream_t stream);
+
+/* Bytes of workspace tgs_layer_norm_grad needs (0 if the sizes are invalid): up
+   to 512 partial rows of 2 D floats. */
+size_t tgs_layer_norm_grad_workspace_bytes(int64_t T, int64_t D);
+
+/*
+ * Gradients of the layer norm, with xh = (x - mean) rstd and gw = grad weight:
+ *   grad_x      = rstd (gw - sum gw / D - xh sum (gw xh) / D)
+ *   grad_weight = sum over rows of grad xh,  grad_bias = sum over rows of grad
+ *   grad      [T][D] fp32, bf16 or fp16; x, mean, rstd, weight as given to and
+ *             left by tgs_layer_norm.
+ *   grad_x    [T][D] of x's type; x itself, or grad where the types agree, included.
+ *   grad_weight, grad_bias  [D] of param_dtype; either may be null.
+ * The sums over rows are fp32, in an order that depends on the sizes and types
+ * alone: equal inputs give equal bits.
+ */
+tgs_status tgs_layer_norm_grad(const void* grad, tgs_dtype grad_dtype, const void* x, tgs_dtype x_dtype, int64_t T,
+                               int64_t D, const float* mean, const float* rstd, const void* weight,
+                               tgs_dtype weight_dtype, void* grad_x, void* grad_weight, void* grad_bias,
+                               tgs_dtype param_dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace tgs_token_logprobs needs (0 if the sizes or the type are
+   invalid): the header, and what slices of rows leave where rows are few. */
+size_t tgs_token_logprobs_workspace_bytes(int64_t T, int64_t V, tgs_dtype dtype, int32_t top);
+
+/*
+ * Log probabilities of given tokens under p = softmax(logits / temperature).
+ *   logits    [T] rows of V scores, fp32, bf16 or fp16, `ld` elements from row to
+ *             row (ld >= V; what lies between rows is not read).
+ *   tokens    [T] int32 or int64.  A negative token is a masked place: its row
+ *             is not read, and its results are +0 and -1.  A token >= V sets
+ *             the bad-input bit of the device error word and is masked too.
+ *   logprobs  [T] float: log p(token).
+ *   stats     [T][2] float: (r, l) with log sum e^(logits / temperature) = r /
+ *             temperature + l, for the gradient; here r is the largest score.
+ *   entropy   [T] float: -sum p log p; may be null.
+ *   top_indices, top_logprobs  [T][top] int32 and float: the `top` largest
+ *             scores of each row, ties to the lower index, and their log
+ *             probabilities; 0 <= top <= min(64, V).
+ * 1e-6 <= temperature <= 1e6.  A score of -inf has no probability (its log is
+ * -inf and it adds nothing to the entropy); the type's lowest finite value is a
+ * score like any other.  A row of which every score is -inf has log
+ * probabilities of -inf and entropy 0.  NaN or +inf in a row makes its
+ * log probabilities and entropy NaN; among alternatives a NaN ranks above all.
+ */
+tgs_status tgs_token_logprobs(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                              const void* tokens, tgs_dtype tokens_dtype, float temperature, float* logprobs,
+                              float* stats, float* entropy, int32_t top, int32_t* top_indices, float* top_logprobs,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The gradient of the logits:
+ *   out = (grad_logprobs (onehot(token) - p) - grad_entropy p (log p + entropy)) / temperature
+ *   stats     as tgs_token_logprobs left them; entropy too where grad_entropy is given.
+ *   grad_logprobs, grad_entropy  [T] float; either may be null, not both.
+ *   out       [T] rows of V of the logits' type, ld_out elements apart (what lies
+ *             between rows is left as it is); the logits themselves with ld_out
+ *             == ld included.
+ * Rows of masked places, and rows of which every score is -inf, are +0.  The
+ * workspace is a header (32 KB).
+ */
+tgs_status tgs_token_logprobs_grad(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                   const void* tokens, tgs_dtype tokens_dtype, float temperature, const float* stats,
+                                   const float* grad_logprobs, const float* entropy, const float* grad_entropy,
+                                   void* out, int64_t ld_out, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+/* Bytes of workspace tgs_distillation_loss and tgs_distillation_loss_and_grad
+   need (0 if the sizes or the type are invalid). */
+size_t tgs_distillation_workspace_bytes(int64_t T, int64_t V, tgs_dtype dtype);
+
+/*
+ * Distillation from a teacher's top logits: KL(q || p) of each row with p =
+ * softmax(logits / temperature) over all V and q = softmax(teacher /
+ * temperature) over the row's slots,
+ *   loss = sum over slots of q (log q - log p(index)).
+ *   logits, ld  as tgs_token_logprobs.
+ *   indices   [T][K] int32 or int64: the tokens of the teacher's K slots, 1 <=
+ *             K <= 1024, in any order; a negative one is an empty slot, one >= V
+ *             sets the bad-input bit and is empty too.  An index may stand in
+ *             several slots.
+ *   teacher   [T][K] fp32, bf16 or fp16 scores (logits, or log probabilities:
+ *             what they have in common cancels); -inf gives a slot q = 0.
+ *   loss      [T] float.  +inf where a slot with q > 0 has a student's score of -inf.
+ *   stats     [T][2] float as tgs_token_logprobs', for the gradient; may be null.
+ * A row without a slot of q > 0 is a masked place: loss 0, gradient +0, its
+ * logits not needed.  NaN in a row's logits, or in its teacher's scores, and
+ * +inf in either make its loss and gradient NaN.
+ */
+tgs_status tgs_distillation_loss(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                 const void* indices, tgs_dtype indices_dtype, const void* teacher,
+                                 tgs_dtype teacher_dtype, int64_t K, float temperature, float* loss, float* stats,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The gradient of the logits: out = grad_loss (p - q) / temperature, where q
+ * sums the slots that name a token.
+ *   grad_loss [T] float; stats as tgs_distillation_loss left them.
+ *   out, ld_out  as tgs_token_logprobs_grad, the logits themselves included.
+ * Rows of which every score is -inf are +0.  The workspace is a header (32 KB).
+ */
+tgs_status tgs_distillation_grad(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                 const void* indices, tgs_dtype indices_dtype, const void* teacher,
+                                 tgs_dtype teacher_dtype, int64_t K, float temperature, const float* stats,
+                                 const float* grad_loss, void* out, int64_t ld_out, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Both in one call, for rows whose weights are known: the losses, and in out the
+ * gradient of sum over rows of weights loss (weights [T] float, or null for 1).
+ * The logits come from memory once, where the two calls above read them twice.
+ */
+tgs_status tgs_distillation_loss_and_grad(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                          const void* indices, tgs_dtype indices_dtype, const void* teacher,
+                                          tgs_dtype teacher_dtype, int64_t K, float temperature, const float* weights,
+                                          float* loss, void* out, int64_t ld_out, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+
 /* Waits for `stream`, then reads and clears the device error word of
    `workspace`: TGS_OK if no kernel flagged a problem since it was last read,
    TGS_EINVAL for an input index outside its range (a merge row's index out

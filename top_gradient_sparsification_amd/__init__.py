@@ -30,15 +30,22 @@ Operators of the training step around it:
   scaling, and the table's dense gradient by sorted tokens.
 * ``newton_schulz`` / ``muon_step`` -- a matrix orthogonalised by Newton-Schulz
   products, and the Muon update of weight matrices that takes it.
+* ``layer_norm`` / ``layer_norm_grad`` -- layer norm of rows and its gradients.
+* ``token_logprobs`` / ``token_logprobs_grad`` -- log probabilities of given
+  tokens with entropy and top alternatives, and the logits' gradient.
+* ``distillation_loss`` / ``distillation_grad`` / ``distillation_loss_and_grad``
+  -- KL divergence from a teacher's top logits, its gradient, and both at once.
 
 There is no fallback: if ``libtgs.so`` is missing or cannot be loaded, every
 call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -136,6 +143,28 @@ def _load():
         lib.tgs_muon_step.argtypes = [vp, i32, vp, i32, vp, i64, i64, i64, f32, f32, i32, f32, i32, f32, f32, f32, f32,
                                       vp, sz, vp]
         lib.tgs_muon_step.restype = i32
+        lib.tgs_layer_norm.argtypes = [vp, i32, i64, i64, vp, vp, i32, f32, vp, i32, vp, vp, vp]
+        lib.tgs_layer_norm.restype = i32
+        lib.tgs_layer_norm_grad_workspace_bytes.argtypes = [i64, i64]
+        lib.tgs_layer_norm_grad_workspace_bytes.restype = sz
+        lib.tgs_layer_norm_grad.argtypes = [vp, i32, vp, i32, i64, i64, vp, vp, vp, i32, vp, vp, vp, i32, vp, sz, vp]
+        lib.tgs_layer_norm_grad.restype = i32
+        lib.tgs_token_logprobs_workspace_bytes.argtypes = [i64, i64, i32, i32]
+        lib.tgs_token_logprobs_workspace_bytes.restype = sz
+        lib.tgs_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, i32, f32, vp, vp, vp, i32, vp, vp, vp, sz, vp]
+        lib.tgs_token_logprobs.restype = i32
+        lib.tgs_token_logprobs_grad.argtypes = [vp, i32, i64, i64, i64, vp, i32, f32, vp, vp, vp, vp, vp, i64, vp, sz,
+                                                vp]
+        lib.tgs_token_logprobs_grad.restype = i32
+        lib.tgs_distillation_workspace_bytes.argtypes = [i64, i64, i32]
+        lib.tgs_distillation_workspace_bytes.restype = sz
+        slots = [vp, i32, i64, i64, i64, vp, i32, vp, i32, i64, f32]
+        lib.tgs_distillation_loss.argtypes = [*slots, vp, vp, vp, sz, vp]
+        lib.tgs_distillation_loss.restype = i32
+        lib.tgs_distillation_grad.argtypes = [*slots, vp, vp, vp, i64, vp, sz, vp]
+        lib.tgs_distillation_grad.restype = i32
+        lib.tgs_distillation_loss_and_grad.argtypes = [*slots, vp, vp, vp, i64, vp, sz, vp]
+        lib.tgs_distillation_loss_and_grad.restype = i32
         lib.tgs_status_string.argtypes = [i32]
         lib.tgs_status_string.restype = ctypes.c_char_p
         lib.tgs_last_error.argtypes = []
@@ -942,6 +971,490 @@ def muon_step(weight: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, 
     return weight
 
 
+# ------------------------------------------ rows, from hidden states to losses --
+def _on(dev):
+    """Launches go to the current device: the tensors' own for the time of a call."""
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+class _NoWayBack(torch.autograd.Function):
+    """The result of a call that has no gradient, on inputs that require one: going back through it raises."""
+
+    @staticmethod
+    def forward(ctx, what, call, *inputs):
+        ctx.what = what
+        return call()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise NotImplementedError("%s has no gradient: detach its inputs" % ctx.what)
+
+
+def _tracked(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _spaced_rows(t, name, dtypes, device=None):
+    """(rows, columns, elements from row to row) of ``[..., V]``, whose rows may lie further apart than they are long."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be one of %s, got %s" % (name, ", ".join(map(str, dtypes)), t.dtype))
+    if not t.is_cuda:
+        raise TypeError("%s must be a GPU tensor" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dim() < 1:
+        raise ValueError("%s must have a last axis of scores" % name)
+    V = t.shape[-1]
+    rows = t.numel() // V if V else 0
+    if t.is_contiguous():
+        return rows, V, V
+    if V > 1 and t.stride(-1) != 1:
+        raise ValueError("%s must be contiguous along its last axis" % name)
+    gap = run = None  # elements from row to row; from one index of the next axis to another
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if gap is None:
+            gap = run = stride
+        if stride != run:
+            raise ValueError("%s must have rows a fixed number of elements apart" % name)
+        run = stride * size
+    gap = V if gap is None else gap
+    if gap < V:
+        raise ValueError("%s has rows that overlap" % name)
+    return rows, V, gap
+
+
+def _places(t, dtypes, name, device, shape):
+    _require_any(t, dtypes, name, device)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _rows_out(logits, out):
+    """(out, its elements from row to row, whether it was given) of a gradient of ``logits``."""
+    if out is None:
+        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), logits.shape[-1], False
+    _, _, gap = _spaced_rows(out, "out", (logits.dtype,), logits.device)
+    if out.shape != logits.shape:
+        raise ValueError("out must have shape %s" % (tuple(logits.shape),))
+    return out, gap, True
+
+
+def _row_scratch(ws, need, dev, stream, what):
+    if need == 0:
+        raise ValueError("invalid sizes of %s" % what)
+    if ws is None:
+        return _scratch("rows", need, dev, stream)
+    _require_ws(ws, dev)
+    return ws
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, out_dtype):
+        y, mean, rstd = layer_norm(x, weight, bias, eps, out_dtype, return_stats=True)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.param_dtype = (weight if weight is not None else bias).dtype if (
+            weight is not None or bias is not None) else None
+        ctx.mark_non_differentiable(mean, rstd)
+        ctx.set_materialize_grads(False)
+        return y, mean, rstd
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, _mean, _rstd):
+        if grad is None:
+            return None, None, None, None, None
+        x, weight, mean, rstd = ctx.saved_tensors
+        _, need_w, need_b = ctx.needs_input_grad[:3]
+        gx, gw, gb = layer_norm_grad(grad.contiguous(), x, mean, rstd, weight, params=need_w or need_b,
+                                     param_dtype=ctx.param_dtype)
+        return gx, gw if need_w else None, gb if need_b else None, None, None
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+               eps: float = 1e-5, out_dtype=None, out=None, return_stats: bool = False):
+    """Layer norm over the last axis: ``(x - mean) * rstd * weight + bias``
+    with ``rstd = 1 / sqrt(var + eps)``.
+
+    ``x`` is fp32, bf16 or fp16; ``weight`` and ``bias`` (``[D]``, one type of
+    the three) may each be left out.  The result has ``x``'s shape and the type
+    ``out_dtype`` (``x``'s if not given); ``out`` may be ``x`` itself.  With
+    ``return_stats`` the call returns ``(y, mean, rstd)``, fp32 of the shape
+    ``x.shape[:-1]``, as ``layer_norm_grad`` takes them.  Sums are fp32.
+
+    Differentiable in ``x``, ``weight`` and ``bias``; not with ``out``."""
+    _require_any(x, _FLOATS, "x")
+    dev = x.device
+    if x.dim() < 1:
+        raise ValueError("x must have a last axis")
+    D = x.shape[-1]
+    wt = None
+    for p, name in ((weight, "weight"), (bias, "bias")):
+        if p is None:
+            continue
+        _places(p, _FLOATS if wt is None else (wt,), name, dev, (D,))
+        wt = p.dtype
+    if _tracked(x, weight, bias):
+        if out is not None:
+            raise RuntimeError("an input requires a gradient, which a call with out= has not")
+        y, mean, rstd = _LayerNorm.apply(x, weight, bias, eps, out_dtype)
+        return (y, mean, rstd) if return_stats else y
+    given = out is not None
+    if not given:
+        out_dtype = out_dtype or x.dtype
+        if out_dtype not in _FLOATS:
+            raise TypeError("out_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
+        out = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    else:
+        _places(out, _FLOATS if out_dtype is None else (out_dtype,), "out", dev, x.shape)
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = x.new_empty((2, *x.shape[:-1]), dtype=torch.float32)
+    with _on(dev):
+        st = _load().tgs_layer_norm(x.data_ptr(), _DTYPES[x.dtype], x.numel() // D if D else 0, D,
+                                    None if weight is None else weight.data_ptr(),
+                                    None if bias is None else bias.data_ptr(), 0 if wt is None else _DTYPES[wt], eps,
+                                    out.data_ptr(), _DTYPES[out.dtype], _ptr(mean), _ptr(rstd), _stream_handle(dev))
+    if st:
+        _check(st, "tgs_layer_norm")
+    if given:
+        _written(out)
+    return (out, mean, rstd) if return_stats else out
+
+
+def layer_norm_grad_workspace_bytes(T: int, D: int) -> int:
+    return int(_load().tgs_layer_norm_grad_workspace_bytes(T, D))
+
+
+def layer_norm_grad(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                    weight: torch.Tensor | None = None, params: bool = True, param_dtype=None, out=None,
+                    ws: torch.Tensor | None = None):
+    """The gradients of ``layer_norm``: ``(grad_x, grad_weight, grad_bias)``.
+
+    ``grad`` has ``x``'s shape, ``mean`` and ``rstd`` are what the forward pass
+    left.  ``grad_x`` has ``x``'s type and may go to ``out``, which may be ``x``
+    or (of the same type) ``grad`` itself.  ``grad_weight`` and ``grad_bias``
+    are sums over all rows, ``[D]`` of ``param_dtype`` (``weight``'s type, fp32
+    without one), and ``None`` unless ``params``.  Sums are fp32 in a fixed
+    order: equal inputs give equal bits.  It has no gradient itself."""
+    _require_any(x, _FLOATS, "x")
+    dev = x.device
+    if x.dim() < 1:
+        raise ValueError("x must have a last axis")
+    D = x.shape[-1]
+    _places(grad, _FLOATS, "grad", dev, x.shape)
+    _places(mean, (torch.float32,), "mean", dev, x.shape[:-1])
+    _places(rstd, (torch.float32,), "rstd", dev, x.shape[:-1])
+    if weight is not None:
+        _places(weight, _FLOATS, "weight", dev, (D,))
+    if _tracked(grad, x, mean, rstd, weight):
+        if out is not None:
+            raise RuntimeError("an input requires a gradient, which a call with out= has not")
+        results = _NoWayBack.apply("layer_norm_grad", lambda: tuple(
+            r for r in layer_norm_grad(grad, x, mean, rstd, weight, params, param_dtype, ws=ws) if r is not None),
+            grad, x, mean, rstd, weight)
+        return results if params else (results[0], None, None)
+    given = out is not None
+    if not given:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _places(out, (x.dtype,), "out", dev, x.shape)
+    gw = gb = None
+    if params:
+        param_dtype = param_dtype or (torch.float32 if weight is None else weight.dtype)
+        if param_dtype not in _FLOATS:
+            raise TypeError("param_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
+        gw, gb = (torch.empty(D, dtype=param_dtype, device=dev) for _ in range(2))
+    T = x.numel() // D if D else 0
+    lib = _load()
+    with _on(dev):
+        stream = _stream_handle(dev)
+        ws = _row_scratch(ws, lib.tgs_layer_norm_grad_workspace_bytes(T, D), dev, stream, "layer_norm_grad")
+        st = lib.tgs_layer_norm_grad(grad.data_ptr(), _DTYPES[grad.dtype], x.data_ptr(), _DTYPES[x.dtype], T, D,
+                                     mean.data_ptr(), rstd.data_ptr(), None if weight is None else weight.data_ptr(),
+                                     0 if weight is None else _DTYPES[weight.dtype], out.data_ptr(), _ptr(gw),
+                                     _ptr(gb), _DTYPES[param_dtype] if params else 0, ws.data_ptr(), ws.numel(),
+                                     stream)
+    if st:
+        _check(st, "tgs_layer_norm_grad")
+    if given:
+        _written(out)
+    return out, gw, gb
+
+
+class TokenLogprobs(NamedTuple):
+    """What ``token_logprobs`` returns; what was not asked for is ``None``."""
+    logprobs: torch.Tensor
+    entropy: torch.Tensor | None
+    top_logprobs: torch.Tensor | None
+    top_indices: torch.Tensor | None
+    stats: torch.Tensor
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, temperature, top, entropy, ws):
+        r = token_logprobs(logits, tokens, temperature, top, entropy, ws)
+        ctx.save_for_backward(logits, tokens, r.stats, r.entropy)
+        ctx.temperature = temperature
+        ctx.mark_non_differentiable(*(t for t in (r.top_logprobs, r.top_indices, r.stats) if t is not None))
+        ctx.set_materialize_grads(False)
+        return tuple(r)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, grad_entropy, *_):
+        if grad is None and grad_entropy is None:
+            return None, None, None, None, None, None
+        logits, tokens, stats, entropy = ctx.saved_tensors
+        grads = (None if g is None else g.contiguous() for g in (grad, grad_entropy))
+        g, ge = grads
+        return token_logprobs_grad(logits, tokens, stats, g, entropy, ge, ctx.temperature), None, None, None, None, None
+
+
+def token_logprobs_workspace_bytes(T: int, V: int, dtype=torch.float32, top: int = 0) -> int:
+    return int(_load().tgs_token_logprobs_workspace_bytes(T, V, _DTYPES[dtype], top))
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0, top: int = 0,
+                   entropy: bool = False, ws: torch.Tensor | None = None) -> TokenLogprobs:
+    """Log probabilities of given tokens under ``softmax(logits / temperature)``.
+
+    ``logits`` (fp32, bf16 or fp16, ``[..., V]``) may be a view whose rows lie
+    further apart than they are long (a padded vocabulary); ``tokens`` (int32 or
+    int64) has the shape ``logits.shape[:-1]``.  Returns a ``TokenLogprobs``
+    of fp32 ``logprobs``, with ``entropy`` the distribution's entropy, with
+    ``top`` (up to 64) the rows' largest scores as ``top_indices`` (int32, ties
+    to the lower index) and ``top_logprobs``, ``[..., top]``; and ``stats``, as
+    ``token_logprobs_grad`` takes them.
+
+    A negative token is a masked place: its row is not read and its results are
+    0 (alternatives -1); a token >= V too, and it sets the bad-input bit that
+    ``check_device_error(ws)`` reports.  Scores of -inf have no probability.
+
+    Differentiable in ``logits`` through ``logprobs`` and ``entropy``."""
+    T, V, gap = _spaced_rows(logits, "logits", _FLOATS)
+    dev = logits.device
+    _places(tokens, _TOKENS, "tokens", dev, logits.shape[:-1])
+    if _tracked(logits):
+        return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, top, entropy, ws))
+    top = int(top)
+    shape = tokens.shape
+    logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
+    stats = torch.empty((*shape, 2), dtype=torch.float32, device=dev)
+    ent = torch.empty(shape, dtype=torch.float32, device=dev) if entropy else None
+    at = values = None
+    if top > 0:
+        at = torch.empty((*shape, top), dtype=torch.int32, device=dev)
+        values = torch.empty((*shape, top), dtype=torch.float32, device=dev)
+    lib = _load()
+    dt = _DTYPES[logits.dtype]
+    with _on(dev):
+        stream = _stream_handle(dev)
+        need = lib.tgs_token_logprobs_workspace_bytes(T, V, dt, top)
+        ws = _row_scratch(ws, need, dev, stream, "token_logprobs: V=%d, top=%d" % (V, top) if need == 0 else "")
+        st = lib.tgs_token_logprobs(logits.data_ptr(), dt, T, V, gap, tokens.data_ptr(), _DTYPES[tokens.dtype],
+                                    temperature, logprobs.data_ptr(), stats.data_ptr(), _ptr(ent), top, _ptr(at),
+                                    _ptr(values), ws.data_ptr(), ws.numel(), stream)
+    if st:
+        _check(st, "tgs_token_logprobs")
+    return TokenLogprobs(logprobs, ent, values, at, stats)
+
+
+def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, stats: torch.Tensor,
+                        grad_logprobs: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                        grad_entropy: torch.Tensor | None = None, temperature: float = 1.0, out=None,
+                        ws: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of ``token_logprobs`` with respect to its logits:
+    ``(grad_logprobs (onehot(token) - p) - grad_entropy p (log p + entropy)) /
+    temperature``, of the logits' type and shape.
+
+    ``stats`` (and ``entropy``, with ``grad_entropy``) are what the forward pass
+    left; either incoming gradient may be left out.  ``out`` may be the logits
+    themselves, which are then overwritten.  Masked places, and rows of which
+    every score is -inf, give zeros.  It has no gradient itself."""
+    T, V, gap = _spaced_rows(logits, "logits", _FLOATS)
+    dev = logits.device
+    shape = logits.shape[:-1]
+    _places(tokens, _TOKENS, "tokens", dev, shape)
+    _places(stats, (torch.float32,), "stats", dev, (*shape, 2))
+    if grad_logprobs is None and grad_entropy is None:
+        raise ValueError("grad_logprobs or grad_entropy must be given")
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs entropy")
+    for t, name in ((grad_logprobs, "grad_logprobs"), (entropy, "entropy"), (grad_entropy, "grad_entropy")):
+        if t is not None:
+            _places(t, (torch.float32,), name, dev, shape)
+    if _tracked(logits, stats, grad_logprobs, entropy, grad_entropy):
+        if out is not None:
+            raise RuntimeError("an input requires a gradient, which a call with out= has not")
+        return _NoWayBack.apply("token_logprobs_grad", lambda: token_logprobs_grad(
+            logits, tokens, stats, grad_logprobs, entropy, grad_entropy, temperature, ws=ws),
+            logits, stats, grad_logprobs, entropy, grad_entropy)
+    out, gap_out, given = _rows_out(logits, out)
+    with _on(dev):
+        stream = _stream_handle(dev)
+        ws = _row_scratch(ws, _HEADER_BYTES, dev, stream, "")
+        st = _load().tgs_token_logprobs_grad(
+            logits.data_ptr(), _DTYPES[logits.dtype], T, V, gap, tokens.data_ptr(), _DTYPES[tokens.dtype], temperature,
+            stats.data_ptr(), _ptr(grad_logprobs), _ptr(entropy), _ptr(grad_entropy), out.data_ptr(), gap_out,
+            ws.data_ptr(), ws.numel(), stream)
+    if st:
+        _check(st, "tgs_token_logprobs_grad")
+    if given:
+        _written(out)
+    return out
+
+
+def _slots(logits, indices, teacher):
+    """(rows, V, elements from row to row, K) of a distillation's inputs."""
+    T, V, gap = _spaced_rows(logits, "logits", _FLOATS)
+    dev = logits.device
+    _require_any(indices, _TOKENS, "teacher_indices", dev)
+    if indices.dim() != logits.dim() or indices.shape[:-1] != logits.shape[:-1]:
+        raise ValueError("teacher_indices must have the logits' shape but for its last axis, the slots")
+    _places(teacher, _FLOATS, "teacher_logits", dev, indices.shape)
+    if teacher.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("the teacher has no gradient: detach teacher_logits")
+    return T, V, gap, indices.shape[-1]
+
+
+class _DistillationLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, indices, teacher, temperature, ws):
+        loss, stats = distillation_loss(logits, indices, teacher, temperature, return_stats=True, ws=ws)
+        ctx.save_for_backward(logits, indices, teacher, stats)
+        ctx.temperature = temperature
+        ctx.mark_non_differentiable(stats)
+        ctx.set_materialize_grads(False)
+        return loss, stats
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, _stats):
+        if grad is None:
+            return None, None, None, None, None
+        logits, indices, teacher, stats = ctx.saved_tensors
+        return (distillation_grad(logits, indices, teacher, stats, grad.contiguous(), ctx.temperature), None, None,
+                None, None)
+
+
+def distillation_workspace_bytes(T: int, V: int, dtype=torch.float32) -> int:
+    return int(_load().tgs_distillation_workspace_bytes(T, V, _DTYPES[dtype]))
+
+
+def distillation_loss(logits: torch.Tensor, teacher_indices: torch.Tensor, teacher_logits: torch.Tensor,
+                      temperature: float = 1.0, return_stats: bool = False, ws: torch.Tensor | None = None):
+    """Distillation from a teacher's top logits: of each place KL(q || p) with
+    ``p = softmax(logits / temperature)`` over the vocabulary and ``q =
+    softmax(teacher_logits / temperature)`` over the place's slots.
+
+    ``logits`` is fp32, bf16 or fp16, ``[..., V]``, rows possibly further apart
+    than they are long; ``teacher_indices`` (int32 or int64) and
+    ``teacher_logits`` (fp32, bf16 or fp16) are ``[..., K]``, K up to 1,024.  A
+    negative index is an empty slot; an index >= V too, and it sets the
+    bad-input bit that ``check_device_error(ws)`` reports; an index may stand in
+    several slots.  A place without any slot is masked: loss 0, gradient 0.
+    Returns the losses, fp32 of the shape ``logits.shape[:-1]``; with
+    ``return_stats`` also the ``stats`` that ``distillation_grad`` takes.
+
+    Differentiable in ``logits``."""
+    T, V, gap, K = _slots(logits, teacher_indices, teacher_logits)
+    dev = logits.device
+    if _tracked(logits):
+        loss, stats = _DistillationLoss.apply(logits, teacher_indices, teacher_logits, temperature, ws)
+        return (loss, stats) if return_stats else loss
+    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=dev)
+    stats = torch.empty((*logits.shape[:-1], 2), dtype=torch.float32, device=dev) if return_stats else None
+    lib = _load()
+    dt = _DTYPES[logits.dtype]
+    with _on(dev):
+        stream = _stream_handle(dev)
+        ws = _row_scratch(ws, lib.tgs_distillation_workspace_bytes(T, V, dt), dev, stream, "distillation_loss")
+        st = lib.tgs_distillation_loss(logits.data_ptr(), dt, T, V, gap, teacher_indices.data_ptr(),
+                                       _DTYPES[teacher_indices.dtype], teacher_logits.data_ptr(),
+                                       _DTYPES[teacher_logits.dtype], K, temperature, loss.data_ptr(), _ptr(stats),
+                                       ws.data_ptr(), ws.numel(), stream)
+    if st:
+        _check(st, "tgs_distillation_loss")
+    return (loss, stats) if return_stats else loss
+
+
+def distillation_grad(logits: torch.Tensor, teacher_indices: torch.Tensor, teacher_logits: torch.Tensor,
+                      stats: torch.Tensor, grad_loss: torch.Tensor, temperature: float = 1.0, out=None,
+                      ws: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of ``distillation_loss`` with respect to its logits:
+    ``grad_loss (p - q) / temperature``, of the logits' type and shape.
+
+    ``stats`` are what the forward pass left.  ``out`` may be the logits
+    themselves, which are then overwritten.  Masked places, and rows of which
+    every score is -inf, give zeros.  It has no gradient itself."""
+    T, V, gap, K = _slots(logits, teacher_indices, teacher_logits)
+    dev = logits.device
+    _places(stats, (torch.float32,), "stats", dev, (*logits.shape[:-1], 2))
+    _places(grad_loss, (torch.float32,), "grad_loss", dev, logits.shape[:-1])
+    if _tracked(logits, stats, grad_loss):
+        if out is not None:
+            raise RuntimeError("an input requires a gradient, which a call with out= has not")
+        return _NoWayBack.apply("distillation_grad", lambda: distillation_grad(
+            logits, teacher_indices, teacher_logits, stats, grad_loss, temperature, ws=ws), logits, stats, grad_loss)
+    out, gap_out, given = _rows_out(logits, out)
+    with _on(dev):
+        stream = _stream_handle(dev)
+        ws = _row_scratch(ws, _HEADER_BYTES, dev, stream, "")
+        st = _load().tgs_distillation_grad(
+            logits.data_ptr(), _DTYPES[logits.dtype], T, V, gap, teacher_indices.data_ptr(),
+            _DTYPES[teacher_indices.dtype], teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], K, temperature,
+            stats.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), gap_out, ws.data_ptr(), ws.numel(), stream)
+    if st:
+        _check(st, "tgs_distillation_grad")
+    if given:
+        _written(out)
+    return out
+
+
+def distillation_loss_and_grad(logits: torch.Tensor, teacher_indices: torch.Tensor, teacher_logits: torch.Tensor,
+                               weights: torch.Tensor | None = None, temperature: float = 1.0, out=None,
+                               ws: torch.Tensor | None = None):
+    """``distillation_loss`` and the gradient of ``sum(weights * loss)`` with
+    respect to the logits in one call that reads the logits from memory once:
+    ``(loss, grad)``.
+
+    ``weights`` (fp32, ``logits.shape[:-1]``) are 1 if not given: a training
+    step over N places whose loss is their mean passes 1 / N.  ``out``, for the
+    gradient, may be the logits themselves, which are then overwritten.  It has
+    no gradient itself."""
+    T, V, gap, K = _slots(logits, teacher_indices, teacher_logits)
+    dev = logits.device
+    if weights is not None:
+        _places(weights, (torch.float32,), "weights", dev, logits.shape[:-1])
+    if _tracked(logits, weights):
+        if out is not None:
+            raise RuntimeError("an input requires a gradient, which a call with out= has not")
+        return _NoWayBack.apply("distillation_loss_and_grad", lambda: distillation_loss_and_grad(
+            logits, teacher_indices, teacher_logits, weights, temperature, ws=ws), logits, weights)
+    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=dev)
+    out, gap_out, given = _rows_out(logits, out)
+    lib = _load()
+    dt = _DTYPES[logits.dtype]
+    with _on(dev):
+        stream = _stream_handle(dev)
+        ws = _row_scratch(ws, lib.tgs_distillation_workspace_bytes(T, V, dt), dev, stream, "distillation_loss_and_grad")
+        st = lib.tgs_distillation_loss_and_grad(
+            logits.data_ptr(), dt, T, V, gap, teacher_indices.data_ptr(), _DTYPES[teacher_indices.dtype],
+            teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], K, temperature, _ptr(weights), loss.data_ptr(),
+            out.data_ptr(), gap_out, ws.data_ptr(), ws.numel(), stream)
+    if st:
+        _check(st, "tgs_distillation_loss_and_grad")
+    if given:
+        _written(out)
+    return loss, out
+
+
 def check_device_error(ws: torch.Tensor):
     """Waits for the current stream, then reads and clears the workspace's
     device error word: raises ValueError for bad merge input, TgsError for a
@@ -983,6 +1496,9 @@ __all__ = [
     "newton_schulz", "newton_schulz_workspace_bytes", "muon_step", "muon_workspace_bytes",
     "NEWTON_SCHULZ_COEFFICIENTS",
     "embedding_lookup", "embedding_lookup_workspace_bytes", "embedding_grad", "embedding_grad_workspace_bytes",
+    "layer_norm", "layer_norm_grad", "layer_norm_grad_workspace_bytes",
+    "TokenLogprobs", "token_logprobs", "token_logprobs_workspace_bytes", "token_logprobs_grad",
+    "distillation_loss", "distillation_grad", "distillation_loss_and_grad", "distillation_workspace_bytes",
     "profile_next_call", "profile_elapsed_ms", "library", "workspace",
     "TgsError", "OPT_TOPK_PATH", "OPT_MAIN_GRID", "LIB_PATH",
 ]

@@ -1,0 +1,617 @@
+// Layer norm over the last axis and its gradients on gfx950.
+//
+//   mean = sum x / D,  var = sum (x - mean)^2 / D,  rstd = 1 / sqrt(var + eps)
+//   y = xh w + b with xh = (x - mean) rstd
+//   dx = rstd (g w - sum(g w) / D - xh sum(g w xh) / D)
+//   dw = sum over rows of g xh,  db = sum over rows of g
+//
+// Bound by HBM: 8 and 14 operations a value that is read and written once.  A
+// row stays in the registers of the lanes that read it (8 lanes to 1,024,
+// several vectors each), so that the mean is known before the squares are
+// summed and no value is read twice.  Rows that registers do not hold are read
+// again, from the caches.
+#include <type_traits>
+
+#include "tgs_rows.h"
+
+namespace tgs {
+
+struct NormArgs {
+  const void* x;
+  const void* weight;
+  const void* bias;
+  void* out;
+  float* mean;
+  float* rstd;
+  int64_t T, row0;
+  u32 D;
+  int weight_dtype;
+  float eps;
+  bool streaming;
+};
+
+// Calls f(e) for the elements of vector [c, c + E) that lie in the row.
+template <int E, class F>
+__device__ __forceinline__ void in_row(u32 c, u32 n, F&& f) {
+  if (c + E <= n) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f(e);
+  } else if (c < n) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (c + e < n) f(e);
+  }
+}
+
+// Where the sum of squares passes fp32's range it is taken of values smaller by
+// this, beside which eps is nothing.
+constexpr float kShrink = 0x1p-80f;
+
+constexpr int norm_threads(int L) { return L > 256 ? L : 256; }
+
+// A row in L lanes of NV vectors of E elements each.
+template <class TX, class TY, int E, int L, int NV>
+__global__ __launch_bounds__(norm_threads(L)) void k_norm(NormArgs a) {
+  constexpr int NT = norm_threads(L);
+  __shared__ float s_red[2][L > kWave ? L / kWave : 1];
+  const int64_t row = a.row0 + (int64_t)blockIdx.x * (NT / L) + threadIdx.x / L;
+  const bool real = row < a.T;
+  const u32 D = a.D, t = threadIdx.x % L;
+  const TX* x = (const TX*)a.x + (real ? row : 0) * (int64_t)D;
+  float v[NV][E];
+  float sum[1] = {0.0f}, squares[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const u32 c = (i * L + t) * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[i][e] = 0.0f;
+    if (c < D) {
+      const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = to_f32(raw.v[e]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float part = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) part += v[i][e];
+    sum[0] += part;
+  }
+  group_reduce<Sum, L>(sum, s_red[0]);
+  const float mean = sum[0] / (float)D;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float part = 0.0f;
+    in_row<E>((i * L + t) * E, D, [&](int e) {
+      v[i][e] -= mean;
+      part = fmaf(v[i][e], v[i][e], part);
+    });
+    squares[0] += part;
+  }
+  group_reduce<Sum, L>(squares, s_red[1]);
+  float rstd = 1.0f / sqrtf(squares[0] / (float)D + a.eps), shown_mean = mean, shown_rstd = rstd;
+  if (__any(!(squares[0] < __builtin_huge_valf()))) {  // the same for a whole workgroup where a row is one
+    float again[1] = {0.0f};
+    Vec<TX, E> raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const u32 c = (i * L + t) * E;
+      if (c < D) raw[i] = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+      in_row<E>(c, D, [&](int e) { again[0] += to_f32(raw[i].v[e]) * kShrink; });
+    }
+    group_reduce<Sum, L>(again, s_red[0]);
+    const float m = again[0] / (float)D;
+    const bool far = !(squares[0] < __builtin_huge_valf());
+    again[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      in_row<E>((i * L + t) * E, D, [&](int e) {
+        const float d = to_f32(raw[i].v[e]) * kShrink - m;
+        again[0] = fmaf(d, d, again[0]);
+        if (far) v[i][e] = d;
+      });
+    group_reduce<Sum, L>(again, s_red[1]);
+    if (far) {
+      rstd = 1.0f / sqrtf(again[0] / (float)D);
+      shown_mean = m / kShrink;
+      shown_rstd = rstd * kShrink;
+    }
+  }
+  if (!real) return;
+  if (t == 0) {
+    if (a.mean) a.mean[row] = shown_mean;
+    if (a.rstd) a.rstd[row] = shown_rstd;
+  }
+  TY* out = (TY*)a.out + row * (int64_t)D;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const u32 c = (i * L + t) * E;
+    if (c >= D) continue;
+    float w[E], b[E], y[E];
+    load_params<E>(a.weight, a.weight_dtype, c, D, 1.0f, w);
+    load_params<E>(a.bias, a.weight_dtype, c, D, 0.0f, b);
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = fmaf(v[i][e] * rstd, w[e], b[e]);
+    store_part<TY, E>(out, c, D, round_vec<TY, E>(y), a.streaming);
+  }
+}
+
+constexpr int kLongThreads = 1024;
+
+// Rows longer than registers hold: read three times, twice from the caches.
+// out may be x: a thread writes what it alone reads.
+template <class TX, class TY, int E>
+__global__ __launch_bounds__(kLongThreads) void k_norm_long(NormArgs a) {
+  __shared__ float s_red[2][kLongThreads / kWave];
+  const int64_t row = a.row0 + blockIdx.x;
+  const u32 D = a.D;
+  const TX* x = (const TX*)a.x + row * (int64_t)D;
+  float sum[1] = {0.0f}, squares[1] = {0.0f};
+  for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
+    const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+    float part = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) part += to_f32(raw.v[e]);
+    sum[0] += part;
+  }
+  group_reduce<Sum, kLongThreads>(sum, s_red[0]);
+  float mean = sum[0] / (float)D;
+  for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
+    const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+    float part = 0.0f;
+    in_row<E>(c, D, [&](int e) {
+      const float d = to_f32(raw.v[e]) - mean;
+      part = fmaf(d, d, part);
+    });
+    squares[0] += part;
+  }
+  group_reduce<Sum, kLongThreads>(squares, s_red[1]);
+  float rstd = 1.0f / sqrtf(squares[0] / (float)D + a.eps), shrink = 1.0f;
+  if (!(squares[0] < __builtin_huge_valf())) {
+    float again[1] = {0.0f};
+    for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
+      const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+      in_row<E>(c, D, [&](int e) { again[0] += to_f32(raw.v[e]) * kShrink; });
+    }
+    group_reduce<Sum, kLongThreads>(again, s_red[0]);
+    mean = again[0] / (float)D;
+    again[0] = 0.0f;
+    for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
+      const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+      in_row<E>(c, D, [&](int e) {
+        const float d = to_f32(raw.v[e]) * kShrink - mean;
+        again[0] = fmaf(d, d, again[0]);
+      });
+    }
+    group_reduce<Sum, kLongThreads>(again, s_red[1]);
+    rstd = 1.0f / sqrtf(again[0] / (float)D);
+    shrink = kShrink;
+  }
+  if (threadIdx.x == 0) {
+    if (a.mean) a.mean[row] = mean / shrink;
+    if (a.rstd) a.rstd[row] = rstd * shrink;
+  }
+  TY* out = (TY*)a.out + row * (int64_t)D;
+  for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
+    const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+    float w[E], b[E], y[E];
+    load_params<E>(a.weight, a.weight_dtype, c, D, 1.0f, w);
+    load_params<E>(a.bias, a.weight_dtype, c, D, 0.0f, b);
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = fmaf((to_f32(raw.v[e]) * shrink - mean) * rstd, w[e], b[e]);
+    store_part<TY, E>(out, c, D, round_vec<TY, E>(y), a.streaming);
+  }
+}
+
+// -------------------------------------------------------------- gradients --
+struct NormGradArgs {
+  const void* grad;
+  const void* x;
+  const float* mean;
+  const float* rstd;
+  const void* weight;
+  void* out;
+  float* part;  // [groups][2][D] sums of g xh and of g, null without parameters' gradients
+  int64_t T;
+  u32 D;
+  int weight_dtype;
+  bool streaming;
+};
+
+// A workgroup takes every gridDim.x-th set of NT / L rows and keeps its
+// columns' sums of g xh and of g in registers; its sums go to one partial row.
+template <class TX, class TY, int E, int L, int NV>
+__global__ __launch_bounds__(norm_threads(L)) void k_norm_grad(NormGradArgs a) {
+  constexpr int NT = norm_threads(L);
+  constexpr int kCols = L * NV * E;
+  __shared__ float s_red[2][2 * (L > kWave ? L / kWave : 1)];
+  __shared__ float s_cols[L < 256 ? 2 * kCols : 1];
+  const u32 D = a.D, t = threadIdx.x % L;
+  const float inv = 1.0f / (float)D;
+  float w[NV][E], dw[NV][E], db[NV][E];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const u32 c = (i * L + t) * E;
+    if (c < D) load_params<E>(a.weight, a.weight_dtype, c, D, 1.0f, w[i]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw[i][e] = db[i][e] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t set = blockIdx.x; set * (NT / L) < a.T; set += gridDim.x, turn ^= 1) {
+    const int64_t row = set * (NT / L) + threadIdx.x / L;
+    const bool real = row < a.T;
+    const int64_t at = (real ? row : 0) * (int64_t)D;
+    const TX* x = (const TX*)a.x + at;
+    const TY* g = (const TY*)a.grad + at;
+    const float mean = real ? a.mean[row] : 0.0f, rstd = real ? a.rstd[row] : 0.0f;
+    Vec<TX, E> rx[NV];
+    Vec<TY, E> rg[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const u32 c = (i * L + t) * E;
+      if (real && c < D) {
+        rx[i] = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+        rg[i] = load_part<TY, E>(g, c, D, from_f32<TY>(0.0f));
+      }
+    }
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float p0 = 0.0f, p1 = 0.0f;
+      if (real)
+        in_row<E>((i * L + t) * E, D, [&](int e) {
+          const float xh = (to_f32(rx[i].v[e]) - mean) * rstd, gv = to_f32(rg[i].v[e]), gw = gv * w[i][e];
+          p0 += gw;
+          p1 = fmaf(gw, xh, p1);
+          dw[i][e] = fmaf(gv, xh, dw[i][e]);
+          db[i][e] += gv;
+        });
+      s[0] += p0;
+      s[1] += p1;
+    }
+    group_reduce<Sum, L>(s, s_red[turn]);
+    if (!real) continue;
+    const float m0 = s[0] * inv, m1 = s[1] * inv;
+    TX* out = (TX*)a.out + at;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const u32 c = (i * L + t) * E;
+      if (c >= D) continue;
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float xh = (to_f32(rx[i].v[e]) - mean) * rstd, gw = to_f32(rg[i].v[e]) * w[i][e];
+        y[e] = rstd * fmaf(-xh, m1, gw - m0);
+      }
+      store_part<TX, E>(out, c, D, round_vec<TX, E>(y), a.streaming);
+    }
+  }
+  if (!a.part) return;
+  float* part = a.part + (int64_t)blockIdx.x * 2 * D;
+  if constexpr (L >= 256) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const u32 c = (i * L + t) * E;
+      in_row<E>(c, D, [&](int e) {
+        part[c + e] = dw[i][e];
+        part[(int64_t)D + c + e] = db[i][e];
+      });
+    }
+  } else {
+    // groups of a wave first, then the waves in turn
+#pragma unroll
+    for (int m = L; m < kWave; m *= 2) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          dw[i][e] += __shfl_xor(dw[i][e], m);
+          db[i][e] += __shfl_xor(db[i][e], m);
+        }
+      }
+    }
+    for (int turn_of = 0; turn_of < NT / kWave; ++turn_of) {
+      if (threadIdx.x / kWave == turn_of && lane_id() < L) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const u32 c = (i * L + t) * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            s_cols[c + e] = dw[i][e] + (turn_of ? s_cols[c + e] : 0.0f);
+            s_cols[kCols + c + e] = db[i][e] + (turn_of ? s_cols[kCols + c + e] : 0.0f);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (u32 c = threadIdx.x; c < D; c += NT) {
+      part[c] = s_cols[c];
+      part[(int64_t)D + c] = s_cols[kCols + c];
+    }
+  }
+}
+
+// Rows longer than registers hold: x's gradient, each row read twice.
+template <class TX, class TY, int E>
+__global__ __launch_bounds__(kLongThreads) void k_norm_grad_long(NormGradArgs a, int64_t row0) {
+  __shared__ float s_red[2 * (kLongThreads / kWave)];
+  const int64_t row = row0 + blockIdx.x;
+  const u32 D = a.D;
+  const int64_t at = row * (int64_t)D;
+  const TX* x = (const TX*)a.x + at;
+  const TY* g = (const TY*)a.grad + at;
+  const float mean = a.mean[row], rstd = a.rstd[row], inv = 1.0f / (float)D;
+  float s[2] = {0.0f, 0.0f};
+  for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
+    const Vec<TX, E> rx = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+    const Vec<TY, E> rg = load_part<TY, E>(g, c, D, from_f32<TY>(0.0f));
+    float w[E], p0 = 0.0f, p1 = 0.0f;
+    load_params<E>(a.weight, a.weight_dtype, c, D, 1.0f, w);
+    in_row<E>(c, D, [&](int e) {
+      const float gw = to_f32(rg.v[e]) * w[e];
+      p0 += gw;
+      p1 = fmaf(gw, (to_f32(rx.v[e]) - mean) * rstd, p1);
+    });
+    s[0] += p0;
+    s[1] += p1;
+  }
+  group_reduce<Sum, kLongThreads>(s, s_red);
+  const float m0 = s[0] * inv, m1 = s[1] * inv;
+  TX* out = (TX*)a.out + at;
+  for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
+    const Vec<TX, E> rx = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+    const Vec<TY, E> rg = load_part<TY, E>(g, c, D, from_f32<TY>(0.0f));
+    float w[E], y[E];
+    load_params<E>(a.weight, a.weight_dtype, c, D, 1.0f, w);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      y[e] = rstd * fmaf(-(to_f32(rx.v[e]) - mean) * rstd, m1, to_f32(rg.v[e]) * w[e] - m0);
+    store_part<TX, E>(out, c, D, round_vec<TX, E>(y), a.streaming);
+  }
+}
+
+// Such rows' sums by columns: a workgroup takes 256 columns of every
+// gridDim.y-th row.  It runs before k_norm_grad_long, which may overwrite x or g.
+template <class TX, class TY>
+__global__ __launch_bounds__(256) void k_norm_columns(NormGradArgs a) {
+  const u32 D = a.D, c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= D) return;
+  float dw = 0.0f, db = 0.0f;
+  for (int64_t row = blockIdx.y; row < a.T; row += gridDim.y) {
+    const float xh = (to_f32(((const TX*)a.x)[row * D + c]) - a.mean[row]) * a.rstd[row];
+    const float g = to_f32(((const TY*)a.grad)[row * D + c]);
+    dw = fmaf(g, xh, dw);
+    db += g;
+  }
+  float* part = a.part + (int64_t)blockIdx.y * 2 * D;
+  part[c] = dw;
+  part[(int64_t)D + c] = db;
+}
+
+// Adds the partial rows, each column's in a fixed order, and rounds the sums.
+constexpr int kJoinThreads = 1024;
+__global__ __launch_bounds__(kJoinThreads) void k_norm_join(const float* part, u32 groups, u32 D, void* weight,
+                                                            void* bias, int dtype) {
+  constexpr u32 W = kJoinThreads / kWave;
+  __shared__ float s_sum[W][kWave];
+  const int lane = lane_id();
+  const u32 w = threadIdx.x / kWave;
+  const int64_t width = 2 * (int64_t)D, c = (int64_t)blockIdx.x * kWave + lane;
+  float sum = 0.0f;
+  if (c < width) {
+#pragma unroll 8
+    for (u32 g = w; g < groups; g += W) sum += part[g * width + c];
+  }
+  s_sum[w][lane] = sum;
+  __syncthreads();
+  if (w == 0 && c < width) {
+#pragma unroll
+    for (u32 i = 1; i < W; ++i) sum += s_sum[i][lane];
+    if (c < D) {
+      if (weight) store_param(weight, dtype, (u32)c, sum);
+    } else if (bias) {
+      store_param(bias, dtype, (u32)(c - D), sum);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host --
+static int norm_vector(tgs_dtype a, tgs_dtype b) { return dtype_bytes(a) == 2 && dtype_bytes(b) == 2 ? 8 : 4; }
+
+// Lanes and vectors a lane for rows of `vectors`: the smallest that holds them.
+// Calls f(L, NV) as integral constants; false where none does.
+template <class F>
+static bool with_shape(u32 vectors, F&& f) {
+  using std::integral_constant;
+  if (vectors <= 8) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (vectors <= 32) f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  else if (vectors <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (vectors <= 128) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (vectors <= 256) f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+  else if (vectors <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (vectors <= 1024) f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (vectors <= 2048) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  else return false;
+  return true;
+}
+
+constexpr int64_t kMostD = (int64_t)1 << 24;  // exact in fp32, and no launch reaches 2^32 threads
+constexpr u32 kMostHeld = 2048;  // vectors of a row that registers hold
+
+// Workgroups that add up the parameters' gradients, hence partial rows.
+static int64_t norm_groups(int64_t T, int64_t D, int E) {
+  const u32 vectors = (u32)((D + E - 1) / E);
+  if (vectors > kMostHeld) return std::max<int64_t>(1, std::min<int64_t>(64, T));
+  int64_t rows = 1;
+  int threads = 256;
+  with_shape(vectors, [&](auto l, auto) {
+    threads = norm_threads(l.value);
+    rows = threads / l.value;
+  });
+  const int64_t most = threads > 256 ? 256 : 512;
+  return std::max<int64_t>(1, std::min(most, (T + rows - 1) / rows));
+}
+
+static tgs_status check_norm_sizes(const char* what, int64_t T, int64_t D) {
+  if (T < 0 || T > INT32_MAX) return fail(TGS_EINVAL, "%s: T=%lld outside [0, 2^31-1]", what, (long long)T);
+  if (D < 1 || D > kMostD) return fail(TGS_EINVAL, "%s: D=%lld outside [1, 2^24]", what, (long long)D);
+  return TGS_OK;
+}
+
+template <class F>
+static void with_two_types(tgs_dtype a, tgs_dtype b, F&& f) {
+  with_float_dtype(a, [&](auto* x) { with_float_dtype(b, [&](auto* y) { f(x, y); }); });
+}
+
+}  // namespace tgs
+
+using namespace tgs;
+
+extern "C" tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T, int64_t D, const void* weight,
+                                     const void* bias, tgs_dtype weight_dtype, float eps, void* out,
+                                     tgs_dtype out_dtype, float* mean, float* rstd, hipStream_t stream) {
+  const char* what = "layer_norm";
+  tgs_status st = check_norm_sizes(what, T, D);
+  if (st != TGS_OK) return st;
+  if (!is_float_dtype(x_dtype) || !is_float_dtype(out_dtype) || ((weight || bias) && !is_float_dtype(weight_dtype)))
+    return fail(TGS_EINVAL, "%s: values must be fp32, bf16 or fp16", what);
+  if (!(eps >= 0.0f) || !(eps - eps == 0.0f)) return fail(TGS_EINVAL, "%s: eps must be finite and >= 0", what);
+  const size_t wa = dtype_bytes(weight || bias ? weight_dtype : TGS_FP32);
+  if ((st = check_rows_array(what, "x", x, dtype_bytes(x_dtype), T > 0)) != TGS_OK ||
+      (st = check_rows_array(what, "out", out, dtype_bytes(out_dtype), T > 0)) != TGS_OK ||
+      (st = check_rows_array(what, "weight", weight, wa, false)) != TGS_OK ||
+      (st = check_rows_array(what, "bias", bias, wa, false)) != TGS_OK ||
+      (st = check_rows_array(what, "mean", mean, 4, false)) != TGS_OK ||
+      (st = check_rows_array(what, "rstd", rstd, 4, false)) != TGS_OK)
+    return st;
+  const size_t nx = (size_t)T * D * dtype_bytes(x_dtype), no = (size_t)T * D * dtype_bytes(out_dtype);
+  const size_t nw = (size_t)D * wa, ns = (size_t)T * 4;
+  const bool in_place = x == out && x_dtype == out_dtype;
+  if ((!in_place && overlaps(out, no, x, nx)) || overlaps(out, no, weight, nw) || overlaps(out, no, bias, nw))
+    return fail(TGS_EINVAL, "%s: out overlaps an input", what);
+  for (float* s : {mean, rstd})
+    if (overlaps(s, ns, x, nx) || overlaps(s, ns, out, no) || overlaps(s, ns, weight, nw) || overlaps(s, ns, bias, nw))
+      return fail(TGS_EINVAL, "%s: mean or rstd overlaps another array", what);
+  if (overlaps(mean, ns, rstd, ns)) return fail(TGS_EINVAL, "%s: mean overlaps rstd", what);
+  if (T == 0) return TGS_OK;
+  NormArgs a{};
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.out = out;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.T = T;
+  a.D = (u32)D;
+  a.weight_dtype = weight_dtype;
+  a.eps = eps;
+  a.streaming = no > kRowsStreamingBytes;
+  with_two_types(x_dtype, out_dtype, [&](auto* tx, auto* ty) {
+    using TX = std::remove_pointer_t<decltype(tx)>;
+    using TY = std::remove_pointer_t<decltype(ty)>;
+    constexpr int E = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
+    const u32 vectors = (u32)((D + E - 1) / E);
+    const bool held = with_shape(vectors, [&](auto l, auto nv) {
+      constexpr int L = decltype(l)::value, NV = decltype(nv)::value, NT = norm_threads(L);
+      const int64_t most = most_groups(NT) * (NT / L);
+      for (a.row0 = 0; a.row0 < T; a.row0 += most) {
+        const int64_t rows = std::min(most, T - a.row0);
+        hipLaunchKernelGGL((k_norm<TX, TY, E, L, NV>), dim3((u32)((rows + NT / L - 1) / (NT / L))), dim3(NT), 0,
+                           stream, a);
+      }
+    });
+    if (!held) {
+      const int64_t most = most_groups(kLongThreads);
+      for (a.row0 = 0; a.row0 < T; a.row0 += most)
+        hipLaunchKernelGGL((k_norm_long<TX, TY, E>), dim3((u32)std::min(most, T - a.row0)), dim3(kLongThreads), 0,
+                           stream, a);
+    }
+  });
+  return launched(what);
+}
+
+extern "C" size_t tgs_layer_norm_grad_workspace_bytes(int64_t T, int64_t D) {
+  if (T < 0 || T > INT32_MAX || D < 1 || D > kMostD) return 0;
+  // the types decide how many lanes a row takes: the most of either
+  const int64_t groups = std::max(norm_groups(T, D, 4), norm_groups(T, D, 8));
+  return kWorkspaceHeader + round_up_256((size_t)groups * 2 * (size_t)D * 4);
+}
+
+extern "C" tgs_status tgs_layer_norm_grad(const void* grad, tgs_dtype grad_dtype, const void* x, tgs_dtype x_dtype,
+                                          int64_t T, int64_t D, const float* mean, const float* rstd,
+                                          const void* weight, tgs_dtype weight_dtype, void* grad_x, void* grad_weight,
+                                          void* grad_bias, tgs_dtype param_dtype, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream) {
+  const char* what = "layer_norm_grad";
+  tgs_status st = check_norm_sizes(what, T, D);
+  if (st != TGS_OK) return st;
+  const bool params = grad_weight || grad_bias;
+  if (!is_float_dtype(x_dtype) || !is_float_dtype(grad_dtype) || (weight && !is_float_dtype(weight_dtype)) ||
+      (params && !is_float_dtype(param_dtype)))
+    return fail(TGS_EINVAL, "%s: values must be fp32, bf16 or fp16", what);
+  const size_t pa = dtype_bytes(params ? param_dtype : TGS_FP32), wa = dtype_bytes(weight ? weight_dtype : TGS_FP32);
+  if ((st = check_rows_array(what, "grad", grad, dtype_bytes(grad_dtype), T > 0)) != TGS_OK ||
+      (st = check_rows_array(what, "x", x, dtype_bytes(x_dtype), T > 0)) != TGS_OK ||
+      (st = check_rows_array(what, "mean", mean, 4, T > 0)) != TGS_OK ||
+      (st = check_rows_array(what, "rstd", rstd, 4, T > 0)) != TGS_OK ||
+      (st = check_rows_array(what, "weight", weight, wa, false)) != TGS_OK ||
+      (st = check_rows_array(what, "grad_x", grad_x, dtype_bytes(x_dtype), T > 0)) != TGS_OK ||
+      (st = check_rows_array(what, "grad_weight", grad_weight, pa, false)) != TGS_OK ||
+      (st = check_rows_array(what, "grad_bias", grad_bias, pa, false)) != TGS_OK ||
+      (st = check_rows_workspace(what, workspace, workspace_bytes, tgs_layer_norm_grad_workspace_bytes(T, D))) != TGS_OK)
+    return st;
+  struct Span {
+    const void* p;
+    size_t n;
+  };
+  const size_t nx = (size_t)T * D * dtype_bytes(x_dtype), ng = (size_t)T * D * dtype_bytes(grad_dtype);
+  const Span in[] = {{grad, ng}, {x, nx}, {mean, (size_t)T * 4}, {rstd, (size_t)T * 4}, {weight, (size_t)D * wa}};
+  const Span out[] = {{grad_x, nx}, {grad_weight, (size_t)D * pa}, {grad_bias, (size_t)D * pa}, {workspace, workspace_bytes}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 5; ++i) {
+      // x's gradient may take the place of x or of the incoming gradient
+      if (o == 0 && (i == 1 || (i == 0 && grad_dtype == x_dtype)) && out[o].p == in[i].p) continue;
+      if (overlaps(out[o].p, out[o].n, in[i].p, in[i].n)) return fail(TGS_EINVAL, "%s: an output overlaps an input", what);
+    }
+    for (int i = 0; i < o; ++i)
+      if (overlaps(out[o].p, out[o].n, out[i].p, out[i].n)) return fail(TGS_EINVAL, "%s: outputs overlap", what);
+  }
+  if (T == 0 && !params) return TGS_OK;
+  NormGradArgs a{};
+  a.grad = grad;
+  a.x = x;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.weight = weight;
+  a.out = grad_x;
+  a.part = params ? (float*)((char*)workspace + kWorkspaceHeader) : nullptr;
+  a.T = T;
+  a.D = (u32)D;
+  a.weight_dtype = weight_dtype;
+  a.streaming = nx > kRowsStreamingBytes;
+  const int64_t groups = T == 0 ? 0 : norm_groups(T, D, norm_vector(x_dtype, grad_dtype));
+  if (T > 0)
+    with_two_types(x_dtype, grad_dtype, [&](auto* tx, auto* ty) {
+      using TX = std::remove_pointer_t<decltype(tx)>;
+      using TY = std::remove_pointer_t<decltype(ty)>;
+      constexpr int E = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
+      const u32 vectors = (u32)((D + E - 1) / E);
+      const bool held = with_shape(vectors, [&](auto l, auto nv) {
+        constexpr int L = decltype(l)::value, NV = decltype(nv)::value, NT = norm_threads(L);
+        hipLaunchKernelGGL((k_norm_grad<TX, TY, E, L, NV>), dim3((u32)groups), dim3(NT), 0, stream, a);
+      });
+      if (!held) {
+        if (params)
+          hipLaunchKernelGGL((k_norm_columns<TX, TY>), dim3((u32)((D + 255) / 256), (u32)groups), dim3(256), 0, stream, a);
+        const int64_t most = most_groups(kLongThreads);
+        for (int64_t row0 = 0; row0 < T; row0 += most)
+          hipLaunchKernelGGL((k_norm_grad_long<TX, TY, E>), dim3((u32)std::min(most, T - row0)), dim3(kLongThreads), 0,
+                             stream, a, row0);
+      }
+    });
+  if (params)
+    hipLaunchKernelGGL(k_norm_join, dim3((u32)((2 * D + kWave - 1) / kWave)), dim3(kJoinThreads), 0, stream, a.part,
+                       (u32)groups, (u32)D, grad_weight, grad_bias, param_dtype);
+  return launched(what);
+}

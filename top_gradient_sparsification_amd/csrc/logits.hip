@@ -1,0 +1,783 @@
+// Losses on rows of logits on gfx950: log probabilities of given tokens with
+// entropy and top alternatives, distillation from a teacher's top logits, and
+// the gradients of both.
+//
+//   p = softmax(z / tau) = e^((z - m) / tau) / s,  s = sum e^((z - m) / tau)
+//   log p(j) = (z_j - m) / tau - log s
+//   H = log s - sum of e^d d / s with d = (z - m) / tau
+//   L = sum over slots of q (log q - log p(index)), q = softmax(teacher / tau)
+//   gradients: of log p(j)  (onehot(j) - p) / tau
+//              of H         -p (log p + H) / tau
+//              of L         (p - q) / tau
+//
+// Bound by HBM: a row is read once on the way out, read and written once on
+// the way back.
+#include <type_traits>
+
+#include "tgs_softmax.h"
+
+namespace tgs {
+
+constexpr int kRowThreads = 256;
+
+// What one slice of a row leaves for the join: its sums, and behind all of them
+// its largest keys.
+struct SliceSums {
+  float m, s, w, pad;
+};
+
+struct Split {
+  u32 slices;  // a row's; 1: nothing is joined
+  u32 length;  // elements of a slice, a multiple of every vector
+  SliceSums* sums;  // [row][slice]
+  u64* keys;        // [row][slice][top]
+};
+
+__device__ __forceinline__ int64_t load_index(const void* p, bool wide, int64_t i) {
+  return wide ? ((const int64_t*)p)[i] : (int64_t)((const int32_t*)p)[i];
+}
+
+// The index, -1 where it stands for none; one past the row is reported.
+__device__ __forceinline__ int load_entry(const void* p, bool wide, int64_t i, u32 V, u32* err) {
+  const int64_t v = load_index(p, wide, i);
+  if (v >= (int64_t)V) atomicOr(err, kErrBadInput);
+  return v >= 0 && v < (int64_t)V ? (int)v : -1;
+}
+
+// ----------------------------------------------- log probabilities of tokens --
+struct LogprobsArgs {
+  Logits z;
+  Split split;
+  const void* tokens;
+  float* logprobs;
+  float* stats;    // [T][2]: largest score, log s
+  float* entropy;  // or null
+  int32_t* top_indices;
+  float* top_logprobs;
+  u32* err;
+  int64_t T, row0;
+  u32 top;
+  bool wide;  // 64-bit tokens
+};
+
+__device__ __forceinline__ float log_probability(const Logits& z, float x, const RowSums& r, float log_s) {
+  return r.s == 0.0f ? -kInf : (x - r.m) * z.inv - log_s;
+}
+
+// One row's results from its sums, by any number of threads.
+template <bool ENTROPY>
+__device__ __forceinline__ void write_logprobs(const LogprobsArgs& a, int64_t row, int token, float score,
+                                               const RowSums& r, const u64* keys) {
+  const bool real = token >= 0;
+  const float log_s = r.s == 0.0f ? 0.0f : logf(r.s);
+  if (threadIdx.x == 0) {
+    a.logprobs[row] = real ? log_probability(a.z, score, r, log_s) : 0.0f;
+    a.stats[2 * row] = real ? r.m : 0.0f;
+    a.stats[2 * row + 1] = real ? log_s : 0.0f;
+    if constexpr (ENTROPY) a.entropy[row] = real && r.s != 0.0f ? log_s - r.w / r.s * kLn2 : 0.0f;
+  }
+  for (u32 i = threadIdx.x; i < a.top; i += blockDim.x) {
+    const u64 key = real ? keys[i] : 0;
+    a.top_indices[row * a.top + i] = real ? (int32_t)key_index(key) : -1;
+    a.top_logprobs[row * a.top + i] = real ? log_probability(a.z, key_score(key), r, log_s) : 0.0f;
+  }
+}
+
+template <class T, int NT, bool ENTROPY, bool TOP>
+__global__ __launch_bounds__(NT) void k_logprobs(LogprobsArgs a) {
+  constexpr int E = kLogitsVector<T>;
+  __shared__ float s_red[kJoinLds<NT>];
+  __shared__ std::conditional_t<TOP, TopLds<NT>, int> s_top;
+  const u32 slices = a.split.slices, slice = slices == 1 ? 0 : blockIdx.x % slices;
+  const int64_t row = a.row0 + (slices == 1 ? blockIdx.x : blockIdx.x / slices);
+  const int token = load_entry(a.tokens, a.wide, row, a.z.V, a.err);
+  if (token < 0) {  // nothing of the row is read
+    if (slice == 0) write_logprobs<ENTROPY>(a, row, -1, 0.0f, RowSums{0.0f, 1.0f, 0.0f}, nullptr);
+    return;
+  }
+  const T* z = (const T*)a.z.p + row * a.z.ld;
+  const float score = to_f32(z[token]);
+  const u32 c0 = slice * a.split.length, c1 = min(c0 + a.split.length, a.z.V);
+  const Share h = row_pass<T, NT, ENTROPY, TOP>(z, c0, c1, a.z.c2);
+  const RowSums r = join_shares<NT>(h, a.z.c2, s_red);
+  if constexpr (TOP) {
+    const u32 first = c0 + threadIdx.x * E, at = first + h.at * (NT * E);
+    const u64 bound = first < c1 ? entry_key(h.top, min(at + E, c1) - 1) : 0;
+    largest_keys<NT>(s_top, bound, (c1 - c0 + NT * E - 1) / (NT * E), a.top, r.s != r.s, [&](u32 owner, u32 j, auto&& f) {
+      const u32 c = c0 + (owner + j * NT) * E;
+      if (c >= c1) return;
+      const Vec<T, E> v = load_part<T, E>(z, c, c1, lowest_fill<T>());
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (c + e < c1) f(entry_key(to_f32(v.v[e]), c + e));
+    });
+  }
+  const u64* keys = nullptr;
+  if constexpr (TOP) keys = s_top.out;
+  if (slices == 1) {
+    write_logprobs<ENTROPY>(a, row, token, score, r, keys);
+    return;
+  }
+  const int64_t part = (row - a.row0) * slices + slice;
+  if (threadIdx.x == 0) a.split.sums[part] = SliceSums{r.m, r.s, r.w, 0.0f};
+  for (u32 i = threadIdx.x; i < a.top; i += NT) a.split.keys[part * a.top + i] = keys[i];
+}
+
+// A row's sums from its slices' (64 at most), by the first wave; every thread gets them.
+__device__ __forceinline__ RowSums join_slices(const Split& split, int64_t row, float c2, float* lds) {
+  if (threadIdx.x < kWave) {
+    SliceSums p{-kInf, 0.0f, 0.0f, 0.0f};
+    if (threadIdx.x < split.slices) p = split.sums[row * split.slices + threadIdx.x];
+    const float m = lanes_reduce<Max, kWave>(p.m);
+    float s = 0.0f, w = 0.0f;
+    if (p.s != 0.0f) {
+      const float step = (p.m - m) * c2, f = p.m == m ? 1.0f : __builtin_amdgcn_exp2f(step);
+      s = p.s * f;
+      w = p.m == m ? p.w : f == 0.0f ? 0.0f : f * fmaf(p.s, step, p.w);
+    }
+    s = lanes_reduce<Sum, kWave>(s);
+    w = lanes_reduce<Sum, kWave>(w);
+    if (threadIdx.x == 0) {
+      lds[0] = m;
+      lds[1] = s;
+      lds[2] = w;
+    }
+  }
+  __syncthreads();
+  return RowSums{lds[0], lds[1], lds[2]};
+}
+
+template <class T, bool ENTROPY, bool TOP>
+__global__ __launch_bounds__(kRowThreads) void k_logprobs_join(LogprobsArgs a) {
+  constexpr int NT = kRowThreads;
+  __shared__ float s_red[4];
+  __shared__ std::conditional_t<TOP, TopLds<NT>, int> s_top;
+  const int64_t row = a.row0 + blockIdx.x;
+  const int token = load_entry(a.tokens, a.wide, row, a.z.V, a.err);
+  if (token < 0) return;  // written
+  const float score = to_f32(((const T*)a.z.p)[row * a.z.ld + token]);
+  const RowSums r = join_slices(a.split, blockIdx.x, a.z.c2, s_red);
+  const u64* keys = nullptr;
+  if constexpr (TOP) {
+    // thread t holds the keys t, t + NT, ..
+    const u32 n = a.split.slices * a.top, count = (n + NT - 1) / NT;
+    const u64* all = a.split.keys + (int64_t)blockIdx.x * n;
+    u64 bound = 0;
+    for (u32 i = threadIdx.x; i < n; i += NT) bound = max(bound, all[i]);
+    largest_keys<NT>(s_top, bound, count, a.top, false, [&](u32 owner, u32 j, auto&& f) {
+      const u32 i = owner + j * NT;
+      if (i < n && all[i] != 0) f(all[i]);
+    });
+    keys = s_top.out;
+  }
+  write_logprobs<ENTROPY>(a, row, token, score, r, keys);
+}
+
+// ------------------------------------------------------------ way back --
+struct LogprobsGradArgs {
+  Logits z;
+  const void* tokens;
+  const float* stats;
+  const float* grad;          // of the log probabilities, or null
+  const float* entropy;       // with grad_entropy
+  const float* grad_entropy;  // or null
+  void* out;
+  int64_t ld_out;
+  u32* err;
+  int64_t row0;
+  u32 slices, length;
+  bool wide, streaming;
+};
+
+// Element x's p / tau times its coefficient: (b - a (log p + h)) p, with b and a
+// times 1 / tau already; 0 where p is.
+struct Coefficients {
+  float m, log_s, l2;  // l2: log2 s
+  float a, b, h;
+};
+
+template <bool ENTROPY>
+__device__ __forceinline__ float slope(const Logits& z, const Coefficients& k, float x) {
+  const float d = x - k.m;
+  const float p = __builtin_amdgcn_exp2f(fmaf(d, z.c2, -k.l2));
+  if constexpr (!ENTROPY) return p * k.b;
+  const float lp = fmaxf(fmaf(d, z.inv, -k.log_s), -1024.0f);
+  return p * fmaf(-k.a, lp + k.h, k.b);
+}
+
+template <class T, int NT, class F>
+__device__ __forceinline__ void map_row(const T* z, T* out, u32 c0, u32 c1, bool streaming, F&& f) {
+  constexpr int E = kLogitsVector<T>, U = 4;
+  constexpr u32 kStep = NT * E;
+  for (u32 base = c0; base < c1; base += U * kStep) {
+    const u32 c = base + threadIdx.x * E;
+    Vec<T, E> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c + u * kStep < c1) v[u] = load_part<T, E>(z, c + u * kStep, c1, lowest_fill<T>());
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const u32 at = c + u * kStep;
+      if (at >= c1) continue;
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = f(to_f32(v[u].v[e]), at + e);
+      store_part<T, E>(out, at, c1, round_vec<T, E>(y), streaming);
+    }
+  }
+}
+
+template <class T, int NT>
+__device__ __forceinline__ void zero_row(T* out, u32 c0, u32 c1, bool streaming) {
+  constexpr int E = kLogitsVector<T>;
+  const float zero[E] = {};
+  for (u32 c = c0 + threadIdx.x * E; c < c1; c += NT * E) store_part<T, E>(out, c, c1, round_vec<T, E>(zero), streaming);
+}
+
+template <class T, int NT, bool ENTROPY>
+__global__ __launch_bounds__(NT) void k_logprobs_grad(LogprobsGradArgs a) {
+  const u32 slice = a.slices == 1 ? 0 : blockIdx.x % a.slices;
+  const int64_t row = a.row0 + (a.slices == 1 ? blockIdx.x : blockIdx.x / a.slices);
+  const u32 c0 = slice * a.length, c1 = min(c0 + a.length, a.z.V);
+  T* out = (T*)a.out + row * a.ld_out;
+  const int token = load_entry(a.tokens, a.wide, row, a.z.V, a.err);
+  Coefficients k;
+  k.m = a.stats[2 * row];
+  k.log_s = a.stats[2 * row + 1];
+  if (token < 0 || k.m == -kInf) {  // masked, or no score above -inf
+    zero_row<T, NT>(out, c0, c1, a.streaming);
+    return;
+  }
+  k.l2 = k.log_s * kLog2e;
+  const float g = a.grad ? a.grad[row] * a.z.inv : 0.0f;
+  k.b = -g;
+  k.a = ENTROPY ? a.grad_entropy[row] * a.z.inv : 0.0f;
+  k.h = ENTROPY ? a.entropy[row] : 0.0f;
+  map_row<T, NT>((const T*)a.z.p + row * a.z.ld, out, c0, c1, a.streaming, [&](float x, u32 c) {
+    const float y = slope<ENTROPY>(a.z, k, x);
+    return c == (u32)token ? y + g : y;
+  });
+}
+
+// ---------------------------------------------------------- distillation --
+struct DistillArgs {
+  Logits z;
+  Split split;
+  const void* indices;
+  const void* teacher;
+  float* loss;
+  float* stats;        // or null
+  const float* given;  // grad: upstream gradients; step: weights or null
+  void* out;
+  int64_t ld_out;
+  u32* err;
+  int64_t row0;
+  u32 K;
+  int teacher_dtype;
+  bool wide, streaming;
+};
+
+constexpr int kMostSlots = 1024;
+
+struct SlotLds {
+  float q[kMostSlots];
+  float lq[kMostSlots];
+  float x[kMostSlots];  // the row's score there
+  int index[kMostSlots];
+  float red[5][16];
+};
+
+// The slots' probabilities q, and the scores of those in [c0, c1) (others may be
+// overwritten already); false where no slot has any.  Ends with a barrier.
+template <class T, int NT>
+__device__ __forceinline__ bool load_slots(const DistillArgs& a, int64_t row, const T* z, u32 c0, u32 c1, SlotLds& s) {
+  float top[1] = {-kInf}, any[1] = {-kInf};
+  for (u32 i = threadIdx.x; i < a.K; i += NT) {
+    const int64_t at = row * a.K + i;
+    const int index = load_entry(a.indices, a.wide, at, a.z.V, a.err);
+    float t = -kInf;
+    if (index >= 0) {
+      t = a.teacher_dtype == TGS_FP32 ? ((const float*)a.teacher)[at]
+          : a.teacher_dtype == TGS_BF16 ? to_f32(((const bf16_t*)a.teacher)[at]) : to_f32(((const fp16_t*)a.teacher)[at]);
+      s.x[i] = (u32)index >= c0 && (u32)index < c1 ? to_f32(z[index]) : 0.0f;
+    }
+    s.index[i] = index;
+    s.lq[i] = t;
+    top[0] = fmaxf(top[0], t);
+    if (t != -kInf) any[0] = 1.0f;
+  }
+  group_reduce<Max, NT>(top, s.red[0]);
+  group_reduce<Max, NT>(any, s.red[1]);
+  if (any[0] < 0.0f) return false;
+  float sum[1] = {0.0f};
+  for (u32 i = threadIdx.x; i < a.K; i += NT) {
+    const float d = (s.lq[i] - top[0]) * a.z.inv, e = s.index[i] >= 0 ? __builtin_amdgcn_exp2f(d * kLog2e) : 0.0f;
+    s.q[i] = e;
+    s.lq[i] = d;
+    sum[0] += e;
+  }
+  group_reduce<Sum, NT>(sum, s.red[2]);
+  const float scale = 1.0f / sum[0], log_sum = logf(sum[0]);
+  for (u32 i = threadIdx.x; i < a.K; i += NT) {
+    s.q[i] *= scale;
+    s.lq[i] -= log_sum;
+  }
+  __syncthreads();
+  return true;
+}
+
+// The row's loss, in every thread's hands.
+template <int NT>
+__device__ __forceinline__ float slots_loss(const DistillArgs& a, const RowSums& r, float log_s, SlotLds& s) {
+  float sum[1] = {0.0f};
+  for (u32 i = threadIdx.x; i < a.K; i += NT) {
+    const float q = s.q[i];
+    if (!(q == 0.0f)) sum[0] = fmaf(q, s.lq[i] - (r.s == 0.0f ? -kInf : (s.x[i] - r.m) * a.z.inv - log_s), sum[0]);
+  }
+  group_reduce<Sum, NT>(sum, s.red[3]);
+  return sum[0];
+}
+
+// A teacher's NaN, which every q then is, goes to the whole row's gradient.
+__device__ __forceinline__ Coefficients distill_coefficients(const DistillArgs& a, int64_t row, float m, float log_s,
+                                                             const SlotLds& s) {
+  const float g = a.given ? a.given[row] : 1.0f;
+  return Coefficients{m, log_s, log_s * kLog2e, 0.0f, fmaf(0.0f, s.q[0], g * a.z.inv), 0.0f};
+}
+
+// The gradient at the slots' entries inside [c0, c1), over what map_row stored
+// there: those stores have completed, and another store to the same address lands later.
+template <class T, int NT>
+__device__ __forceinline__ void store_slots(const DistillArgs& a, const Coefficients& k, T* out, u32 c0, u32 c1,
+                                            const SlotLds& s) {
+  wait_all_memory();
+  __syncthreads();
+  for (u32 i = threadIdx.x; i < a.K; i += NT) {
+    const int index = s.index[i];
+    if (index < 0 || (u32)index < c0 || (u32)index >= c1) continue;
+    float q = 0.0f;
+    bool first = true;
+    for (u32 j = 0; j < a.K; ++j) {  // an index may stand in several slots
+      if (s.index[j] != index) continue;
+      first = first && j >= i;
+      q += s.q[j];
+    }
+    if (first) {
+      const float p = __builtin_amdgcn_exp2f(fmaf(s.x[i] - k.m, a.z.c2, -k.l2));
+      out[index] = from_f32<T>((p - q) * k.b);
+    }
+  }
+}
+
+// The losses; with GRAD the gradient of their weighted sum too, for which the
+// row is read again, from the caches.
+template <class T, int NT, bool GRAD>
+__global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
+  __shared__ float s_red[kJoinLds<NT>];
+  __shared__ SlotLds s;
+  const u32 slices = a.split.slices, slice = slices == 1 ? 0 : blockIdx.x % slices;
+  const int64_t row = a.row0 + (slices == 1 ? blockIdx.x : blockIdx.x / slices);
+  const T* z = (const T*)a.z.p + row * a.z.ld;
+  T* out = GRAD ? (T*)a.out + row * a.ld_out : nullptr;
+  if (slices == 1 && !load_slots<T, NT>(a, row, z, 0, a.z.V, s)) {
+    if (threadIdx.x == 0) {
+      a.loss[row] = 0.0f;
+      if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
+    }
+    if constexpr (GRAD) zero_row<T, NT>(out, 0, a.z.V, a.streaming);
+    return;
+  }
+  const u32 c0 = slice * a.split.length, c1 = min(c0 + a.split.length, a.z.V);
+  const Share h = row_pass<T, NT, false, false>(z, c0, c1, a.z.c2);
+  const RowSums r = join_shares<NT>(h, a.z.c2, s_red);
+  if (slices > 1) {
+    if (threadIdx.x == 0) a.split.sums[(row - a.row0) * slices + slice] = SliceSums{r.m, r.s, 0.0f, 0.0f};
+    return;
+  }
+  const float log_s = r.s == 0.0f ? 0.0f : logf(r.s);
+  const float loss = slots_loss<NT>(a, r, log_s, s);
+  if (threadIdx.x == 0) {
+    a.loss[row] = loss;
+    if (a.stats) {
+      a.stats[2 * row] = r.m;
+      a.stats[2 * row + 1] = log_s;
+    }
+  }
+  if constexpr (GRAD) {
+    if (r.s == 0.0f) {
+      zero_row<T, NT>(out, 0, a.z.V, a.streaming);
+      return;
+    }
+    const Coefficients k = distill_coefficients(a, row, r.m, log_s, s);
+    map_row<T, NT>(z, out, 0, a.z.V, a.streaming, [&](float x, u32) { return slope<false>(a.z, k, x); });
+    store_slots<T, NT>(a, k, out, 0, a.z.V, s);
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void k_distill_join(DistillArgs a) {
+  constexpr int NT = kRowThreads;
+  __shared__ float s_red[4];
+  __shared__ SlotLds s;
+  const int64_t row = a.row0 + blockIdx.x;
+  const T* z = (const T*)a.z.p + row * a.z.ld;
+  float loss = 0.0f, m = 0.0f, log_s = 0.0f;
+  if (load_slots<T, NT>(a, row, z, 0, a.z.V, s)) {
+    const RowSums r = join_slices(a.split, blockIdx.x, a.z.c2, s_red);
+    m = r.m;
+    log_s = r.s == 0.0f ? 0.0f : logf(r.s);
+    loss = slots_loss<NT>(a, r, log_s, s);
+  }
+  if (threadIdx.x == 0) {
+    a.loss[row] = loss;
+    if (a.stats) {
+      a.stats[2 * row] = m;
+      a.stats[2 * row + 1] = log_s;
+    }
+  }
+}
+
+template <class T, int NT>
+__global__ __launch_bounds__(NT) void k_distill_grad(DistillArgs a) {
+  __shared__ SlotLds s;
+  const u32 slices = a.split.slices, slice = slices == 1 ? 0 : blockIdx.x % slices;
+  const int64_t row = a.row0 + (slices == 1 ? blockIdx.x : blockIdx.x / slices);
+  const u32 c0 = slice * a.split.length, c1 = min(c0 + a.split.length, a.z.V);
+  T* out = (T*)a.out + row * a.ld_out;
+  const T* z = (const T*)a.z.p + row * a.z.ld;
+  const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
+  if (!load_slots<T, NT>(a, row, z, c0, c1, s) || m == -kInf) {
+    zero_row<T, NT>(out, c0, c1, a.streaming);
+    return;
+  }
+  const Coefficients k = distill_coefficients(a, row, m, log_s, s);
+  map_row<T, NT>(z, out, c0, c1, a.streaming, [&](float x, u32) { return slope<false>(a.z, k, x); });
+  store_slots<T, NT>(a, k, out, c0, c1, s);
+}
+
+// ------------------------------------------------------------------ host --
+struct RowPlan {
+  u32 slices, length;
+};
+
+// Slices of a row for about `groups` workgroups in all, none shorter than two
+// vectors a thread.
+static RowPlan row_plan(int64_t T, int64_t V, u32 unit, int64_t groups, int64_t most) {
+  const int64_t want = std::max<int64_t>(1, std::min(most, groups / std::max<int64_t>(T, 1)));
+  const int64_t per = std::max<int64_t>((V + want - 1) / want, 2 * (int64_t)unit);
+  const int64_t length = (per + unit - 1) / unit * unit;
+  return RowPlan{(u32)((V + length - 1) / length), (u32)std::min<int64_t>(length, (int64_t)1 << 31)};
+}
+
+constexpr int64_t kShortRow = 512;  // up to here a row is one wave's
+constexpr int64_t kMostSlices = 64;  // that a wave joins
+
+static u32 row_unit(tgs_dtype t) { return kRowThreads * (u32)(16 / dtype_bytes(t)); }
+static RowPlan pass_plan(int64_t T, int64_t V, tgs_dtype t) { return row_plan(T, V, row_unit(t), 2048, kMostSlices); }
+static RowPlan grad_plan_of(int64_t T, int64_t V, tgs_dtype t) { return row_plan(T, V, row_unit(t), 4096, INT32_MAX); }
+
+static size_t sums_bytes(int64_t T, const RowPlan& p) {
+  return p.slices == 1 ? 0 : round_up_256((size_t)T * p.slices * sizeof(SliceSums));
+}
+static size_t keys_bytes(int64_t T, const RowPlan& p, int32_t top) {
+  return p.slices == 1 ? 0 : round_up_256((size_t)T * p.slices * (size_t)top * 8);
+}
+
+static bool row_sizes(int64_t T, int64_t V) { return T >= 0 && T <= INT32_MAX && V >= 1 && V <= INT32_MAX; }
+
+// Rows of V elements every ld elements.
+static size_t rows_bytes(int64_t T, int64_t V, int64_t ld, tgs_dtype t) {
+  return T == 0 ? 0 : ((size_t)(T - 1) * (size_t)ld + (size_t)V) * dtype_bytes(t);
+}
+
+static tgs_status check_logits(const char* what, const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                               float temperature) {
+  if (T < 0 || T > INT32_MAX) return fail(TGS_EINVAL, "%s: T=%lld outside [0, 2^31-1]", what, (long long)T);
+  if (V < 1 || V > INT32_MAX) return fail(TGS_EINVAL, "%s: V=%lld outside [1, 2^31-1]", what, (long long)V);
+  if (ld < V || ld > INT32_MAX) return fail(TGS_EINVAL, "%s: rows %lld elements apart, outside [V, 2^31-1]", what, (long long)ld);
+  if (!is_float_dtype(dtype)) return fail(TGS_EINVAL, "%s: logits must be fp32, bf16 or fp16", what);
+  if (!(temperature >= 1e-6f && temperature <= 1e6f)) return fail(TGS_EINVAL, "%s: temperature outside [1e-6, 1e6]", what);
+  return check_rows_array(what, "logits", logits, dtype_bytes(dtype), T > 0);
+}
+
+struct Array {
+  const char* name;
+  const void* p;
+  size_t bytes;
+  size_t align;
+  bool needed;
+};
+
+// Nulls, alignment, and outputs that overlap an input or one another.  `same`:
+// the output that may be the logits (the first input) themselves.
+template <int NI, int NO>
+static tgs_status check_arrays(const char* what, const Array (&in)[NI], const Array (&out)[NO], bool same) {
+  for (const Array& x : in)
+    if (tgs_status st = check_rows_array(what, x.name, x.p, x.align, x.needed); st != TGS_OK) return st;
+  for (const Array& x : out)
+    if (tgs_status st = check_rows_array(what, x.name, x.p, x.align, x.needed); st != TGS_OK) return st;
+  for (int o = 0; o < NO; ++o) {
+    for (int i = 0; i < NI; ++i)
+      if (!(same && o == 0 && i == 0) && overlaps(out[o].p, out[o].bytes, in[i].p, in[i].bytes))
+        return fail(TGS_EINVAL, "%s: %s overlaps %s", what, out[o].name, in[i].name);
+    for (int i = 0; i < o; ++i)
+      if (overlaps(out[o].p, out[o].bytes, out[i].p, out[i].bytes))
+        return fail(TGS_EINVAL, "%s: %s overlaps %s", what, out[o].name, out[i].name);
+  }
+  return TGS_OK;
+}
+
+static Logits logits_of(const void* p, int64_t ld, int64_t V, float temperature) {
+  return Logits{p, ld, (u32)V, (float)(1.4426950408889634 / (double)temperature), (float)(1.0 / (double)temperature)};
+}
+
+// Launches over rows [row0, row0 + rows), as many as a launch takes.
+template <class F>
+static void over_rows(int64_t T, int64_t groups_a_row, int threads, F&& f) {
+  const int64_t most = std::max<int64_t>(1, most_groups(threads) / groups_a_row);
+  for (int64_t row0 = 0; row0 < T; row0 += most) f(row0, std::min(most, T - row0));
+}
+
+template <class F>
+static void with_flag(bool b, F&& f) {
+  if (b) f(std::true_type{});
+  else f(std::false_type{});
+}
+
+}  // namespace tgs
+
+using namespace tgs;
+
+extern "C" size_t tgs_token_logprobs_workspace_bytes(int64_t T, int64_t V, tgs_dtype dtype, int32_t top) {
+  if (!row_sizes(T, V) || !is_float_dtype(dtype) || top < 0 || top > kMostTop || top > V) return 0;
+  const RowPlan p = pass_plan(T, V, dtype);
+  return kWorkspaceHeader + sums_bytes(T, p) + keys_bytes(T, p, top);
+}
+
+extern "C" tgs_status tgs_token_logprobs(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                         const void* tokens, tgs_dtype tokens_dtype, float temperature,
+                                         float* logprobs, float* stats, float* entropy, int32_t top,
+                                         int32_t* top_indices, float* top_logprobs, void* workspace,
+                                         size_t workspace_bytes, hipStream_t stream) {
+  const char* what = "token_logprobs";
+  tgs_status st = check_logits(what, logits, dtype, T, V, ld, temperature);
+  if (st != TGS_OK) return st;
+  if (!is_token_dtype(tokens_dtype)) return fail(TGS_EINVAL, "%s: tokens must be int32 or int64", what);
+  if (top < 0 || top > kMostTop || top > V)
+    return fail(TGS_EINVAL, "%s: top=%d outside [0, min(%d, V)]", what, (int)top, kMostTop);
+  const size_t need = tgs_token_logprobs_workspace_bytes(T, V, dtype, top);
+  if ((st = check_rows_workspace(what, workspace, workspace_bytes, need)) != TGS_OK) return st;
+  const size_t ts = dtype_bytes(tokens_dtype), n = (size_t)T * 4;
+  const bool some = T > 0;
+  const Array in[] = {{"logits", logits, rows_bytes(T, V, ld, dtype), dtype_bytes(dtype), some},
+                      {"tokens", tokens, (size_t)T * ts, ts, some}};
+  const Array out[] = {{"logprobs", logprobs, n, 4, some},
+                       {"stats", stats, 2 * n, 4, some},
+                       {"entropy", entropy, n, 4, false},
+                       {"top_indices", top_indices, n * top, 4, some && top > 0},
+                       {"top_logprobs", top_logprobs, n * top, 4, some && top > 0},
+                       {"the workspace", workspace, workspace_bytes, 256, true}};
+  if ((st = check_arrays(what, in, out, false)) != TGS_OK) return st;
+  if (T == 0) return TGS_OK;
+  const RowPlan p = pass_plan(T, V, dtype);
+  char* scratch = (char*)workspace + kWorkspaceHeader;
+  LogprobsArgs a{};
+  a.z = logits_of(logits, ld, V, temperature);
+  a.split = Split{p.slices, p.length, (SliceSums*)scratch, (u64*)(scratch + sums_bytes(T, p))};
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  a.stats = stats;
+  a.entropy = entropy;
+  a.top_indices = top_indices;
+  a.top_logprobs = top_logprobs;
+  a.err = (u32*)workspace;
+  a.T = T;
+  a.top = (u32)top;
+  a.wide = tokens_dtype == TGS_INT64;
+  with_float_dtype(dtype, [&](auto* z) {
+    using Z = std::remove_pointer_t<decltype(z)>;
+    with_flag(entropy != nullptr, [&](auto ent) {
+      with_flag(top > 0, [&](auto tops) {
+        constexpr bool ENT = decltype(ent)::value, TOP = decltype(tops)::value;
+        const int threads = V <= kShortRow ? kWave : kRowThreads;
+        over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
+          a.row0 = row0;
+          const dim3 grid((u32)(rows * p.slices));
+          if (V <= kShortRow) hipLaunchKernelGGL((k_logprobs<Z, kWave, ENT, TOP>), grid, dim3(kWave), 0, stream, a);
+          else hipLaunchKernelGGL((k_logprobs<Z, kRowThreads, ENT, TOP>), grid, dim3(kRowThreads), 0, stream, a);
+          if (p.slices > 1)
+            hipLaunchKernelGGL((k_logprobs_join<Z, ENT, TOP>), dim3((u32)rows), dim3(kRowThreads), 0, stream, a);
+        });
+      });
+    });
+  });
+  return launched(what);
+}
+
+extern "C" tgs_status tgs_token_logprobs_grad(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                              const void* tokens, tgs_dtype tokens_dtype, float temperature,
+                                              const float* stats, const float* grad_logprobs, const float* entropy,
+                                              const float* grad_entropy, void* out, int64_t ld_out, void* workspace,
+                                              size_t workspace_bytes, hipStream_t stream) {
+  const char* what = "token_logprobs_grad";
+  tgs_status st = check_logits(what, logits, dtype, T, V, ld, temperature);
+  if (st != TGS_OK) return st;
+  if (!is_token_dtype(tokens_dtype)) return fail(TGS_EINVAL, "%s: tokens must be int32 or int64", what);
+  if (ld_out < V || ld_out > INT32_MAX) return fail(TGS_EINVAL, "%s: rows of out %lld elements apart", what, (long long)ld_out);
+  if (T > 0 && !grad_logprobs && !grad_entropy) return fail(TGS_EINVAL, "%s: no incoming gradient", what);
+  if (T > 0 && grad_entropy && !entropy) return fail(TGS_EINVAL, "%s: null entropy", what);
+  if ((st = check_rows_workspace(what, workspace, workspace_bytes, kWorkspaceHeader)) != TGS_OK) return st;
+  const size_t ts = dtype_bytes(tokens_dtype), n = (size_t)T * 4;
+  const bool some = T > 0, same = out == logits && ld_out == ld;
+  const Array in[] = {{"logits", logits, rows_bytes(T, V, ld, dtype), dtype_bytes(dtype), some},
+                      {"tokens", tokens, (size_t)T * ts, ts, some},
+                      {"stats", stats, 2 * n, 4, some},
+                      {"grad_logprobs", grad_logprobs, n, 4, false},
+                      {"entropy", grad_entropy ? entropy : nullptr, n, 4, false},
+                      {"grad_entropy", grad_entropy, n, 4, false}};
+  const Array outs[] = {{"out", out, rows_bytes(T, V, ld_out, dtype), dtype_bytes(dtype), some},
+                        {"the workspace", workspace, workspace_bytes, 256, true}};
+  if ((st = check_arrays(what, in, outs, same)) != TGS_OK) return st;
+  if (T == 0) return TGS_OK;
+  const RowPlan p = grad_plan_of(T, V, dtype);
+  LogprobsGradArgs a{};
+  a.z = logits_of(logits, ld, V, temperature);
+  a.tokens = tokens;
+  a.stats = stats;
+  a.grad = grad_logprobs;
+  a.entropy = entropy;
+  a.grad_entropy = grad_entropy;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.err = (u32*)workspace;
+  a.slices = p.slices;
+  a.length = p.length;
+  a.wide = tokens_dtype == TGS_INT64;
+  a.streaming = (size_t)T * V * dtype_bytes(dtype) > kRowsStreamingBytes;
+  with_float_dtype(dtype, [&](auto* z) {
+    using Z = std::remove_pointer_t<decltype(z)>;
+    with_flag(grad_entropy != nullptr, [&](auto ent) {
+      constexpr bool ENT = decltype(ent)::value;
+      const int threads = V <= kShortRow ? kWave : kRowThreads;
+      over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
+        a.row0 = row0;
+        const dim3 grid((u32)(rows * p.slices));
+        if (V <= kShortRow) hipLaunchKernelGGL((k_logprobs_grad<Z, kWave, ENT>), grid, dim3(kWave), 0, stream, a);
+        else hipLaunchKernelGGL((k_logprobs_grad<Z, kRowThreads, ENT>), grid, dim3(kRowThreads), 0, stream, a);
+      });
+    });
+  });
+  return launched(what);
+}
+
+// The three calls of the distillation: losses (out null), a gradient from the
+// forward pass's sums (loss null), both.
+static tgs_status distillation(const char* what, const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                               const void* indices, tgs_dtype indices_dtype, const void* teacher,
+                               tgs_dtype teacher_dtype, int64_t K, float temperature, bool has_loss, float* loss,
+                               bool has_grad, float* stats, const float* given, void* out, int64_t ld_out,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  tgs_status st = check_logits(what, logits, dtype, T, V, ld, temperature);
+  if (st != TGS_OK) return st;
+  if (!is_token_dtype(indices_dtype)) return fail(TGS_EINVAL, "%s: indices must be int32 or int64", what);
+  if (!is_float_dtype(teacher_dtype)) return fail(TGS_EINVAL, "%s: teacher must be fp32, bf16 or fp16", what);
+  if (K < 1 || K > kMostSlots) return fail(TGS_EINVAL, "%s: K=%lld outside [1, %d]", what, (long long)K, kMostSlots);
+  if (has_grad && (ld_out < V || ld_out > INT32_MAX))
+    return fail(TGS_EINVAL, "%s: rows of out %lld elements apart", what, (long long)ld_out);
+  const RowPlan p = pass_plan(T, V, dtype), g = grad_plan_of(T, V, dtype);
+  const size_t need = has_loss ? tgs_distillation_workspace_bytes(T, V, dtype) : kWorkspaceHeader;
+  if ((st = check_rows_workspace(what, workspace, workspace_bytes, need)) != TGS_OK) return st;
+  const size_t is = dtype_bytes(indices_dtype), es = dtype_bytes(teacher_dtype), n = (size_t)T * 4;
+  const bool some = T > 0, same = has_grad && out == logits && ld_out == ld;
+  const Array in[] = {{"logits", logits, rows_bytes(T, V, ld, dtype), dtype_bytes(dtype), some},
+                      {"indices", indices, (size_t)T * K * is, is, some},
+                      {"teacher", teacher, (size_t)T * K * es, es, some},
+                      {has_loss ? "weights" : "grad_loss", given, n, 4, some && !has_loss},
+                      {"stats", has_loss ? nullptr : stats, 2 * n, 4, some && !has_loss}};
+  const Array outs[] = {{"out", has_grad ? out : nullptr, has_grad ? rows_bytes(T, V, ld_out, dtype) : 0, dtype_bytes(dtype),
+                         some && has_grad},
+                        {"loss", has_loss ? loss : nullptr, n, 4, some && has_loss},
+                        {"stats", has_loss ? stats : nullptr, 2 * n, 4, false},
+                        {"the workspace", workspace, workspace_bytes, 256, true}};
+  if ((st = check_arrays(what, in, outs, same)) != TGS_OK) return st;
+  if (T == 0) return TGS_OK;
+  char* scratch = (char*)workspace + kWorkspaceHeader;
+  DistillArgs a{};
+  a.z = logits_of(logits, ld, V, temperature);
+  a.indices = indices;
+  a.teacher = teacher;
+  a.loss = loss;
+  a.stats = stats;
+  a.given = given;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.err = (u32*)workspace;
+  a.K = (u32)K;
+  a.teacher_dtype = teacher_dtype;
+  a.wide = indices_dtype == TGS_INT64;
+  a.streaming = (size_t)T * V * dtype_bytes(dtype) > kRowsStreamingBytes;
+  const bool both = has_loss && has_grad, split = p.slices > 1;
+  // split rows' gradients wait for the join
+  if (both && split) a.stats = (float*)(scratch + sums_bytes(T, p));
+  with_float_dtype(dtype, [&](auto* z) {
+    using Z = std::remove_pointer_t<decltype(z)>;
+    const int threads = V <= kShortRow ? kWave : kRowThreads;
+    if (has_loss) {
+      a.split = Split{p.slices, p.length, (SliceSums*)scratch, nullptr};
+      over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
+        a.row0 = row0;
+        const dim3 grid((u32)(rows * p.slices));
+        with_flag(both && !split, [&](auto grad) {
+          constexpr bool GRAD = decltype(grad)::value;
+          if (V <= kShortRow) hipLaunchKernelGGL((k_distill<Z, kWave, GRAD>), grid, dim3(kWave), 0, stream, a);
+          else hipLaunchKernelGGL((k_distill<Z, kRowThreads, GRAD>), grid, dim3(kRowThreads), 0, stream, a);
+        });
+        if (split) hipLaunchKernelGGL((k_distill_join<Z>), dim3((u32)rows), dim3(kRowThreads), 0, stream, a);
+      });
+      if (!both || !split) return;
+    }
+    a.split = Split{g.slices, g.length, nullptr, nullptr};
+    over_rows(T, g.slices, threads, [&](int64_t row0, int64_t rows) {
+      a.row0 = row0;
+      const dim3 grid((u32)(rows * g.slices));
+      if (V <= kShortRow) hipLaunchKernelGGL((k_distill_grad<Z, kWave>), grid, dim3(kWave), 0, stream, a);
+      else hipLaunchKernelGGL((k_distill_grad<Z, kRowThreads>), grid, dim3(kRowThreads), 0, stream, a);
+    });
+  });
+  return launched(what);
+}
+
+extern "C" size_t tgs_distillation_workspace_bytes(int64_t T, int64_t V, tgs_dtype dtype) {
+  if (!row_sizes(T, V) || !is_float_dtype(dtype)) return 0;
+  const RowPlan p = pass_plan(T, V, dtype);
+  return kWorkspaceHeader + sums_bytes(T, p) + (p.slices == 1 ? 0 : round_up_256((size_t)T * 8));
+}
+
+extern "C" tgs_status tgs_distillation_loss(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                            const void* indices, tgs_dtype indices_dtype, const void* teacher,
+                                            tgs_dtype teacher_dtype, int64_t K, float temperature, float* loss,
+                                            float* stats, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return distillation("distillation_loss", logits, dtype, T, V, ld, indices, indices_dtype, teacher, teacher_dtype, K,
+                      temperature, true, loss, false, stats, nullptr, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+extern "C" tgs_status tgs_distillation_grad(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                            const void* indices, tgs_dtype indices_dtype, const void* teacher,
+                                            tgs_dtype teacher_dtype, int64_t K, float temperature, const float* stats,
+                                            const float* grad_loss, void* out, int64_t ld_out, void* workspace,
+                                            size_t workspace_bytes, hipStream_t stream) {
+  return distillation("distillation_grad", logits, dtype, T, V, ld, indices, indices_dtype, teacher, teacher_dtype, K,
+                      temperature, false, nullptr, true, (float*)stats, grad_loss, out, ld_out, workspace,
+                      workspace_bytes, stream);
+}
+
+extern "C" tgs_status tgs_distillation_loss_and_grad(const void* logits, tgs_dtype dtype, int64_t T, int64_t V,
+                                                     int64_t ld, const void* indices, tgs_dtype indices_dtype,
+                                                     const void* teacher, tgs_dtype teacher_dtype, int64_t K,
+                                                     float temperature, const float* weights, float* loss, void* out,
+                                                     int64_t ld_out, void* workspace, size_t workspace_bytes,
+                                                     hipStream_t stream) {
+  return distillation("distillation_loss_and_grad", logits, dtype, T, V, ld, indices, indices_dtype, teacher,
+                      teacher_dtype, K, temperature, true, loss, true, nullptr, weights, out, ld_out, workspace,
+                      workspace_bytes, stream);
+}

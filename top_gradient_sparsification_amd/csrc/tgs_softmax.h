@@ -1,0 +1,231 @@
+// One pass over a row of logits, and what is made of it.
+//
+// With d = (x - r) / temperature for a reference score r, a thread keeps the
+// sum of e^d and (for the entropy) of d e^d over its elements, relative to a
+// reference of its own: its first vector's largest score, replaced only where
+// a later score is more than 2^24 times as probable.  That is one exponential
+// a value and no running rescale; a row's sums are joined at its largest score.
+#pragma once
+
+#include <limits>
+
+#include "tgs_rows.h"
+
+namespace tgs {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+constexpr float kLowest = -3.402823466385288598117e+38f;
+constexpr float kInf = __builtin_huge_valf();
+constexpr float kRescale = 24.0f;  // powers of two above the reference at which it is replaced
+
+struct Logits {
+  const void* p;
+  int64_t ld;  // elements from row to row
+  u32 V;
+  float c2;   // log2(e) / temperature
+  float inv;  // 1 / temperature
+};
+
+template <class T>
+constexpr int kLogitsVector = 16 / sizeof(T);
+
+template <class T>
+__device__ __forceinline__ T lowest_fill() {
+  return from_f32<T>(-kInf);
+}
+
+// A thread's share: sums relative to `ref`, the largest score and the first
+// vector that holds it (counted in the thread's own).
+struct Share {
+  float ref = kLowest, s = 0.0f, w = 0.0f, top = -kInf;
+  u32 at = 0;
+};
+
+template <class T, int E, bool ENTROPY, bool TOP>
+__device__ __forceinline__ void take(const Vec<T, E>& raw, u32 j, float c2, Share& h) {
+  float x[E], top = -kInf;
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = to_f32(raw.v[e]);
+#pragma unroll
+  for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);
+  if constexpr (TOP) {
+    if (top > h.top) h.at = j;
+  }
+  h.top = fmaxf(h.top, top);
+  const float step = (h.ref - top) * c2;
+  if (step < -kRescale) {
+    const float f = __builtin_amdgcn_exp2f(step);
+    if (f == 0.0f) {
+      h.s *= 0.0f;  // a NaN stays one
+      h.w = 0.0f;
+    } else {
+      if constexpr (ENTROPY) h.w = f * fmaf(h.s, step, h.w);
+      h.s *= f;
+    }
+    h.ref = top;
+  }
+  float s = 0.0f, w = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float d = (x[e] - h.ref) * c2, p = __builtin_amdgcn_exp2f(d);
+    s += p;
+    if constexpr (ENTROPY) w = fmaf(p, fmaxf(d, -1024.0f), w);  // 0 where p is, not 0 times infinity
+  }
+  h.s += s;
+  if constexpr (ENTROPY) h.w += w;
+}
+
+// Elements [c0, c1) of a row by NT threads; thread t takes the vectors that
+// start at c0 + (t + j NT) E.
+template <class T, int NT, bool ENTROPY, bool TOP>
+__device__ __forceinline__ Share row_pass(const T* row, u32 c0, u32 c1, float c2) {
+  constexpr int E = kLogitsVector<T>, U = 4;
+  constexpr u32 kStep = NT * E;
+  Share h;
+  u32 c = c0 + threadIdx.x * E, j = 0;
+  for (u32 rest = c1 - c0; rest >= U * kStep; rest -= U * kStep, c += U * kStep, j += U) {
+    Vec<T, E> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = load_vec<T, E>(row + c + u * kStep);
+#pragma unroll
+    for (int u = 0; u < U; ++u) take<T, E, ENTROPY, TOP>(v[u], j + u, c2, h);
+  }
+  Vec<T, E> v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (c + u * kStep < c1) v[u] = load_part<T, E>(row, c + u * kStep, c1, lowest_fill<T>());
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (c + u * kStep < c1) take<T, E, ENTROPY, TOP>(v[u], j + u, c2, h);
+  return h;
+}
+
+// A row's (or a slice's) sums relative to its largest score m; m = -inf where
+// every score is, and then s = 0.  log_s = log(s).
+struct RowSums {
+  float m, s, w;
+};
+
+template <int NT>
+__device__ __forceinline__ RowSums join_shares(const Share& h, float c2, float* lds) {
+  float m[1] = {h.top};
+  group_reduce<Max, NT>(m, lds);
+  float x[2] = {0.0f, 0.0f};
+  if (h.s != 0.0f) {
+    const float step = (h.ref - m[0]) * c2, f = __builtin_amdgcn_exp2f(step);
+    x[0] = h.s * f;
+    x[1] = f == 0.0f ? 0.0f : f * fmaf(h.s, step, h.w);
+  }
+  group_reduce<Sum, NT>(x, lds + NT / kWave);
+  return RowSums{m[0], x[0], x[1]};
+}
+template <int NT>
+constexpr int kJoinLds = 3 * (NT / kWave);
+
+// ------------------------------------------------------ largest entries --
+// Key of an entry: larger for a larger score, then for a lower index.  -0 counts
+// as +0 and a NaN above infinity.  0 stands for no entry.
+__device__ __forceinline__ u32 score_order(float x) {
+  const u32 b = __float_as_uint(x + 0.0f);
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ u64 entry_key(float x, u32 index) { return (u64)score_order(x) << 32 | (0xFFFFFFFEu - index); }
+__device__ __forceinline__ u32 key_index(u64 key) { return 0xFFFFFFFEu - (u32)key; }
+__device__ __forceinline__ float key_score(u64 key) {
+  const u32 o = (u32)(key >> 32);
+  if (o == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+
+__device__ __forceinline__ u64 readlane64(u64 v, int lane) {
+  return (u64)(u32)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 | (u32)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+constexpr int kMostTop = 64;
+
+template <int NT>
+struct TopLds {
+  static constexpr int kList = NT == kWave ? 512 : 1024;
+  u64 keys[NT];
+  u64 list[kList];
+  u64 out[kMostTop];
+  u64 least;
+  u32 owner[NT];
+  u32 owners, listed;
+};
+
+// The k <= 64 largest keys of what the threads hold, descending, to s.out (0
+// where there are fewer).  `bound` is a key no larger than the thread's largest
+// one (0: it holds none); every thread holds `count` items of E keys at most:
+// keys_of(owner, j, f) calls f(key) for item j of thread `owner`.
+//
+// The k-th largest of 64 groups' bounds is no larger than the k-th largest key.
+// The few threads whose own bound reaches it hold all that do; their items are
+// looked at by the whole workgroup, and the few keys found are ranked by counting.  Where
+// they are too many (an order made for it) or `all` is set (bounds that NaNs
+// passed by), k rounds over everything find the largest below the last.
+template <int NT, class F>
+__device__ __forceinline__ void largest_keys(TopLds<NT>& s, u64 bound, u32 count, u32 k, bool all, F&& keys_of) {
+  const u32 t = threadIdx.x;
+  s.keys[t] = bound;
+  if (t < kMostTop) s.out[t] = 0;
+  if (t == 0) s.owners = s.listed = 0;
+  __syncthreads();
+  if (t < kWave) {
+    u64 g = s.keys[t];
+#pragma unroll
+    for (int i = kWave; i < NT; i += kWave) g = max(g, s.keys[t + i]);
+    u32 larger = 0;
+    for (int i = 0; i < kWave; ++i) {
+      const u64 o = readlane64(g, i);
+      larger += o > g || (o == g && i < (int)t);
+    }
+    if (larger == k - 1) s.least = g;
+  }
+  __syncthreads();
+  const u64 least = s.least;
+  if (!all) {
+    if (bound >= least && bound != 0) s.owner[atomicAdd(&s.owners, 1u)] = t;
+    __syncthreads();
+    const u32 items = s.owners * count;
+    for (u32 i = t; i < items; i += NT) {
+      const u32 o = i / count;
+      keys_of(s.owner[o], i - o * count, [&](u64 key) {
+        if (key < least) return;
+        const u32 at = atomicAdd(&s.listed, 1u);
+        if (at < TopLds<NT>::kList) s.list[at] = key;
+      });
+    }
+    __syncthreads();
+  }
+  const u32 n = s.listed;
+  if (!all && n <= TopLds<NT>::kList) {
+    for (u32 i = t; i < n; i += NT) {
+      const u64 mine = s.list[i];
+      u32 larger = 0;
+      for (u32 o = 0; o < n; ++o) larger += s.list[o] > mine;
+      if (larger < k) s.out[larger] = mine;
+    }
+  } else {
+    u64 last = ~(u64)0;
+    for (u32 r = 0; r < k; ++r) {
+      u64 best = 0;
+      for (u32 j = 0; j < count; ++j)
+        keys_of(t, j, [&](u64 key) {
+          if (key < last && key > best) best = key;
+        });
+      best = wave_max64(best);
+      __syncthreads();
+      if (lane_id() == 0) s.keys[t / kWave] = best;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NT / kWave; ++i) best = max(best, s.keys[i]);
+      if (t == 0) s.out[r] = best;
+      last = best;
+    }
+  }
+  __syncthreads();
+}
+
+}  // namespace tgs
