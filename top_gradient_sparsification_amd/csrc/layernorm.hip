@@ -30,6 +30,140 @@ struct NormArgs {
   bool streaming;
 };
 
+// Where the sum of squares passes fp32's range it is taken of values smaller by
+// this, beside which eps is nothing.
+constexpr float kShrink = 0x1p-80f;
+
+constexpr int norm_threads(int L) { return L > 256 ? L : 256; }
+
+// How a row lies in L lanes of NV vectors of E <= D elements.  Vector i of a lane
+// stands for columns c .. c + E - 1; past the row's end it is moved back to end
+// with the row, so that it is one load without a branch, and its first `skip`
+// elements are another vector's.  Those are computed and stored twice, with the
+// same bits, and left out of the sums.
+template <int E, int L>
+struct Place {
+  u32 D, t;
+  __device__ __forceinline__ u32 column(int i) const { return (i * L + t) * E; }
+  __device__ __forceinline__ bool inside(int i) const { return column(i) < D; }
+  __device__ __forceinline__ u32 at(int i) const { return min(column(i), D - E); }
+  // the same for the whole launch: no lane's vector i passes the row's end
+  __device__ __forceinline__ bool whole(int i) const { return (u32)((i + 1) * L * E) <= D; }
+  // calls f(e, counts) with counts = false where the element is another vector's
+  template <class F>
+  __device__ __forceinline__ void each(int i, F&& f) const {
+    if (whole(i)) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f(e, true);
+    } else {
+      const u32 skip = column(i) - at(i);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f(e, (u32)e >= skip);
+    }
+  }
+};
+
+// Has the compiler read values of narrow types out of their registers again,
+// instead of holding each of them in 32 bits from one pass over them to the next.
+template <class T, int E, int NV>
+__device__ __forceinline__ void forget(Vec<T, E> (&v)[NV]) {
+  if constexpr (sizeof(T) * E >= 8) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      u32 x[sizeof(T) * E / 4];
+      __builtin_memcpy(x, &v[i], sizeof(x));
+#pragma unroll
+      for (u32& y : x) asm volatile("" : "+v"(y));
+      __builtin_memcpy(&v[i], x, sizeof(x));
+    }
+  }
+}
+
+// A lane's parameters.
+template <int E, int L, int NV>
+__device__ __forceinline__ void lane_params(const Place<E, L>& at, const void* p, int dtype, float absent,
+                                            float (&w)[NV][E]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) load_params<E>(p, dtype, at.at(i), at.D, absent, w[i]);
+}
+
+// A row in L lanes of NV vectors of E elements each; a workgroup takes every
+// gridDim.x-th set of rows and keeps its columns' parameters in registers.
+template <class TX, class TY, int E, int L, int NV>
+__global__ __launch_bounds__(norm_threads(L)) void k_norm(NormArgs a) {
+  constexpr int NT = norm_threads(L);
+  __shared__ float s_red[2][L > kWave ? L / kWave : 1];
+  const Place<E, L> at{a.D, threadIdx.x % L};
+  const float D = (float)a.D;
+  float w[NV][E], b[NV][E];
+  lane_params<E, L, NV>(at, a.weight, a.weight_dtype, 1.0f, w);
+  lane_params<E, L, NV>(at, a.bias, a.weight_dtype, 0.0f, b);
+  for (int64_t set = blockIdx.x; set * (NT / L) < a.T; set += gridDim.x) {
+    const int64_t row = set * (NT / L) + threadIdx.x / L;
+    const bool real = row < a.T;
+    const TX* x = (const TX*)a.x + (real ? row : 0) * (int64_t)a.D;
+    Vec<TX, E> raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (at.inside(i)) raw[i] = load_vec<TX, E>(x + at.at(i));
+    float sum[1] = {0.0f}, squares[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float part = 0.0f;
+      at.each(i, [&](int e, bool counts) { part += counts ? to_f32(raw[i].v[e]) : 0.0f; });
+      sum[0] += part;
+    }
+    group_reduce<Sum, L>(sum, s_red[0]);
+    float mean = sum[0] / D, shrink = 1.0f;
+    forget(raw);
+    const auto add_squares = [&] {
+      squares[0] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float part = 0.0f;
+        at.each(i, [&](int e, bool counts) {
+          const float d = counts ? fmaf(to_f32(raw[i].v[e]), shrink, -mean) : 0.0f;
+          part = fmaf(d, d, part);
+        });
+        squares[0] += part;
+      }
+      group_reduce<Sum, L>(squares, s_red[1]);
+    };
+    add_squares();
+    float rstd = 1.0f / sqrtf(squares[0] / D + a.eps);
+    const bool far = !(squares[0] < __builtin_huge_valf());
+    if (__any(far)) {  // the same for a whole workgroup where a row is one
+      if (far) shrink = kShrink;
+      sum[0] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        at.each(i, [&](int e, bool counts) { sum[0] += counts ? to_f32(raw[i].v[e]) * shrink : 0.0f; });
+      group_reduce<Sum, L>(sum, s_red[0]);
+      if (far) mean = sum[0] / D;
+      add_squares();
+      if (far) rstd = 1.0f / sqrtf(squares[0] / D);
+    }
+    forget(raw);
+    if (real) {
+      if (at.t == 0) {
+        if (a.mean) a.mean[row] = mean / shrink;
+        if (a.rstd) a.rstd[row] = rstd * shrink;
+      }
+      TY* out = (TY*)a.out + row * (int64_t)a.D;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!at.inside(i)) continue;
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = fmaf(fmaf(to_f32(raw[i].v[e]), shrink, -mean) * rstd, w[i][e], b[i][e]);
+        const Vec<TY, E> r = round_vec<TY, E>(y);
+        if (a.streaming) store_vec_streaming<TY, E>(out + at.at(i), r);
+        else store_vec<TY, E>(out + at.at(i), r);
+      }
+    }
+  }
+}
+
 // Calls f(e) for the elements of vector [c, c + E) that lie in the row.
 template <int E, class F>
 __device__ __forceinline__ void in_row(u32 c, u32 n, F&& f) {
@@ -40,100 +174,6 @@ __device__ __forceinline__ void in_row(u32 c, u32 n, F&& f) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
       if (c + e < n) f(e);
-  }
-}
-
-// Where the sum of squares passes fp32's range it is taken of values smaller by
-// this, beside which eps is nothing.
-constexpr float kShrink = 0x1p-80f;
-
-constexpr int norm_threads(int L) { return L > 256 ? L : 256; }
-
-// A row in L lanes of NV vectors of E elements each.
-template <class TX, class TY, int E, int L, int NV>
-__global__ __launch_bounds__(norm_threads(L)) void k_norm(NormArgs a) {
-  constexpr int NT = norm_threads(L);
-  __shared__ float s_red[2][L > kWave ? L / kWave : 1];
-  const int64_t row = a.row0 + (int64_t)blockIdx.x * (NT / L) + threadIdx.x / L;
-  const bool real = row < a.T;
-  const u32 D = a.D, t = threadIdx.x % L;
-  const TX* x = (const TX*)a.x + (real ? row : 0) * (int64_t)D;
-  float v[NV][E];
-  float sum[1] = {0.0f}, squares[1] = {0.0f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const u32 c = (i * L + t) * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[i][e] = 0.0f;
-    if (c < D) {
-      const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[i][e] = to_f32(raw.v[e]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float part = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) part += v[i][e];
-    sum[0] += part;
-  }
-  group_reduce<Sum, L>(sum, s_red[0]);
-  const float mean = sum[0] / (float)D;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float part = 0.0f;
-    in_row<E>((i * L + t) * E, D, [&](int e) {
-      v[i][e] -= mean;
-      part = fmaf(v[i][e], v[i][e], part);
-    });
-    squares[0] += part;
-  }
-  group_reduce<Sum, L>(squares, s_red[1]);
-  float rstd = 1.0f / sqrtf(squares[0] / (float)D + a.eps), shown_mean = mean, shown_rstd = rstd;
-  if (__any(!(squares[0] < __builtin_huge_valf()))) {  // the same for a whole workgroup where a row is one
-    float again[1] = {0.0f};
-    Vec<TX, E> raw[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const u32 c = (i * L + t) * E;
-      if (c < D) raw[i] = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
-      in_row<E>(c, D, [&](int e) { again[0] += to_f32(raw[i].v[e]) * kShrink; });
-    }
-    group_reduce<Sum, L>(again, s_red[0]);
-    const float m = again[0] / (float)D;
-    const bool far = !(squares[0] < __builtin_huge_valf());
-    again[0] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      in_row<E>((i * L + t) * E, D, [&](int e) {
-        const float d = to_f32(raw[i].v[e]) * kShrink - m;
-        again[0] = fmaf(d, d, again[0]);
-        if (far) v[i][e] = d;
-      });
-    group_reduce<Sum, L>(again, s_red[1]);
-    if (far) {
-      rstd = 1.0f / sqrtf(again[0] / (float)D);
-      shown_mean = m / kShrink;
-      shown_rstd = rstd * kShrink;
-    }
-  }
-  if (!real) return;
-  if (t == 0) {
-    if (a.mean) a.mean[row] = shown_mean;
-    if (a.rstd) a.rstd[row] = shown_rstd;
-  }
-  TY* out = (TY*)a.out + row * (int64_t)D;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const u32 c = (i * L + t) * E;
-    if (c >= D) continue;
-    float w[E], b[E], y[E];
-    load_params<E>(a.weight, a.weight_dtype, c, D, 1.0f, w);
-    load_params<E>(a.bias, a.weight_dtype, c, D, 0.0f, b);
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = fmaf(v[i][e] * rstd, w[e], b[e]);
-    store_part<TY, E>(out, c, D, round_vec<TY, E>(y), a.streaming);
   }
 }
 
@@ -227,64 +267,65 @@ __global__ __launch_bounds__(norm_threads(L)) void k_norm_grad(NormGradArgs a) {
   constexpr int kCols = L * NV * E;
   __shared__ float s_red[2][2 * (L > kWave ? L / kWave : 1)];
   __shared__ float s_cols[L < 256 ? 2 * kCols : 1];
-  const u32 D = a.D, t = threadIdx.x % L;
+  const Place<E, L> at{a.D, threadIdx.x % L};
+  const u32 D = a.D;
   const float inv = 1.0f / (float)D;
   float w[NV][E], dw[NV][E], db[NV][E];
+  lane_params<E, L, NV>(at, a.weight, a.weight_dtype, 1.0f, w);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const u32 c = (i * L + t) * E;
-    if (c < D) load_params<E>(a.weight, a.weight_dtype, c, D, 1.0f, w[i]);
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[i][e] = db[i][e] = 0.0f;
-  }
   int turn = 0;
   for (int64_t set = blockIdx.x; set * (NT / L) < a.T; set += gridDim.x, turn ^= 1) {
     const int64_t row = set * (NT / L) + threadIdx.x / L;
     const bool real = row < a.T;
-    const int64_t at = (real ? row : 0) * (int64_t)D;
-    const TX* x = (const TX*)a.x + at;
-    const TY* g = (const TY*)a.grad + at;
-    const float mean = real ? a.mean[row] : 0.0f, rstd = real ? a.rstd[row] : 0.0f;
+    const int64_t base = (real ? row : 0) * (int64_t)D;
+    const TX* x = (const TX*)a.x + base;
+    const TY* g = (const TY*)a.grad + base;
     Vec<TX, E> rx[NV];
     Vec<TY, E> rg[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const u32 c = (i * L + t) * E;
-      if (real && c < D) {
-        rx[i] = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
-        rg[i] = load_part<TY, E>(g, c, D, from_f32<TY>(0.0f));
+    for (int i = 0; i < NV; ++i)
+      if (at.inside(i)) {
+        rx[i] = load_vec<TX, E>(x + at.at(i));
+        rg[i] = load_vec<TY, E>(g + at.at(i));
       }
-    }
+    const float mean = a.mean[real ? row : 0], rstd = a.rstd[real ? row : 0];
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float p0 = 0.0f, p1 = 0.0f;
-      if (real)
-        in_row<E>((i * L + t) * E, D, [&](int e) {
-          const float xh = (to_f32(rx[i].v[e]) - mean) * rstd, gv = to_f32(rg[i].v[e]), gw = gv * w[i][e];
-          p0 += gw;
-          p1 = fmaf(gw, xh, p1);
-          dw[i][e] = fmaf(gv, xh, dw[i][e]);
-          db[i][e] += gv;
-        });
+      at.each(i, [&](int e, bool counts) {
+        // a row past the last, or another vector's element, may be a NaN, and adds nothing all the same
+        const bool on = L < NT ? counts && real : counts;
+        const float xh = on ? (to_f32(rx[i].v[e]) - mean) * rstd : 0.0f;
+        const float gv = on ? to_f32(rg[i].v[e]) : 0.0f, gw = gv * w[i][e];
+        p0 += gw;
+        p1 = fmaf(gw, xh, p1);
+        dw[i][e] = fmaf(gv, xh, dw[i][e]);
+        db[i][e] += gv;
+      });
       s[0] += p0;
       s[1] += p1;
     }
     group_reduce<Sum, L>(s, s_red[turn]);
-    if (!real) continue;
     const float m0 = s[0] * inv, m1 = s[1] * inv;
-    TX* out = (TX*)a.out + at;
+    forget(rx);
+    forget(rg);
+    TX* out = (TX*)a.out + base;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const u32 c = (i * L + t) * E;
-      if (c >= D) continue;
+      if (!real || !at.inside(i)) continue;
       float y[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float xh = (to_f32(rx[i].v[e]) - mean) * rstd, gw = to_f32(rg[i].v[e]) * w[i][e];
         y[e] = rstd * fmaf(-xh, m1, gw - m0);
       }
-      store_part<TX, E>(out, c, D, round_vec<TX, E>(y), a.streaming);
+      const Vec<TX, E> r = round_vec<TX, E>(y);
+      if (a.streaming) store_vec_streaming<TX, E>(out + at.at(i), r);
+      else store_vec<TX, E>(out + at.at(i), r);
     }
   }
   if (!a.part) return;
@@ -292,8 +333,9 @@ __global__ __launch_bounds__(norm_threads(L)) void k_norm_grad(NormGradArgs a) {
   if constexpr (L >= 256) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const u32 c = (i * L + t) * E;
-      in_row<E>(c, D, [&](int e) {
+      const u32 c = at.at(i);
+      at.each(i, [&](int e, bool counts) {
+        if (!counts) return;
         part[c + e] = dw[i][e];
         part[(int64_t)D + c + e] = db[i][e];
       });
@@ -315,12 +357,12 @@ __global__ __launch_bounds__(norm_threads(L)) void k_norm_grad(NormGradArgs a) {
       if (threadIdx.x / kWave == turn_of && lane_id() < L) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const u32 c = (i * L + t) * E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
+          const u32 c = at.at(i);
+          at.each(i, [&](int e, bool counts) {
+            if (!counts) return;
             s_cols[c + e] = dw[i][e] + (turn_of ? s_cols[c + e] : 0.0f);
             s_cols[kCols + c + e] = db[i][e] + (turn_of ? s_cols[kCols + c + e] : 0.0f);
-          }
+          });
         }
       }
       __syncthreads();
@@ -417,39 +459,51 @@ __global__ __launch_bounds__(kJoinThreads) void k_norm_join(const float* part, u
 }
 
 // ------------------------------------------------------------------ host --
-static int norm_vector(tgs_dtype a, tgs_dtype b) { return dtype_bytes(a) == 2 && dtype_bytes(b) == 2 ? 8 : 4; }
+constexpr int64_t kMostD = (int64_t)1 << 24;  // exact in fp32, and no launch reaches 2^32 threads
+// Vectors of a row that registers hold: on the way back they hold the columns' sums too.
+constexpr int64_t kMostHeld = 4096;
+template <int E>
+constexpr int64_t kMostHeldBack = E == 4 ? 4096 : 2048;
 
-// Lanes and vectors a lane for rows of `vectors`: the smallest that holds them.
-// Calls f(L, NV) as integral constants; false where none does.
-template <class F>
-static bool with_shape(u32 vectors, F&& f) {
+
+// Elements of a vector, lanes of a row and vectors a lane for rows of D: the
+// smallest that holds them.  Calls f(E, L, NV) as integral constants; false where
+// none does.
+template <int E, class F>
+static bool with_shape(int64_t D, int64_t most, F&& f) {
+  const int64_t vectors = (D + E - 1) / E;
+  const auto call = [&](auto e, auto l, auto nv) { f(e, l, nv); };
   using std::integral_constant;
-  if (vectors <= 8) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  else if (vectors <= 32) f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  else if (vectors <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  else if (vectors <= 128) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  else if (vectors <= 256) f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-  else if (vectors <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  else if (vectors <= 1024) f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-  else if (vectors <= 2048) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  constexpr integral_constant<int, E> e{};
+  if (D < E) call(integral_constant<int, 1>{}, integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (vectors <= 8) call(e, integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (vectors <= 32) call(e, integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  else if (vectors <= 64) call(e, integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (vectors <= 128) call(e, integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (vectors <= 256) call(e, integral_constant<int, 64>{}, integral_constant<int, 4>{});
+  else if (vectors <= 512) call(e, integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (vectors <= 1024) call(e, integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (vectors <= 2048) call(e, integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  else if (vectors <= most) call(e, integral_constant<int, 1024>{}, integral_constant<int, 4>{});
   else return false;
   return true;
 }
 
-constexpr int64_t kMostD = (int64_t)1 << 24;  // exact in fp32, and no launch reaches 2^32 threads
-constexpr u32 kMostHeld = 2048;  // vectors of a row that registers hold
-
-// Workgroups that add up the parameters' gradients, hence partial rows.
-static int64_t norm_groups(int64_t T, int64_t D, int E) {
-  const u32 vectors = (u32)((D + E - 1) / E);
-  if (vectors > kMostHeld) return std::max<int64_t>(1, std::min<int64_t>(64, T));
-  int64_t rows = 1;
-  int threads = 256;
-  with_shape(vectors, [&](auto l, auto) {
-    threads = norm_threads(l.value);
-    rows = threads / l.value;
+// Workgroups that add up the parameters' gradients, hence partial rows.  With one
+// vector a lane, whose five workgroups a unit all reside, 1,280: 1,000,000 rows of
+// 64 in bf16 take 134, 102, 83 and 112 us with 512, 768, 1,280 and 1,536, 262,144 of
+// 512 273, 212, 168 and 218.  With more vectors 512: 131,072 of 2,048 309, 326 and 311
+// with 512, 768 and 1,024, 65,536 of 4,096 304, 318 and 344, 65,536 of 1,024 79, 84
+// and 86.  Of 1,024 threads 256: 16,384 rows of 16,384 480, 309 and 328 with 128, 256
+// and 512.
+template <int E>
+static int64_t norm_groups(int64_t T, int64_t D) {
+  int64_t rows = 1, most = 64;
+  with_shape<E>(D, kMostHeldBack<E>, [&](auto, auto l, auto nv) {
+    constexpr int NT = norm_threads(decltype(l)::value);
+    rows = NT / decltype(l)::value;
+    most = NT > 256 ? 256 : decltype(nv)::value == 1 ? 1280 : 512;
   });
-  const int64_t most = threads > 256 ? 256 : 512;
   return std::max<int64_t>(1, std::min(most, (T + rows - 1) / rows));
 }
 
@@ -511,15 +565,17 @@ extern "C" tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T
     using TX = std::remove_pointer_t<decltype(tx)>;
     using TY = std::remove_pointer_t<decltype(ty)>;
     constexpr int E = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
-    const u32 vectors = (u32)((D + E - 1) / E);
-    const bool held = with_shape(vectors, [&](auto l, auto nv) {
-      constexpr int L = decltype(l)::value, NV = decltype(nv)::value, NT = norm_threads(L);
-      const int64_t most = most_groups(NT) * (NT / L);
-      for (a.row0 = 0; a.row0 < T; a.row0 += most) {
-        const int64_t rows = std::min(most, T - a.row0);
-        hipLaunchKernelGGL((k_norm<TX, TY, E, L, NV>), dim3((u32)((rows + NT / L - 1) / (NT / L))), dim3(NT), 0,
-                           stream, a);
-      }
+    const bool held = with_shape<E>(D, kMostHeld, [&](auto e, auto l, auto nv) {
+      constexpr int L = decltype(l)::value, NT = norm_threads(L);
+      // Workgroups at most.  Of several rows each 8,192 (131,072 rows of 2,048 in bf16 190 us; 193 with 4,096, 197
+      // with 16,384).  Of one row, as many as reside: with two and four vectors a thread 1,024 and 768 (65,536 of
+      // 4,096 225, 200 and 216 us with 768, 1,024 and 1,536; 32,768 of 8,192 193, 227 and 201 with 768, 1,024 and
+      // 1,280), of 1,024 threads 512 and 256 (8,192 of 8,192, fp32 to bf16, 87, 77 and 76 us with 256, 512 and 1,024;
+      // 4,000 of 20,000 in bf16 124 and 134 with 256 and 512).
+      constexpr int64_t kOneRow = decltype(nv)::value == 2 ? (L == 256 ? 1024 : 512) : (L == 256 ? 768 : 256);
+      const int64_t sets = (T + NT / L - 1) / (NT / L), most = L <= kWave ? 8192 : kOneRow;
+      hipLaunchKernelGGL((k_norm<TX, TY, decltype(e)::value, L, decltype(nv)::value>), dim3((u32)std::min(sets, most)),
+                         dim3(NT), 0, stream, a);
     });
     if (!held) {
       const int64_t most = most_groups(kLongThreads);
@@ -534,7 +590,7 @@ extern "C" tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T
 extern "C" size_t tgs_layer_norm_grad_workspace_bytes(int64_t T, int64_t D) {
   if (T < 0 || T > INT32_MAX || D < 1 || D > kMostD) return 0;
   // the types decide how many lanes a row takes: the most of either
-  const int64_t groups = std::max(norm_groups(T, D, 4), norm_groups(T, D, 8));
+  const int64_t groups = std::max(norm_groups<4>(T, D), norm_groups<8>(T, D));
   return kWorkspaceHeader + round_up_256((size_t)groups * 2 * (size_t)D * 4);
 }
 
@@ -590,16 +646,17 @@ extern "C" tgs_status tgs_layer_norm_grad(const void* grad, tgs_dtype grad_dtype
   a.D = (u32)D;
   a.weight_dtype = weight_dtype;
   a.streaming = nx > kRowsStreamingBytes;
-  const int64_t groups = T == 0 ? 0 : norm_groups(T, D, norm_vector(x_dtype, grad_dtype));
+  int64_t groups = 0;
   if (T > 0)
     with_two_types(x_dtype, grad_dtype, [&](auto* tx, auto* ty) {
       using TX = std::remove_pointer_t<decltype(tx)>;
       using TY = std::remove_pointer_t<decltype(ty)>;
       constexpr int E = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
-      const u32 vectors = (u32)((D + E - 1) / E);
-      const bool held = with_shape(vectors, [&](auto l, auto nv) {
-        constexpr int L = decltype(l)::value, NV = decltype(nv)::value, NT = norm_threads(L);
-        hipLaunchKernelGGL((k_norm_grad<TX, TY, E, L, NV>), dim3((u32)groups), dim3(NT), 0, stream, a);
+      groups = norm_groups<E>(T, D);
+      const bool held = with_shape<E>(D, kMostHeldBack<E>, [&](auto e, auto l, auto nv) {
+        constexpr int L = decltype(l)::value;
+        hipLaunchKernelGGL((k_norm_grad<TX, TY, decltype(e)::value, L, decltype(nv)::value>), dim3((u32)groups),
+                           dim3(norm_threads(L)), 0, stream, a);
       });
       if (!held) {
         if (params)
