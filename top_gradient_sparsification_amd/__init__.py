@@ -41,8 +41,8 @@ call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -972,9 +972,12 @@ def muon_step(weight: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, 
 
 
 # ------------------------------------------ rows, from hidden states to losses --
-def _on(dev):
-    """Launches go to the current device: the tensors' own for the time of a call."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _call(dev, entry, *args):
+    """A C entry's status; launches go to the current device, which is the tensors' own for the time of the call."""
+    if dev.index == torch._C._cuda_getDevice():
+        return entry(*args)
+    with torch.cuda.device(dev):
+        return entry(*args)
 
 
 class _NoWayBack(torch.autograd.Function):
@@ -991,7 +994,17 @@ class _NoWayBack(torch.autograd.Function):
 
 
 def _tracked(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
+@functools.lru_cache(maxsize=1024)
+def _need(query, *sizes) -> int:
+    """What a workspace query of the library says of these sizes and types."""
+    return int(getattr(_load(), query)(*sizes))
 
 
 def _spaced_rows(t, name, dtypes, device=None):
@@ -1036,7 +1049,7 @@ def _places(t, dtypes, name, device, shape):
 def _rows_out(logits, out):
     """(out, its elements from row to row, whether it was given) of a gradient of ``logits``."""
     if out is None:
-        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), logits.shape[-1], False
+        return logits.new_empty(logits.shape), logits.shape[-1], False
     _, _, gap = _spaced_rows(out, "out", (logits.dtype,), logits.device)
     if out.shape != logits.shape:
         raise ValueError("out must have shape %s" % (tuple(logits.shape),))
@@ -1108,17 +1121,16 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
         out_dtype = out_dtype or x.dtype
         if out_dtype not in _FLOATS:
             raise TypeError("out_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
-        out = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        out = x.new_empty(x.shape, dtype=out_dtype)
     else:
         _places(out, _FLOATS if out_dtype is None else (out_dtype,), "out", dev, x.shape)
     mean = rstd = None
     if return_stats:
-        mean, rstd = x.new_empty((2, *x.shape[:-1]), dtype=torch.float32)
-    with _on(dev):
-        st = _load().tgs_layer_norm(x.data_ptr(), _DTYPES[x.dtype], x.numel() // D if D else 0, D,
-                                    None if weight is None else weight.data_ptr(),
-                                    None if bias is None else bias.data_ptr(), 0 if wt is None else _DTYPES[wt], eps,
-                                    out.data_ptr(), _DTYPES[out.dtype], _ptr(mean), _ptr(rstd), _stream_handle(dev))
+        mean, rstd = x.new_empty((2, *x.shape[:-1]), dtype=torch.float32).unbind()
+    st = _call(dev, _load().tgs_layer_norm, x.data_ptr(), _DTYPES[x.dtype], x.numel() // D if D else 0, D,
+               None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
+               0 if wt is None else _DTYPES[wt], eps, out.data_ptr(), _DTYPES[out.dtype], _ptr(mean), _ptr(rstd),
+               _stream_handle(dev))
     if st:
         _check(st, "tgs_layer_norm")
     if given:
@@ -1160,7 +1172,7 @@ def layer_norm_grad(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rst
         return results if params else (results[0], None, None)
     given = out is not None
     if not given:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(x.shape)
     else:
         _places(out, (x.dtype,), "out", dev, x.shape)
     gw = gb = None
@@ -1168,17 +1180,14 @@ def layer_norm_grad(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rst
         param_dtype = param_dtype or (torch.float32 if weight is None else weight.dtype)
         if param_dtype not in _FLOATS:
             raise TypeError("param_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
-        gw, gb = (torch.empty(D, dtype=param_dtype, device=dev) for _ in range(2))
+        gw, gb = x.new_empty(D, dtype=param_dtype), x.new_empty(D, dtype=param_dtype)
     T = x.numel() // D if D else 0
-    lib = _load()
-    with _on(dev):
-        stream = _stream_handle(dev)
-        ws = _row_scratch(ws, lib.tgs_layer_norm_grad_workspace_bytes(T, D), dev, stream, "layer_norm_grad")
-        st = lib.tgs_layer_norm_grad(grad.data_ptr(), _DTYPES[grad.dtype], x.data_ptr(), _DTYPES[x.dtype], T, D,
-                                     mean.data_ptr(), rstd.data_ptr(), None if weight is None else weight.data_ptr(),
-                                     0 if weight is None else _DTYPES[weight.dtype], out.data_ptr(), _ptr(gw),
-                                     _ptr(gb), _DTYPES[param_dtype] if params else 0, ws.data_ptr(), ws.numel(),
-                                     stream)
+    stream = _stream_handle(dev)
+    ws = _row_scratch(ws, _need("tgs_layer_norm_grad_workspace_bytes", T, D), dev, stream, "layer_norm_grad")
+    st = _call(dev, _load().tgs_layer_norm_grad, grad.data_ptr(), _DTYPES[grad.dtype], x.data_ptr(), _DTYPES[x.dtype],
+               T, D, mean.data_ptr(), rstd.data_ptr(), None if weight is None else weight.data_ptr(),
+               0 if weight is None else _DTYPES[weight.dtype], out.data_ptr(), _ptr(gw), _ptr(gb),
+               _DTYPES[param_dtype] if params else 0, ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_layer_norm_grad")
     if given:
@@ -1244,22 +1253,20 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: floa
         return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, top, entropy, ws))
     top = int(top)
     shape = tokens.shape
-    logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
-    stats = torch.empty((*shape, 2), dtype=torch.float32, device=dev)
-    ent = torch.empty(shape, dtype=torch.float32, device=dev) if entropy else None
+    logprobs = logits.new_empty(shape, dtype=torch.float32)
+    stats = logits.new_empty((*shape, 2), dtype=torch.float32)
+    ent = logits.new_empty(shape, dtype=torch.float32) if entropy else None
     at = values = None
     if top > 0:
-        at = torch.empty((*shape, top), dtype=torch.int32, device=dev)
-        values = torch.empty((*shape, top), dtype=torch.float32, device=dev)
-    lib = _load()
+        at = logits.new_empty((*shape, top), dtype=torch.int32)
+        values = logits.new_empty((*shape, top), dtype=torch.float32)
     dt = _DTYPES[logits.dtype]
-    with _on(dev):
-        stream = _stream_handle(dev)
-        need = lib.tgs_token_logprobs_workspace_bytes(T, V, dt, top)
-        ws = _row_scratch(ws, need, dev, stream, "token_logprobs: V=%d, top=%d" % (V, top) if need == 0 else "")
-        st = lib.tgs_token_logprobs(logits.data_ptr(), dt, T, V, gap, tokens.data_ptr(), _DTYPES[tokens.dtype],
-                                    temperature, logprobs.data_ptr(), stats.data_ptr(), _ptr(ent), top, _ptr(at),
-                                    _ptr(values), ws.data_ptr(), ws.numel(), stream)
+    stream = _stream_handle(dev)
+    need = _need("tgs_token_logprobs_workspace_bytes", T, V, dt, top)
+    ws = _row_scratch(ws, need, dev, stream, "token_logprobs: V=%d, top=%d" % (V, top) if need == 0 else "")
+    st = _call(dev, _load().tgs_token_logprobs, logits.data_ptr(), dt, T, V, gap, tokens.data_ptr(),
+               _DTYPES[tokens.dtype], temperature, logprobs.data_ptr(), stats.data_ptr(), _ptr(ent), top, _ptr(at),
+               _ptr(values), ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_token_logprobs")
     return TokenLogprobs(logprobs, ent, values, at, stats)
@@ -1296,13 +1303,11 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, stats: torch
             logits, tokens, stats, grad_logprobs, entropy, grad_entropy, temperature, ws=ws),
             logits, stats, grad_logprobs, entropy, grad_entropy)
     out, gap_out, given = _rows_out(logits, out)
-    with _on(dev):
-        stream = _stream_handle(dev)
-        ws = _row_scratch(ws, _HEADER_BYTES, dev, stream, "")
-        st = _load().tgs_token_logprobs_grad(
-            logits.data_ptr(), _DTYPES[logits.dtype], T, V, gap, tokens.data_ptr(), _DTYPES[tokens.dtype], temperature,
-            stats.data_ptr(), _ptr(grad_logprobs), _ptr(entropy), _ptr(grad_entropy), out.data_ptr(), gap_out,
-            ws.data_ptr(), ws.numel(), stream)
+    stream = _stream_handle(dev)
+    ws = _row_scratch(ws, _HEADER_BYTES, dev, stream, "")
+    st = _call(dev, _load().tgs_token_logprobs_grad, logits.data_ptr(), _DTYPES[logits.dtype], T, V, gap,
+               tokens.data_ptr(), _DTYPES[tokens.dtype], temperature, stats.data_ptr(), _ptr(grad_logprobs),
+               _ptr(entropy), _ptr(grad_entropy), out.data_ptr(), gap_out, ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_token_logprobs_grad")
     if given:
@@ -1368,17 +1373,15 @@ def distillation_loss(logits: torch.Tensor, teacher_indices: torch.Tensor, teach
     if _tracked(logits):
         loss, stats = _DistillationLoss.apply(logits, teacher_indices, teacher_logits, temperature, ws)
         return (loss, stats) if return_stats else loss
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=dev)
-    stats = torch.empty((*logits.shape[:-1], 2), dtype=torch.float32, device=dev) if return_stats else None
-    lib = _load()
+    shape = logits.shape[:-1]
+    loss = logits.new_empty(shape, dtype=torch.float32)
+    stats = logits.new_empty((*shape, 2), dtype=torch.float32) if return_stats else None
     dt = _DTYPES[logits.dtype]
-    with _on(dev):
-        stream = _stream_handle(dev)
-        ws = _row_scratch(ws, lib.tgs_distillation_workspace_bytes(T, V, dt), dev, stream, "distillation_loss")
-        st = lib.tgs_distillation_loss(logits.data_ptr(), dt, T, V, gap, teacher_indices.data_ptr(),
-                                       _DTYPES[teacher_indices.dtype], teacher_logits.data_ptr(),
-                                       _DTYPES[teacher_logits.dtype], K, temperature, loss.data_ptr(), _ptr(stats),
-                                       ws.data_ptr(), ws.numel(), stream)
+    stream = _stream_handle(dev)
+    ws = _row_scratch(ws, _need("tgs_distillation_workspace_bytes", T, V, dt), dev, stream, "distillation_loss")
+    st = _call(dev, _load().tgs_distillation_loss, logits.data_ptr(), dt, T, V, gap, teacher_indices.data_ptr(),
+               _DTYPES[teacher_indices.dtype], teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], K, temperature,
+               loss.data_ptr(), _ptr(stats), ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_distillation_loss")
     return (loss, stats) if return_stats else loss
@@ -1403,13 +1406,12 @@ def distillation_grad(logits: torch.Tensor, teacher_indices: torch.Tensor, teach
         return _NoWayBack.apply("distillation_grad", lambda: distillation_grad(
             logits, teacher_indices, teacher_logits, stats, grad_loss, temperature, ws=ws), logits, stats, grad_loss)
     out, gap_out, given = _rows_out(logits, out)
-    with _on(dev):
-        stream = _stream_handle(dev)
-        ws = _row_scratch(ws, _HEADER_BYTES, dev, stream, "")
-        st = _load().tgs_distillation_grad(
-            logits.data_ptr(), _DTYPES[logits.dtype], T, V, gap, teacher_indices.data_ptr(),
-            _DTYPES[teacher_indices.dtype], teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], K, temperature,
-            stats.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), gap_out, ws.data_ptr(), ws.numel(), stream)
+    stream = _stream_handle(dev)
+    ws = _row_scratch(ws, _HEADER_BYTES, dev, stream, "")
+    st = _call(dev, _load().tgs_distillation_grad, logits.data_ptr(), _DTYPES[logits.dtype], T, V, gap,
+               teacher_indices.data_ptr(), _DTYPES[teacher_indices.dtype], teacher_logits.data_ptr(),
+               _DTYPES[teacher_logits.dtype], K, temperature, stats.data_ptr(), grad_loss.data_ptr(), out.data_ptr(),
+               gap_out, ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_distillation_grad")
     if given:
@@ -1437,17 +1439,15 @@ def distillation_loss_and_grad(logits: torch.Tensor, teacher_indices: torch.Tens
             raise RuntimeError("an input requires a gradient, which a call with out= has not")
         return _NoWayBack.apply("distillation_loss_and_grad", lambda: distillation_loss_and_grad(
             logits, teacher_indices, teacher_logits, weights, temperature, ws=ws), logits, weights)
-    loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=dev)
+    loss = logits.new_empty(logits.shape[:-1], dtype=torch.float32)
     out, gap_out, given = _rows_out(logits, out)
-    lib = _load()
     dt = _DTYPES[logits.dtype]
-    with _on(dev):
-        stream = _stream_handle(dev)
-        ws = _row_scratch(ws, lib.tgs_distillation_workspace_bytes(T, V, dt), dev, stream, "distillation_loss_and_grad")
-        st = lib.tgs_distillation_loss_and_grad(
-            logits.data_ptr(), dt, T, V, gap, teacher_indices.data_ptr(), _DTYPES[teacher_indices.dtype],
-            teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], K, temperature, _ptr(weights), loss.data_ptr(),
-            out.data_ptr(), gap_out, ws.data_ptr(), ws.numel(), stream)
+    stream = _stream_handle(dev)
+    ws = _row_scratch(ws, _need("tgs_distillation_workspace_bytes", T, V, dt), dev, stream, "distillation_loss_and_grad")
+    st = _call(dev, _load().tgs_distillation_loss_and_grad, logits.data_ptr(), dt, T, V, gap,
+               teacher_indices.data_ptr(), _DTYPES[teacher_indices.dtype], teacher_logits.data_ptr(),
+               _DTYPES[teacher_logits.dtype], K, temperature, _ptr(weights), loss.data_ptr(), out.data_ptr(), gap_out,
+               ws.data_ptr(), ws.numel(), stream)
     if st:
         _check(st, "tgs_distillation_loss_and_grad")
     if given:

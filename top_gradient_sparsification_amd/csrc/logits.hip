@@ -19,6 +19,7 @@
 namespace tgs {
 
 constexpr int kRowThreads = 256;
+constexpr int kMostSlices = 64;  // of a row, that a wave joins
 
 // What one slice of a row leaves for the join: its sums, and behind all of them
 // its largest keys.
@@ -31,7 +32,57 @@ struct Split {
   u32 length;  // elements of a slice, a multiple of every vector
   SliceSums* sums;  // [row][slice]
   u64* keys;        // [row][slice][top]
+  u32* arrived;     // [row] workgroups that are done, 0 between calls
 };
+
+// Stores a slice's sums where every workgroup of its row sees them.
+__device__ __forceinline__ void store_slice(const Split& split, int64_t row, u32 slice, const RowSums& r) {
+  float* p = &split.sums[row * split.slices + slice].m;
+  st_agent_f32(p, r.m);
+  st_agent_f32(p + 1, r.s);
+  st_agent_f32(p + 2, r.w);
+}
+
+// Whether this workgroup is the last of its row to come here: what the others
+// stored at device scope before is there to be loaded at device scope.
+__device__ __forceinline__ bool last_of_row(const Split& split, int64_t row, u32* lds) {
+  wait_all_memory();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const u32 before = add_agent_relaxed(split.arrived + row, 1u);
+    if (before == split.slices - 1) st_agent(split.arrived + row, 0u);
+    *lds = before;
+  }
+  __syncthreads();
+  return *lds == split.slices - 1;
+}
+
+// A row's sums from its slices' (64 at most), by the first wave; every thread gets them.
+__device__ __forceinline__ RowSums join_slices(const Split& split, int64_t row, float c2, float* lds) {
+  if (threadIdx.x < kWave) {
+    RowSums p{-kInf, 0.0f, 0.0f};
+    if (threadIdx.x < split.slices) {
+      const u32* q = (const u32*)&split.sums[row * split.slices + threadIdx.x];
+      p = RowSums{__uint_as_float(ld_agent(q)), __uint_as_float(ld_agent(q + 1)), __uint_as_float(ld_agent(q + 2))};
+    }
+    const float m = lanes_reduce<Max, kWave>(p.m);
+    float s = 0.0f, w = 0.0f;
+    if (p.s != 0.0f) {
+      const float step = (p.m - m) * c2, f = p.m == m ? 1.0f : __builtin_amdgcn_exp2f(step);
+      s = p.s * f;
+      w = p.m == m ? p.w : f == 0.0f ? 0.0f : f * fmaf(p.s, step, p.w);
+    }
+    s = lanes_reduce<Sum, kWave>(s);
+    w = lanes_reduce<Sum, kWave>(w);
+    if (threadIdx.x == 0) {
+      lds[0] = m;
+      lds[1] = s;
+      lds[2] = w;
+    }
+  }
+  __syncthreads();
+  return RowSums{lds[0], lds[1], lds[2]};
+}
 
 __device__ __forceinline__ int64_t load_index(const void* p, bool wide, int64_t i) {
   return wide ? ((const int64_t*)p)[i] : (int64_t)((const int32_t*)p)[i];
@@ -83,13 +134,13 @@ __device__ __forceinline__ void write_logprobs(const LogprobsArgs& a, int64_t ro
   }
 }
 
-template <class T, int NT, bool ENTROPY, bool TOP>
+template <class T, int NT, bool ENTROPY, bool TOP, bool SPLIT>
 __global__ __launch_bounds__(NT) void k_logprobs(LogprobsArgs a) {
   constexpr int E = kLogitsVector<T>;
   __shared__ float s_red[kJoinLds<NT>];
   __shared__ std::conditional_t<TOP, TopLds<NT>, int> s_top;
-  const u32 slices = a.split.slices, slice = slices == 1 ? 0 : blockIdx.x % slices;
-  const int64_t row = a.row0 + (slices == 1 ? blockIdx.x : blockIdx.x / slices);
+  const u32 slices = SPLIT ? a.split.slices : 1, slice = SPLIT ? blockIdx.x % slices : 0;
+  const int64_t part = SPLIT ? blockIdx.x / slices : blockIdx.x, row = a.row0 + part;
   const int token = load_entry(a.tokens, a.wide, row, a.z.V, a.err);
   if (token < 0) {  // nothing of the row is read
     if (slice == 0) write_logprobs<ENTROPY>(a, row, -1, 0.0f, RowSums{0.0f, 1.0f, 0.0f}, nullptr);
@@ -97,9 +148,10 @@ __global__ __launch_bounds__(NT) void k_logprobs(LogprobsArgs a) {
   }
   const T* z = (const T*)a.z.p + row * a.z.ld;
   const float score = to_f32(z[token]);
-  const u32 c0 = slice * a.split.length, c1 = min(c0 + a.split.length, a.z.V);
+  const u32 c0 = SPLIT ? slice * a.split.length : 0, c1 = SPLIT ? min(c0 + a.split.length, a.z.V) : a.z.V;
   const Share h = row_pass<T, NT, ENTROPY, TOP>(z, c0, c1, a.z.c2);
-  const RowSums r = join_shares<NT>(h, a.z.c2, s_red);
+  RowSums r = join_shares<NT>(h, a.z.c2, s_red);
+  const u64* keys = nullptr;
   if constexpr (TOP) {
     const u32 first = c0 + threadIdx.x * E, at = first + h.at * (NT * E);
     const u64 bound = first < c1 ? entry_key(h.top, min(at + E, c1) - 1) : 0;
@@ -111,64 +163,34 @@ __global__ __launch_bounds__(NT) void k_logprobs(LogprobsArgs a) {
       for (int e = 0; e < E; ++e)
         if (c + e < c1) f(entry_key(to_f32(v.v[e]), c + e));
     });
-  }
-  const u64* keys = nullptr;
-  if constexpr (TOP) keys = s_top.out;
-  if (slices == 1) {
-    write_logprobs<ENTROPY>(a, row, token, score, r, keys);
-    return;
-  }
-  const int64_t part = (row - a.row0) * slices + slice;
-  if (threadIdx.x == 0) a.split.sums[part] = SliceSums{r.m, r.s, r.w, 0.0f};
-  for (u32 i = threadIdx.x; i < a.top; i += NT) a.split.keys[part * a.top + i] = keys[i];
-}
-
-// A row's sums from its slices' (64 at most), by the first wave; every thread gets them.
-__device__ __forceinline__ RowSums join_slices(const Split& split, int64_t row, float c2, float* lds) {
-  if (threadIdx.x < kWave) {
-    SliceSums p{-kInf, 0.0f, 0.0f, 0.0f};
-    if (threadIdx.x < split.slices) p = split.sums[row * split.slices + threadIdx.x];
-    const float m = lanes_reduce<Max, kWave>(p.m);
-    float s = 0.0f, w = 0.0f;
-    if (p.s != 0.0f) {
-      const float step = (p.m - m) * c2, f = p.m == m ? 1.0f : __builtin_amdgcn_exp2f(step);
-      s = p.s * f;
-      w = p.m == m ? p.w : f == 0.0f ? 0.0f : f * fmaf(p.s, step, p.w);
-    }
-    s = lanes_reduce<Sum, kWave>(s);
-    w = lanes_reduce<Sum, kWave>(w);
-    if (threadIdx.x == 0) {
-      lds[0] = m;
-      lds[1] = s;
-      lds[2] = w;
-    }
-  }
-  __syncthreads();
-  return RowSums{lds[0], lds[1], lds[2]};
-}
-
-template <class T, bool ENTROPY, bool TOP>
-__global__ __launch_bounds__(kRowThreads) void k_logprobs_join(LogprobsArgs a) {
-  constexpr int NT = kRowThreads;
-  __shared__ float s_red[4];
-  __shared__ std::conditional_t<TOP, TopLds<NT>, int> s_top;
-  const int64_t row = a.row0 + blockIdx.x;
-  const int token = load_entry(a.tokens, a.wide, row, a.z.V, a.err);
-  if (token < 0) return;  // written
-  const float score = to_f32(((const T*)a.z.p)[row * a.z.ld + token]);
-  const RowSums r = join_slices(a.split, blockIdx.x, a.z.c2, s_red);
-  const u64* keys = nullptr;
-  if constexpr (TOP) {
-    // thread t holds the keys t, t + NT, ..
-    const u32 n = a.split.slices * a.top, count = (n + NT - 1) / NT;
-    const u64* all = a.split.keys + (int64_t)blockIdx.x * n;
-    u64 bound = 0;
-    for (u32 i = threadIdx.x; i < n; i += NT) bound = max(bound, all[i]);
-    largest_keys<NT>(s_top, bound, count, a.top, false, [&](u32 owner, u32 j, auto&& f) {
-      const u32 i = owner + j * NT;
-      if (i < n && all[i] != 0) f(all[i]);
-    });
     keys = s_top.out;
+  }
+  if constexpr (SPLIT) {
+    __shared__ u32 s_last;
+    __shared__ float s_sums[3];
+    if (threadIdx.x == 0) store_slice(a.split, part, slice, r);
+    if constexpr (TOP)
+      for (u32 i = threadIdx.x; i < a.top; i += NT) st_agent64(a.split.keys + (part * slices + slice) * a.top + i, keys[i]);
+    if (!last_of_row(a.split, part, &s_last)) return;
+    r = join_slices(a.split, part, a.z.c2, s_sums);
+    if constexpr (TOP) {
+      // thread t holds the keys t, t + NT, .. of the slices'
+      const u32 n = slices * a.top;
+      const u64* all = a.split.keys + part * n;
+      u64 held[kMostSlices * kMostTop / NT], bound = 0;
+#pragma unroll
+      for (int j = 0; j < kMostSlices * kMostTop / NT; ++j) {
+        const u32 i = threadIdx.x + j * NT;
+        held[j] = i < n ? ld_agent64(all + i) : 0;
+      }
+#pragma unroll
+      for (u64 key : held) bound = max(bound, key);
+      largest_keys<NT>(s_top, bound, (n + NT - 1) / NT, a.top, false, [&](u32 owner, u32 j, auto&& f) {
+        const u32 i = owner + j * NT;
+        const u64 key = i < n ? ld_agent64(all + i) : 0;
+        if (key != 0) f(key);
+      });
+    }
   }
   write_logprobs<ENTROPY>(a, row, token, score, r, keys);
 }
@@ -369,40 +391,33 @@ __device__ __forceinline__ void store_slots(const DistillArgs& a, const Coeffici
   }
 }
 
+__device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, float loss, float m, float log_s) {
+  if (threadIdx.x != 0) return;
+  if (a.loss) a.loss[row] = loss;
+  if (a.stats) {
+    a.stats[2 * row] = m;
+    a.stats[2 * row + 1] = log_s;
+  }
+}
+
 // The losses; with GRAD the gradient of their weighted sum too, for which the
 // row is read again, from the caches.
 template <class T, int NT, bool GRAD>
 __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
   __shared__ float s_red[kJoinLds<NT>];
   __shared__ SlotLds s;
-  const u32 slices = a.split.slices, slice = slices == 1 ? 0 : blockIdx.x % slices;
-  const int64_t row = a.row0 + (slices == 1 ? blockIdx.x : blockIdx.x / slices);
+  const int64_t row = a.row0 + blockIdx.x;
   const T* z = (const T*)a.z.p + row * a.z.ld;
   T* out = GRAD ? (T*)a.out + row * a.ld_out : nullptr;
-  if (slices == 1 && !load_slots<T, NT>(a, row, z, 0, a.z.V, s)) {
-    if (threadIdx.x == 0) {
-      a.loss[row] = 0.0f;
-      if (a.stats) a.stats[2 * row] = a.stats[2 * row + 1] = 0.0f;
-    }
+  if (!load_slots<T, NT>(a, row, z, 0, a.z.V, s)) {
+    write_loss(a, row, 0.0f, 0.0f, 0.0f);
     if constexpr (GRAD) zero_row<T, NT>(out, 0, a.z.V, a.streaming);
     return;
   }
-  const u32 c0 = slice * a.split.length, c1 = min(c0 + a.split.length, a.z.V);
-  const Share h = row_pass<T, NT, false, false>(z, c0, c1, a.z.c2);
+  const Share h = row_pass<T, NT, false, false>(z, 0, a.z.V, a.z.c2);
   const RowSums r = join_shares<NT>(h, a.z.c2, s_red);
-  if (slices > 1) {
-    if (threadIdx.x == 0) a.split.sums[(row - a.row0) * slices + slice] = SliceSums{r.m, r.s, 0.0f, 0.0f};
-    return;
-  }
   const float log_s = r.s == 0.0f ? 0.0f : logf(r.s);
-  const float loss = slots_loss<NT>(a, r, log_s, s);
-  if (threadIdx.x == 0) {
-    a.loss[row] = loss;
-    if (a.stats) {
-      a.stats[2 * row] = r.m;
-      a.stats[2 * row + 1] = log_s;
-    }
-  }
+  write_loss(a, row, slots_loss<NT>(a, r, log_s, s), r.m, log_s);
   if constexpr (GRAD) {
     if (r.s == 0.0f) {
       zero_row<T, NT>(out, 0, a.z.V, a.streaming);
@@ -414,27 +429,29 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
   }
 }
 
+// The losses of rows in slices: the last workgroup of a row joins their sums.
 template <class T>
-__global__ __launch_bounds__(kRowThreads) void k_distill_join(DistillArgs a) {
+__global__ __launch_bounds__(kRowThreads) void k_distill_split(DistillArgs a) {
   constexpr int NT = kRowThreads;
-  __shared__ float s_red[4];
+  __shared__ float s_red[kJoinLds<NT>];
   __shared__ SlotLds s;
-  const int64_t row = a.row0 + blockIdx.x;
+  __shared__ u32 s_last;
+  __shared__ float s_sums[3];
+  const u32 slices = a.split.slices, slice = blockIdx.x % slices;
+  const int64_t part = blockIdx.x / slices, row = a.row0 + part;
   const T* z = (const T*)a.z.p + row * a.z.ld;
-  float loss = 0.0f, m = 0.0f, log_s = 0.0f;
-  if (load_slots<T, NT>(a, row, z, 0, a.z.V, s)) {
-    const RowSums r = join_slices(a.split, blockIdx.x, a.z.c2, s_red);
-    m = r.m;
-    log_s = r.s == 0.0f ? 0.0f : logf(r.s);
-    loss = slots_loss<NT>(a, r, log_s, s);
+  const u32 c0 = slice * a.split.length, c1 = min(c0 + a.split.length, a.z.V);
+  const Share h = row_pass<T, NT, false, false>(z, c0, c1, a.z.c2);
+  const RowSums own = join_shares<NT>(h, a.z.c2, s_red);
+  if (threadIdx.x == 0) store_slice(a.split, part, slice, own);
+  if (!last_of_row(a.split, part, &s_last)) return;
+  if (!load_slots<T, NT>(a, row, z, 0, a.z.V, s)) {
+    write_loss(a, row, 0.0f, 0.0f, 0.0f);
+    return;
   }
-  if (threadIdx.x == 0) {
-    a.loss[row] = loss;
-    if (a.stats) {
-      a.stats[2 * row] = m;
-      a.stats[2 * row + 1] = log_s;
-    }
-  }
+  const RowSums r = join_slices(a.split, part, a.z.c2, s_sums);
+  const float log_s = r.s == 0.0f ? 0.0f : logf(r.s);
+  write_loss(a, row, slots_loss<NT>(a, r, log_s, s), r.m, log_s);
 }
 
 template <class T, int NT>
@@ -470,10 +487,14 @@ static RowPlan row_plan(int64_t T, int64_t V, u32 unit, int64_t groups, int64_t 
 }
 
 constexpr int64_t kShortRow = 512;  // up to here a row is one wave's
-constexpr int64_t kMostSlices = 64;  // that a wave joins
+
+constexpr int64_t kPassGroups = 2048;
+static_assert(kPassGroups / 2 <= (int64_t)(sizeof(HeaderHist::hist) / sizeof(u32)), "a counter for every row in slices");
 
 static u32 row_unit(tgs_dtype t) { return kRowThreads * (u32)(16 / dtype_bytes(t)); }
-static RowPlan pass_plan(int64_t T, int64_t V, tgs_dtype t) { return row_plan(T, V, row_unit(t), 2048, kMostSlices); }
+static RowPlan pass_plan(int64_t T, int64_t V, tgs_dtype t) {
+  return row_plan(T, V, row_unit(t), kPassGroups, kMostSlices);
+}
 static RowPlan grad_plan_of(int64_t T, int64_t V, tgs_dtype t) { return row_plan(T, V, row_unit(t), 4096, INT32_MAX); }
 
 static size_t sums_bytes(int64_t T, const RowPlan& p) {
@@ -583,7 +604,7 @@ extern "C" tgs_status tgs_token_logprobs(const void* logits, tgs_dtype dtype, in
   char* scratch = (char*)workspace + kWorkspaceHeader;
   LogprobsArgs a{};
   a.z = logits_of(logits, ld, V, temperature);
-  a.split = Split{p.slices, p.length, (SliceSums*)scratch, (u64*)(scratch + sums_bytes(T, p))};
+  a.split = Split{p.slices, p.length, (SliceSums*)scratch, (u64*)(scratch + sums_bytes(T, p)), header_hist(workspace)->hist};
   a.tokens = tokens;
   a.logprobs = logprobs;
   a.stats = stats;
@@ -603,10 +624,9 @@ extern "C" tgs_status tgs_token_logprobs(const void* logits, tgs_dtype dtype, in
         over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
           a.row0 = row0;
           const dim3 grid((u32)(rows * p.slices));
-          if (V <= kShortRow) hipLaunchKernelGGL((k_logprobs<Z, kWave, ENT, TOP>), grid, dim3(kWave), 0, stream, a);
-          else hipLaunchKernelGGL((k_logprobs<Z, kRowThreads, ENT, TOP>), grid, dim3(kRowThreads), 0, stream, a);
-          if (p.slices > 1)
-            hipLaunchKernelGGL((k_logprobs_join<Z, ENT, TOP>), dim3((u32)rows), dim3(kRowThreads), 0, stream, a);
+          if (V <= kShortRow) hipLaunchKernelGGL((k_logprobs<Z, kWave, ENT, TOP, false>), grid, dim3(kWave), 0, stream, a);
+          else if (p.slices == 1) hipLaunchKernelGGL((k_logprobs<Z, kRowThreads, ENT, TOP, false>), grid, dim3(kRowThreads), 0, stream, a);
+          else hipLaunchKernelGGL((k_logprobs<Z, kRowThreads, ENT, TOP, true>), grid, dim3(kRowThreads), 0, stream, a);
         });
       });
     });
@@ -723,20 +743,23 @@ static tgs_status distillation(const char* what, const void* logits, tgs_dtype d
     using Z = std::remove_pointer_t<decltype(z)>;
     const int threads = V <= kShortRow ? kWave : kRowThreads;
     if (has_loss) {
-      a.split = Split{p.slices, p.length, (SliceSums*)scratch, nullptr};
+      a.split = Split{p.slices, p.length, (SliceSums*)scratch, nullptr, header_hist(workspace)->hist};
       over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
         a.row0 = row0;
         const dim3 grid((u32)(rows * p.slices));
-        with_flag(both && !split, [&](auto grad) {
+        if (split) {
+          hipLaunchKernelGGL((k_distill_split<Z>), grid, dim3(kRowThreads), 0, stream, a);
+          return;
+        }
+        with_flag(both, [&](auto grad) {
           constexpr bool GRAD = decltype(grad)::value;
           if (V <= kShortRow) hipLaunchKernelGGL((k_distill<Z, kWave, GRAD>), grid, dim3(kWave), 0, stream, a);
           else hipLaunchKernelGGL((k_distill<Z, kRowThreads, GRAD>), grid, dim3(kRowThreads), 0, stream, a);
         });
-        if (split) hipLaunchKernelGGL((k_distill_join<Z>), dim3((u32)rows), dim3(kRowThreads), 0, stream, a);
       });
       if (!both || !split) return;
     }
-    a.split = Split{g.slices, g.length, nullptr, nullptr};
+    a.split = Split{g.slices, g.length, nullptr, nullptr, nullptr};
     over_rows(T, g.slices, threads, [&](int64_t row0, int64_t rows) {
       a.row0 = row0;
       const dim3 grid((u32)(rows * g.slices));

@@ -150,41 +150,43 @@ struct TopLds {
   u64 keys[NT];
   u64 list[kList];
   u64 out[kMostTop];
-  u64 least;
+  u32 larger[NT];
   u32 owner[NT];
   u32 owners, listed;
 };
 
 // The k <= 64 largest keys of what the threads hold, descending, to s.out (0
 // where there are fewer).  `bound` is a key no larger than the thread's largest
-// one (0: it holds none); every thread holds `count` items of E keys at most:
-// keys_of(owner, j, f) calls f(key) for item j of thread `owner`.
+// one (0: it holds none); every thread holds `count` items at most:
+// keys_of(owner, j, f) calls f(key) for each key of item j of thread `owner`.
 //
 // The k-th largest of 64 groups' bounds is no larger than the k-th largest key.
-// The few threads whose own bound reaches it hold all that do; their items are
-// looked at by the whole workgroup, and the few keys found are ranked by counting.  Where
-// they are too many (an order made for it) or `all` is set (bounds that NaNs
-// passed by), k rounds over everything find the largest below the last.
+// The few threads whose own bound reaches it hold all keys that do; their items
+// are looked at by the whole workgroup, and the few keys found are ranked by
+// counting.  Where they are too many (an order made for it) or `all` is set
+// (bounds that NaNs passed by), k rounds over everything find the largest below
+// the last.
 template <int NT, class F>
 __device__ __forceinline__ void largest_keys(TopLds<NT>& s, u64 bound, u32 count, u32 k, bool all, F&& keys_of) {
-  const u32 t = threadIdx.x;
+  constexpr int W = NT / kWave;
+  const u32 t = threadIdx.x, lane = t % kWave, wave = t / kWave;
   s.keys[t] = bound;
   if (t < kMostTop) s.out[t] = 0;
   if (t == 0) s.owners = s.listed = 0;
   __syncthreads();
-  if (t < kWave) {
-    u64 g = s.keys[t];
+  // group g: lane g of every wave; a group without a key gets one of its own below all others
+  u64 g = kWave - 1 - lane;
 #pragma unroll
-    for (int i = kWave; i < NT; i += kWave) g = max(g, s.keys[t + i]);
-    u32 larger = 0;
-    for (int i = 0; i < kWave; ++i) {
-      const u64 o = readlane64(g, i);
-      larger += o > g || (o == g && i < (int)t);
-    }
-    if (larger == k - 1) s.least = g;
-  }
+  for (int i = 0; i < NT; i += kWave) g = max(g, s.keys[lane + i]);
+  u32 larger = 0;
+#pragma unroll
+  for (int i = 0; i < kWave / W; ++i) larger += readlane64(g, wave * (kWave / W) + i) > g;
+  s.larger[t] = larger;
   __syncthreads();
-  const u64 least = s.least;
+  larger = 0;
+#pragma unroll
+  for (int i = 0; i < NT; i += kWave) larger += s.larger[lane + i];
+  const u64 least = readlane64(g, __builtin_ctzll(ballot(larger == k - 1)));
   if (!all) {
     if (bound >= least && bound != 0) s.owner[atomicAdd(&s.owners, 1u)] = t;
     __syncthreads();
@@ -203,9 +205,10 @@ __device__ __forceinline__ void largest_keys(TopLds<NT>& s, u64 bound, u32 count
   if (!all && n <= TopLds<NT>::kList) {
     for (u32 i = t; i < n; i += NT) {
       const u64 mine = s.list[i];
-      u32 larger = 0;
-      for (u32 o = 0; o < n; ++o) larger += s.list[o] > mine;
-      if (larger < k) s.out[larger] = mine;
+      u32 rank = 0;
+#pragma unroll 8
+      for (u32 o = 0; o < n; ++o) rank += s.list[o] > mine;
+      if (rank < k) s.out[rank] = mine;
     }
   } else {
     u64 last = ~(u64)0;
