@@ -125,7 +125,10 @@ __device__ __forceinline__ void write_logprobs(const LogprobsArgs& a, int64_t ro
     a.logprobs[row] = real ? log_probability(a.z, score, r, log_s) : 0.0f;
     a.stats[2 * row] = real ? r.m : 0.0f;
     a.stats[2 * row + 1] = real ? log_s : 0.0f;
-    if constexpr (ENTROPY) a.entropy[row] = real && r.s != 0.0f ? log_s - r.w / r.s * kLn2 : 0.0f;
+    if constexpr (ENTROPY) {
+      const float h = log_s - r.w / r.s * kLn2;  // roundings may leave less than nothing
+      a.entropy[row] = !real || r.s == 0.0f || h < 0.0f ? 0.0f : h;
+    }
   }
   for (u32 i = threadIdx.x; i < a.top; i += blockDim.x) {
     const u64 key = real ? keys[i] : 0;
@@ -149,19 +152,28 @@ __global__ __launch_bounds__(NT) void k_logprobs(LogprobsArgs a) {
   const T* z = (const T*)a.z.p + row * a.z.ld;
   const float score = to_f32(z[token]);
   const u32 c0 = SPLIT ? slice * a.split.length : 0, c1 = SPLIT ? min(c0 + a.split.length, a.z.V) : a.z.V;
-  const Share h = row_pass<T, NT, ENTROPY, TOP>(z, c0, c1, a.z.c2);
+  const Span span{c0, c1};
+  float* parts = nullptr;
+  if constexpr (TOP) parts = s_top.parts;
+  const Share h = row_pass<T, NT, ENTROPY, TOP>(z, span, a.z.c2, parts);
   RowSums r = join_shares<NT>(h, a.z.c2, s_red);
   const u64* keys = nullptr;
   if constexpr (TOP) {
     const u32 first = c0 + threadIdx.x * E, at = first + h.at * (NT * E);
     const u64 bound = first < c1 ? entry_key(h.top, min(at + E, c1) - 1) : 0;
-    largest_keys<NT>(s_top, bound, (c1 - c0 + NT * E - 1) / (NT * E), a.top, r.s != r.s, [&](u32 owner, u32 j, auto&& f) {
+    const u32 count = (c1 - c0 + NT * E - 1) / (NT * E), each = span.part<NT * E>();
+    largest_keys<NT, true>(s_top, bound, count, each, a.top, r.s != r.s, [&](u32 owner, u32 j, auto&& f) {
       const u32 c = c0 + (owner + j * NT) * E;
       if (c >= c1) return;
-      const Vec<T, E> v = load_part<T, E>(z, c, c1, lowest_fill<T>());
+      if (c1 - c0 < (u32)E) {
+        for (u32 i = c; i < c1; ++i) f(entry_key(to_f32(z[i]), i));
+        return;
+      }
+      const u32 from = min(c, c1 - E);
+      const Vec<T, E> v = load_vec<T, E>(z + from);
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (c + e < c1) f(entry_key(to_f32(v.v[e]), c + e));
+        if (from + e >= c) f(entry_key(to_f32(v.v[e]), from + e));
     });
     keys = s_top.out;
   }
@@ -185,7 +197,8 @@ __global__ __launch_bounds__(NT) void k_logprobs(LogprobsArgs a) {
       }
 #pragma unroll
       for (u64 key : held) bound = max(bound, key);
-      largest_keys<NT>(s_top, bound, (n + NT - 1) / NT, a.top, false, [&](u32 owner, u32 j, auto&& f) {
+      const u32 count = (n + NT - 1) / NT;
+      largest_keys<NT, false>(s_top, bound, count, count, a.top, false, [&](u32 owner, u32 j, auto&& f) {
         const u32 i = owner + j * NT;
         const u64 key = i < n ? ld_agent64(all + i) : 0;
         if (key != 0) f(key);
@@ -227,25 +240,43 @@ __device__ __forceinline__ float slope(const Logits& z, const Coefficients& k, f
   return p * fmaf(-k.a, lp + k.h, k.b);
 }
 
-template <class T, int NT, class F>
-__device__ __forceinline__ void map_row(const T* z, T* out, u32 c0, u32 c1, bool streaming, F&& f) {
-  constexpr int E = kLogitsVector<T>, U = 4;
+// out = f(z) for columns [c0, c1), a vector's results passed through patch(y,
+// its first column) on their way; out may be z.  From the end to the start: a
+// pass over the row that came before left its end in the caches.
+template <class T, int NT, class F, class P>
+__device__ __forceinline__ void map_row(const T* z, T* out, u32 c0, u32 c1, bool streaming, F&& f, P&& patch) {
+  constexpr int E = kLogitsVector<T>, U = kUnroll;
   constexpr u32 kStep = NT * E;
-  for (u32 base = c0; base < c1; base += U * kStep) {
-    const u32 c = base + threadIdx.x * E;
-    Vec<T, E> v[U];
+  const auto one = [&](const Vec<T, E>& v, u32 at) {
+    float y[E];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c + u * kStep < c1) v[u] = load_part<T, E>(z, c + u * kStep, c1, lowest_fill<T>());
+    for (int e = 0; e < E; ++e) y[e] = f(to_f32(v.v[e]));
+    patch(y, at);
+    const Vec<T, E> r = round_vec<T, E>(y);
+    if (streaming) store_vec_streaming<T, E>(out + at, r);
+    else store_vec<T, E>(out + at, r);
+  };
+  // the elements behind the last whole vector, a thread each
+  const u32 left = (c1 - c0) % E, at = c1 - left + threadIdx.x;
+  if (threadIdx.x < left) {
+    float y[1] = {f(to_f32(z[at]))};
+    patch(y, at);
+    out[at] = round_vec<T, 1>(y).v[0];
+  }
+  u32 rounds = (c1 - c0) / (U * kStep), c = c0 + rounds * (U * kStep) + threadIdx.x * E;
+  Vec<T, E> v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const u32 at = c + u * kStep;
-      if (at >= c1) continue;
-      float y[E];
+  for (int u = 0; u < U; ++u)
+    if (c + u * kStep + E <= c1) v[u] = load_vec<T, E>(z + c + u * kStep);
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = f(to_f32(v[u].v[e]), at + e);
-      store_part<T, E>(out, at, c1, round_vec<T, E>(y), streaming);
-    }
+  for (int u = 0; u < U; ++u)
+    if (c + u * kStep + E <= c1) one(v[u], c + u * kStep);
+  for (; rounds > 0; --rounds) {
+    c -= U * kStep;
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = load_vec<T, E>(z + c + u * kStep);
+#pragma unroll
+    for (int u = 0; u < U; ++u) one(v[u], c + u * kStep);
   }
 }
 
@@ -253,7 +284,12 @@ template <class T, int NT>
 __device__ __forceinline__ void zero_row(T* out, u32 c0, u32 c1, bool streaming) {
   constexpr int E = kLogitsVector<T>;
   const float zero[E] = {};
-  for (u32 c = c0 + threadIdx.x * E; c < c1; c += NT * E) store_part<T, E>(out, c, c1, round_vec<T, E>(zero), streaming);
+  u32 c = c0 + threadIdx.x * E;
+  for (; c + E <= c1; c += NT * E) {
+    if (streaming) store_vec_streaming<T, E>(out + c, round_vec<T, E>(zero));
+    else store_vec<T, E>(out + c, round_vec<T, E>(zero));
+  }
+  for (; c < c1; ++c) out[c] = from_f32<T>(0.0f);
 }
 
 template <class T, int NT, bool ENTROPY>
@@ -275,10 +311,14 @@ __global__ __launch_bounds__(NT) void k_logprobs_grad(LogprobsGradArgs a) {
   k.b = -g;
   k.a = ENTROPY ? a.grad_entropy[row] * a.z.inv : 0.0f;
   k.h = ENTROPY ? a.entropy[row] : 0.0f;
-  map_row<T, NT>((const T*)a.z.p + row * a.z.ld, out, c0, c1, a.streaming, [&](float x, u32 c) {
-    const float y = slope<ENTROPY>(a.z, k, x);
-    return c == (u32)token ? y + g : y;
-  });
+  map_row<T, NT>(
+      (const T*)a.z.p + row * a.z.ld, out, c0, c1, a.streaming, [&](float x) { return slope<ENTROPY>(a.z, k, x); },
+      [&](auto& y, u32 at) {
+        constexpr u32 N = sizeof(y) / sizeof(y[0]);
+        if ((u32)token - at >= N) return;
+#pragma unroll
+        for (u32 e = 0; e < N; ++e) y[e] += at + e == (u32)token ? g : 0.0f;
+      });
 }
 
 // ---------------------------------------------------------- distillation --
@@ -301,19 +341,53 @@ struct DistillArgs {
 
 constexpr int kMostSlots = 1024;
 
-struct SlotLds {
-  float q[kMostSlots];
-  float lq[kMostSlots];
-  float x[kMostSlots];  // the row's score there
-  int index[kMostSlots];
-  float red[5][16];
-};
+constexpr u32 kHeads = 1024;  // lists of slots, by the vector that an index falls into
+constexpr u32 kNoSlot = ~0u;
 
-// The slots' probabilities q, and the scores of those in [c0, c1) (others may be
-// overwritten already); false where no slot has any.  Ends with a barrier.
-template <class T, int NT>
-__device__ __forceinline__ bool load_slots(const DistillArgs& a, int64_t row, const T* z, u32 c0, u32 c1, SlotLds& s) {
+// The slots of a row in LDS, K of each.
+struct Slots {
+  float* q;    // probability
+  int* index;  // -1: empty
+  float* lq;   // for the loss: its log
+  float* x;    // for the loss: the row's score there
+  float* sum;  // for the gradient: q of all slots with this index, in the first of them
+  u32* next;   // for the gradient: the next slot of a list
+  u32* head;
+  float (*red)[16];
+};
+template <bool LOSS, bool GRAD>
+constexpr size_t slots_bytes(u32 K) {
+  return (size_t)K * 4 * (2 + (LOSS ? 2 : 0) + (GRAD ? 2 : 0)) + (GRAD ? kHeads * 4 : 0);
+}
+template <bool LOSS, bool GRAD>
+__device__ __forceinline__ Slots slots_in(float* lds, u32 K, float (*red)[16]) {
+  Slots s{};
+  s.q = lds;
+  s.index = (int*)(lds + K);
+  lds += 2 * K;
+  if constexpr (LOSS) {
+    s.lq = lds;
+    s.x = lds + K;
+    lds += 2 * K;
+  }
+  if constexpr (GRAD) {
+    s.sum = lds;
+    s.next = (u32*)(lds + K);
+    s.head = (u32*)(lds + 2 * K);
+  }
+  s.red = red;
+  return s;
+}
+
+// Reads a row's slots; for the gradient lists those in [c0, c1).  False where no
+// slot has any probability.  Ends with a barrier.
+template <class T, int NT, bool LOSS, bool GRAD>
+__device__ __forceinline__ bool load_slots(const DistillArgs& a, int64_t row, const T* z, u32 c0, u32 c1, const Slots& s) {
+  constexpr int E = kLogitsVector<T>;
   float top[1] = {-kInf}, any[1] = {-kInf};
+  if constexpr (GRAD) {
+    for (u32 i = threadIdx.x; i < kHeads; i += NT) s.head[i] = kNoSlot;
+  }
   for (u32 i = threadIdx.x; i < a.K; i += NT) {
     const int64_t at = row * a.K + i;
     const int index = load_entry(a.indices, a.wide, at, a.z.V, a.err);
@@ -321,36 +395,61 @@ __device__ __forceinline__ bool load_slots(const DistillArgs& a, int64_t row, co
     if (index >= 0) {
       t = a.teacher_dtype == TGS_FP32 ? ((const float*)a.teacher)[at]
           : a.teacher_dtype == TGS_BF16 ? to_f32(((const bf16_t*)a.teacher)[at]) : to_f32(((const fp16_t*)a.teacher)[at]);
-      s.x[i] = (u32)index >= c0 && (u32)index < c1 ? to_f32(z[index]) : 0.0f;
+      if constexpr (LOSS) s.x[i] = to_f32(z[index]);
     }
     s.index[i] = index;
-    s.lq[i] = t;
+    s.q[i] = t;
     top[0] = fmaxf(top[0], t);
     if (t != -kInf) any[0] = 1.0f;
   }
   group_reduce<Max, NT>(top, s.red[0]);
   group_reduce<Max, NT>(any, s.red[1]);
   if (any[0] < 0.0f) return false;
+  if constexpr (GRAD && NT == kWave) __syncthreads();
   float sum[1] = {0.0f};
   for (u32 i = threadIdx.x; i < a.K; i += NT) {
-    const float d = (s.lq[i] - top[0]) * a.z.inv, e = s.index[i] >= 0 ? __builtin_amdgcn_exp2f(d * kLog2e) : 0.0f;
+    const int index = s.index[i];
+    const float d = (s.q[i] - top[0]) * a.z.inv, e = index >= 0 ? __builtin_amdgcn_exp2f(d * kLog2e) : 0.0f;
     s.q[i] = e;
-    s.lq[i] = d;
+    if constexpr (LOSS) s.lq[i] = d;
+    if constexpr (GRAD) {
+      if (index >= 0 && (u32)index >= c0 && (u32)index < c1)
+        s.next[i] = atomicExch(&s.head[((u32)index - c0) / E % kHeads], i);
+    }
     sum[0] += e;
   }
   group_reduce<Sum, NT>(sum, s.red[2]);
   const float scale = 1.0f / sum[0], log_sum = logf(sum[0]);
   for (u32 i = threadIdx.x; i < a.K; i += NT) {
     s.q[i] *= scale;
-    s.lq[i] -= log_sum;
+    if constexpr (LOSS) s.lq[i] -= log_sum;
   }
   __syncthreads();
+  if constexpr (GRAD) {
+    // an index may stand in several slots: their q are added in the slots' order
+    for (u32 i = threadIdx.x; i < a.K; i += NT) {
+      const int index = s.index[i];
+      if (index < 0 || (u32)index < c0 || (u32)index >= c1) continue;
+      bool first = true, others = false;
+      for (u32 o = s.head[((u32)index - c0) / E % kHeads]; o != kNoSlot; o = s.next[o]) {
+        if (o == i || s.index[o] != index) continue;
+        others = true;
+        first = first && i < o;
+      }
+      float q = first ? s.q[i] : 0.0f;
+      if (others && first)
+        for (u32 o = i + 1; o < a.K; ++o)
+          if (s.index[o] == index) q += s.q[o];
+      s.sum[i] = q;
+    }
+    __syncthreads();
+  }
   return true;
 }
 
 // The row's loss, in every thread's hands.
 template <int NT>
-__device__ __forceinline__ float slots_loss(const DistillArgs& a, const RowSums& r, float log_s, SlotLds& s) {
+__device__ __forceinline__ float slots_loss(const DistillArgs& a, const RowSums& r, float log_s, const Slots& s) {
   float sum[1] = {0.0f};
   for (u32 i = threadIdx.x; i < a.K; i += NT) {
     const float q = s.q[i];
@@ -362,33 +461,27 @@ __device__ __forceinline__ float slots_loss(const DistillArgs& a, const RowSums&
 
 // A teacher's NaN, which every q then is, goes to the whole row's gradient.
 __device__ __forceinline__ Coefficients distill_coefficients(const DistillArgs& a, int64_t row, float m, float log_s,
-                                                             const SlotLds& s) {
+                                                             const Slots& s) {
   const float g = a.given ? a.given[row] : 1.0f;
   return Coefficients{m, log_s, log_s * kLog2e, 0.0f, fmaf(0.0f, s.q[0], g * a.z.inv), 0.0f};
 }
 
-// The gradient at the slots' entries inside [c0, c1), over what map_row stored
-// there: those stores have completed, and another store to the same address lands later.
+// out = (p - q) b for columns [c0, c1) of a row.
 template <class T, int NT>
-__device__ __forceinline__ void store_slots(const DistillArgs& a, const Coefficients& k, T* out, u32 c0, u32 c1,
-                                            const SlotLds& s) {
-  wait_all_memory();
-  __syncthreads();
-  for (u32 i = threadIdx.x; i < a.K; i += NT) {
-    const int index = s.index[i];
-    if (index < 0 || (u32)index < c0 || (u32)index >= c1) continue;
-    float q = 0.0f;
-    bool first = true;
-    for (u32 j = 0; j < a.K; ++j) {  // an index may stand in several slots
-      if (s.index[j] != index) continue;
-      first = first && j >= i;
-      q += s.q[j];
-    }
-    if (first) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(s.x[i] - k.m, a.z.c2, -k.l2));
-      out[index] = from_f32<T>((p - q) * k.b);
-    }
-  }
+__device__ __forceinline__ void write_distill_grad(const DistillArgs& a, const T* z, T* out, u32 c0, u32 c1,
+                                                   const Coefficients& k, const Slots& s) {
+  constexpr int E = kLogitsVector<T>;
+  map_row<T, NT>(
+      z, out, c0, c1, a.streaming, [&](float x) { return slope<false>(a.z, k, x); },
+      [&](auto& y, u32 at) {
+        constexpr u32 N = sizeof(y) / sizeof(y[0]);
+        for (u32 o = s.head[(at - c0) / E % kHeads]; o != kNoSlot; o = s.next[o]) {
+          const u32 place = (u32)s.index[o] - at;
+          const float q = s.sum[o] * k.b;
+#pragma unroll
+          for (u32 e = 0; e < N; ++e) y[e] -= e == place ? q : 0.0f;
+        }
+      });
 }
 
 __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, float loss, float m, float log_s) {
@@ -404,28 +497,24 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, fl
 // row is read again, from the caches.
 template <class T, int NT, bool GRAD>
 __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
-  __shared__ float s_red[kJoinLds<NT>];
-  __shared__ SlotLds s;
+  extern __shared__ float s_slots[];
+  __shared__ float s_red[kJoinLds<NT>], s_more[4][16];
+  const Slots s = slots_in<true, GRAD>(s_slots, a.K, s_more);
   const int64_t row = a.row0 + blockIdx.x;
   const T* z = (const T*)a.z.p + row * a.z.ld;
   T* out = GRAD ? (T*)a.out + row * a.ld_out : nullptr;
-  if (!load_slots<T, NT>(a, row, z, 0, a.z.V, s)) {
+  if (!load_slots<T, NT, true, GRAD>(a, row, z, 0, a.z.V, s)) {
     write_loss(a, row, 0.0f, 0.0f, 0.0f);
     if constexpr (GRAD) zero_row<T, NT>(out, 0, a.z.V, a.streaming);
     return;
   }
-  const Share h = row_pass<T, NT, false, false>(z, 0, a.z.V, a.z.c2);
+  const Share h = row_pass<T, NT, false, false>(z, Span{0, a.z.V}, a.z.c2, nullptr);
   const RowSums r = join_shares<NT>(h, a.z.c2, s_red);
   const float log_s = r.s == 0.0f ? 0.0f : logf(r.s);
   write_loss(a, row, slots_loss<NT>(a, r, log_s, s), r.m, log_s);
   if constexpr (GRAD) {
-    if (r.s == 0.0f) {
-      zero_row<T, NT>(out, 0, a.z.V, a.streaming);
-      return;
-    }
-    const Coefficients k = distill_coefficients(a, row, r.m, log_s, s);
-    map_row<T, NT>(z, out, 0, a.z.V, a.streaming, [&](float x, u32) { return slope<false>(a.z, k, x); });
-    store_slots<T, NT>(a, k, out, 0, a.z.V, s);
+    if (r.s == 0.0f) zero_row<T, NT>(out, 0, a.z.V, a.streaming);
+    else write_distill_grad<T, NT>(a, z, out, 0, a.z.V, distill_coefficients(a, row, r.m, log_s, s), s);
   }
 }
 
@@ -433,19 +522,20 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void k_distill_split(DistillArgs a) {
   constexpr int NT = kRowThreads;
-  __shared__ float s_red[kJoinLds<NT>];
-  __shared__ SlotLds s;
+  extern __shared__ float s_slots[];
+  __shared__ float s_red[kJoinLds<NT>], s_more[4][16];
   __shared__ u32 s_last;
   __shared__ float s_sums[3];
+  const Slots s = slots_in<true, false>(s_slots, a.K, s_more);
   const u32 slices = a.split.slices, slice = blockIdx.x % slices;
   const int64_t part = blockIdx.x / slices, row = a.row0 + part;
   const T* z = (const T*)a.z.p + row * a.z.ld;
   const u32 c0 = slice * a.split.length, c1 = min(c0 + a.split.length, a.z.V);
-  const Share h = row_pass<T, NT, false, false>(z, c0, c1, a.z.c2);
+  const Share h = row_pass<T, NT, false, false>(z, Span{c0, c1}, a.z.c2, nullptr);
   const RowSums own = join_shares<NT>(h, a.z.c2, s_red);
   if (threadIdx.x == 0) store_slice(a.split, part, slice, own);
   if (!last_of_row(a.split, part, &s_last)) return;
-  if (!load_slots<T, NT>(a, row, z, 0, a.z.V, s)) {
+  if (!load_slots<T, NT, true, false>(a, row, z, 0, a.z.V, s)) {
     write_loss(a, row, 0.0f, 0.0f, 0.0f);
     return;
   }
@@ -456,20 +546,17 @@ __global__ __launch_bounds__(kRowThreads) void k_distill_split(DistillArgs a) {
 
 template <class T, int NT>
 __global__ __launch_bounds__(NT) void k_distill_grad(DistillArgs a) {
-  __shared__ SlotLds s;
+  extern __shared__ float s_slots[];
+  __shared__ float s_more[4][16];
+  const Slots s = slots_in<false, true>(s_slots, a.K, s_more);
   const u32 slices = a.split.slices, slice = slices == 1 ? 0 : blockIdx.x % slices;
   const int64_t row = a.row0 + (slices == 1 ? blockIdx.x : blockIdx.x / slices);
   const u32 c0 = slice * a.split.length, c1 = min(c0 + a.split.length, a.z.V);
   T* out = (T*)a.out + row * a.ld_out;
   const T* z = (const T*)a.z.p + row * a.z.ld;
   const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
-  if (!load_slots<T, NT>(a, row, z, c0, c1, s) || m == -kInf) {
-    zero_row<T, NT>(out, c0, c1, a.streaming);
-    return;
-  }
-  const Coefficients k = distill_coefficients(a, row, m, log_s, s);
-  map_row<T, NT>(z, out, c0, c1, a.streaming, [&](float x, u32) { return slope<false>(a.z, k, x); });
-  store_slots<T, NT>(a, k, out, c0, c1, s);
+  if (!load_slots<T, NT, false, true>(a, row, z, c0, c1, s) || m == -kInf) zero_row<T, NT>(out, c0, c1, a.streaming);
+  else write_distill_grad<T, NT>(a, z, out, c0, c1, distill_coefficients(a, row, m, log_s, s), s);
 }
 
 // ------------------------------------------------------------------ host --
@@ -486,7 +573,19 @@ static RowPlan row_plan(int64_t T, int64_t V, u32 unit, int64_t groups, int64_t 
   return RowPlan{(u32)((V + length - 1) / length), (u32)std::min<int64_t>(length, (int64_t)1 << 31)};
 }
 
-constexpr int64_t kShortRow = 512;  // up to here a row is one wave's
+// Rows of up to 320 vectors of 16 bytes are one wave's.  16,384 rows by a wave and
+// by a workgroup of four, in bf16: 1,500 log probabilities with 5 alternatives 33 and
+// 52 us, their gradient 24 and 32; 2,500 36 and 58, 34 and 39; 4,000 48 and 63, but
+// 54 and 49.  In fp32 1,500 scores take 19 and 23 us, 2,500 29 and 28.
+static bool short_row(int64_t V, tgs_dtype t) { return V * (int64_t)dtype_bytes(t) <= 320 * 16; }
+// The call that reads a row twice keeps fewer rows in flight where they are long, so
+// that the second reading finds them in the caches.  With 256, 512 and 1,024 threads
+// 8,192 rows of 32,000 in bf16 take 267, 243 and 281 us, 4,096 of 128,000 606, 561
+// and 491, 2,048 of 64,000 in fp32 301, 280 and 258.
+static int step_threads(int64_t V, tgs_dtype t) {
+  const int64_t bytes = V * (int64_t)dtype_bytes(t);
+  return short_row(V, t) ? kWave : bytes < 32 << 10 ? kRowThreads : bytes < 128 << 10 ? 512 : 1024;
+}
 
 constexpr int64_t kPassGroups = 2048;
 static_assert(kPassGroups / 2 <= (int64_t)(sizeof(HeaderHist::hist) / sizeof(u32)), "a counter for every row in slices");
@@ -620,11 +719,12 @@ extern "C" tgs_status tgs_token_logprobs(const void* logits, tgs_dtype dtype, in
     with_flag(entropy != nullptr, [&](auto ent) {
       with_flag(top > 0, [&](auto tops) {
         constexpr bool ENT = decltype(ent)::value, TOP = decltype(tops)::value;
-        const int threads = V <= kShortRow ? kWave : kRowThreads;
+        const bool wave = short_row(V, dtype);
+    const int threads = wave ? kWave : kRowThreads;
         over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
           a.row0 = row0;
           const dim3 grid((u32)(rows * p.slices));
-          if (V <= kShortRow) hipLaunchKernelGGL((k_logprobs<Z, kWave, ENT, TOP, false>), grid, dim3(kWave), 0, stream, a);
+          if (wave) hipLaunchKernelGGL((k_logprobs<Z, kWave, ENT, TOP, false>), grid, dim3(kWave), 0, stream, a);
           else if (p.slices == 1) hipLaunchKernelGGL((k_logprobs<Z, kRowThreads, ENT, TOP, false>), grid, dim3(kRowThreads), 0, stream, a);
           else hipLaunchKernelGGL((k_logprobs<Z, kRowThreads, ENT, TOP, true>), grid, dim3(kRowThreads), 0, stream, a);
         });
@@ -678,11 +778,12 @@ extern "C" tgs_status tgs_token_logprobs_grad(const void* logits, tgs_dtype dtyp
     using Z = std::remove_pointer_t<decltype(z)>;
     with_flag(grad_entropy != nullptr, [&](auto ent) {
       constexpr bool ENT = decltype(ent)::value;
-      const int threads = V <= kShortRow ? kWave : kRowThreads;
+      const bool wave = short_row(V, dtype);
+    const int threads = wave ? kWave : kRowThreads;
       over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
         a.row0 = row0;
         const dim3 grid((u32)(rows * p.slices));
-        if (V <= kShortRow) hipLaunchKernelGGL((k_logprobs_grad<Z, kWave, ENT>), grid, dim3(kWave), 0, stream, a);
+        if (wave) hipLaunchKernelGGL((k_logprobs_grad<Z, kWave, ENT>), grid, dim3(kWave), 0, stream, a);
         else hipLaunchKernelGGL((k_logprobs_grad<Z, kRowThreads, ENT>), grid, dim3(kRowThreads), 0, stream, a);
       });
     });
@@ -736,25 +837,38 @@ static tgs_status distillation(const char* what, const void* logits, tgs_dtype d
   a.teacher_dtype = teacher_dtype;
   a.wide = indices_dtype == TGS_INT64;
   a.streaming = (size_t)T * V * dtype_bytes(dtype) > kRowsStreamingBytes;
+  const size_t loss_lds = slots_bytes<true, false>(a.K), grad_lds = slots_bytes<false, true>(a.K),
+               both_lds = slots_bytes<true, true>(a.K);
   const bool both = has_loss && has_grad, split = p.slices > 1;
   // split rows' gradients wait for the join
   if (both && split) a.stats = (float*)(scratch + sums_bytes(T, p));
   with_float_dtype(dtype, [&](auto* z) {
     using Z = std::remove_pointer_t<decltype(z)>;
-    const int threads = V <= kShortRow ? kWave : kRowThreads;
+    const bool wave = short_row(V, dtype);
+    const int threads = wave ? kWave : kRowThreads;
     if (has_loss) {
       a.split = Split{p.slices, p.length, (SliceSums*)scratch, nullptr, header_hist(workspace)->hist};
-      over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
+      over_rows(T, p.slices, both ? 1024 : threads, [&](int64_t row0, int64_t rows) {
         a.row0 = row0;
         const dim3 grid((u32)(rows * p.slices));
         if (split) {
-          hipLaunchKernelGGL((k_distill_split<Z>), grid, dim3(kRowThreads), 0, stream, a);
+          hipLaunchKernelGGL((k_distill_split<Z>), grid, dim3(kRowThreads), loss_lds, stream, a);
           return;
         }
         with_flag(both, [&](auto grad) {
           constexpr bool GRAD = decltype(grad)::value;
-          if (V <= kShortRow) hipLaunchKernelGGL((k_distill<Z, kWave, GRAD>), grid, dim3(kWave), 0, stream, a);
-          else hipLaunchKernelGGL((k_distill<Z, kRowThreads, GRAD>), grid, dim3(kRowThreads), 0, stream, a);
+          const size_t bytes = GRAD ? both_lds : loss_lds;
+          const auto launch = [&](auto nt) {
+            constexpr int NT = decltype(nt)::value;
+            hipLaunchKernelGGL((k_distill<Z, NT, GRAD>), grid, dim3(NT), bytes, stream, a);
+          };
+          const int nt = GRAD ? step_threads(V, dtype) : threads;
+          if (nt == kWave) launch(std::integral_constant<int, kWave>{});
+          else if (nt == kRowThreads) launch(std::integral_constant<int, kRowThreads>{});
+          else if constexpr (GRAD) {
+            if (nt == 512) launch(std::integral_constant<int, 512>{});
+            else launch(std::integral_constant<int, 1024>{});
+          }
         });
       });
       if (!both || !split) return;
@@ -763,8 +877,8 @@ static tgs_status distillation(const char* what, const void* logits, tgs_dtype d
     over_rows(T, g.slices, threads, [&](int64_t row0, int64_t rows) {
       a.row0 = row0;
       const dim3 grid((u32)(rows * g.slices));
-      if (V <= kShortRow) hipLaunchKernelGGL((k_distill_grad<Z, kWave>), grid, dim3(kWave), 0, stream, a);
-      else hipLaunchKernelGGL((k_distill_grad<Z, kRowThreads>), grid, dim3(kRowThreads), 0, stream, a);
+      if (wave) hipLaunchKernelGGL((k_distill_grad<Z, kWave>), grid, dim3(kWave), grad_lds, stream, a);
+      else hipLaunchKernelGGL((k_distill_grad<Z, kRowThreads>), grid, dim3(kRowThreads), grad_lds, stream, a);
     });
   });
   return launched(what);

@@ -39,17 +39,32 @@ __device__ __forceinline__ T lowest_fill() {
 struct Share {
   float ref = kLowest, s = 0.0f, w = 0.0f, top = -kInf;
   u32 at = 0;
+  float part = -kInf;  // the largest score of the present part
 };
 
-template <class T, int E, bool ENTROPY, bool TOP>
-__device__ __forceinline__ void take(const Vec<T, E>& raw, u32 j, float c2, Share& h) {
-  float x[E], top = -kInf;
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = to_f32(raw.v[e]);
+// For the search for a row's largest scores its vectors are cut into parts, whose
+// largest score each thread leaves behind.
+constexpr u32 kParts = 8;
+constexpr u32 kUnroll = 4;  // vectors that a thread loads at once
+
+// How elements [c0, c1) of a row lie: vectors of E elements, NT to a step.
+struct Span {
+  u32 c0, c1;
+  template <int STEP>
+  __device__ __forceinline__ u32 rounds() const { return (c1 - c0 + kUnroll * STEP - 1) / (kUnroll * STEP); }
+  // vectors of a thread that make a part
+  template <int STEP>
+  __device__ __forceinline__ u32 part() const { return (rounds<STEP>() + kParts - 1) / kParts * kUnroll; }
+};
+
+template <int E, bool ENTROPY, bool TOP>
+__device__ __forceinline__ void take(const float (&x)[E], u32 j, float c2, Share& h) {
+  float top = -kInf;
 #pragma unroll
   for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);
   if constexpr (TOP) {
     if (top > h.top) h.at = j;
+    h.part = fmaxf(h.part, top);
   }
   h.top = fmaxf(h.top, top);
   const float step = (h.ref - top) * c2;
@@ -76,27 +91,63 @@ __device__ __forceinline__ void take(const Vec<T, E>& raw, u32 j, float c2, Shar
 }
 
 // Elements [c0, c1) of a row by NT threads; thread t takes the vectors that
-// start at c0 + (t + j NT) E.
+// start at c0 + (t + j NT) E.  The last vector is moved back to end with the
+// row, so that it too is one load without a branch; what it has in common with
+// the one before counts as -inf.  parts: with TOP, [kParts][NT] largest scores.
 template <class T, int NT, bool ENTROPY, bool TOP>
-__device__ __forceinline__ Share row_pass(const T* row, u32 c0, u32 c1, float c2) {
-  constexpr int E = kLogitsVector<T>, U = 4;
+__device__ __forceinline__ Share row_pass(const T* row, const Span& sp, float c2, float* parts) {
+  constexpr int E = kLogitsVector<T>, U = kUnroll;
   constexpr u32 kStep = NT * E;
+  const u32 c0 = sp.c0, c1 = sp.c1;
   Share h;
-  u32 c = c0 + threadIdx.x * E, j = 0;
-  for (u32 rest = c1 - c0; rest >= U * kStep; rest -= U * kStep, c += U * kStep, j += U) {
+  if (c1 - c0 < (u32)E) {
+    if (threadIdx.x == 0) {
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = c0 + e < c1 ? to_f32(row[c0 + e]) : -kInf;
+      take<E, ENTROPY, TOP>(x, 0, c2, h);
+    }
+    if constexpr (TOP) parts[threadIdx.x] = h.part;
+    return h;
+  }
+  u32 c = c0 + threadIdx.x * E, j = 0, part = 0, end = TOP ? sp.part<kStep>() : 0;
+  for (u32 rest = c1 - c0; rest >= U * kStep; rest -= U * kStep, c += U * kStep) {
     Vec<T, E> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = load_vec<T, E>(row + c + u * kStep);
 #pragma unroll
-    for (int u = 0; u < U; ++u) take<T, E, ENTROPY, TOP>(v[u], j + u, c2, h);
+    for (int u = 0; u < U; ++u) {
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = to_f32(v[u].v[e]);
+      take<E, ENTROPY, TOP>(x, j + u, c2, h);
+    }
+    j += U;
+    if constexpr (TOP) {
+      if (j == end) {
+        parts[part++ * NT + threadIdx.x] = h.part;
+        h.part = -kInf;
+        end += sp.part<kStep>();
+      }
+    }
   }
   Vec<T, E> v[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (c + u * kStep < c1) v[u] = load_part<T, E>(row, c + u * kStep, c1, lowest_fill<T>());
+    if (c + u * kStep < c1) v[u] = load_vec<T, E>(row + min(c + u * kStep, c1 - E));
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (c + u * kStep < c1) take<T, E, ENTROPY, TOP>(v[u], j + u, c2, h);
+  for (int u = 0; u < U; ++u) {
+    const u32 at = c + u * kStep;
+    if (at >= c1) continue;
+    const u32 skip = at - min(at, c1 - E);
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = (u32)e >= skip ? to_f32(v[u].v[e]) : -kInf;
+    take<E, ENTROPY, TOP>(x, j + u, c2, h);
+  }
+  if constexpr (TOP) {
+    if (part < kParts) parts[part * NT + threadIdx.x] = h.part;
+  }
   return h;
 }
 
@@ -148,26 +199,31 @@ template <int NT>
 struct TopLds {
   static constexpr int kList = NT == kWave ? 512 : 1024;
   u64 keys[NT];
-  u64 list[kList];
+  union {
+    u64 list[kList];
+    float parts[kParts * NT];  // given up once the owners are known
+  };
   u64 out[kMostTop];
   u32 larger[NT];
-  u32 owner[NT];
+  u16 owner[kParts * NT];
   u32 owners, listed;
 };
 
 // The k <= 64 largest keys of what the threads hold, descending, to s.out (0
 // where there are fewer).  `bound` is a key no larger than the thread's largest
-// one (0: it holds none); every thread holds `count` items at most:
-// keys_of(owner, j, f) calls f(key) for each key of item j of thread `owner`.
+// one (0: it holds none); keys_of(owner, j, f) calls f(key) for each key of item
+// j of thread `owner`, of `count` items at most.  With `parted` thread t's items
+// part i `each` .. (i + 1) each - 1 hold scores up to s.parts[i][t].
 //
 // The k-th largest of 64 groups' bounds is no larger than the k-th largest key.
-// The few threads whose own bound reaches it hold all keys that do; their items
-// are looked at by the whole workgroup, and the few keys found are ranked by
-// counting.  Where they are too many (an order made for it) or `all` is set
-// (bounds that NaNs passed by), k rounds over everything find the largest below
-// the last.
-template <int NT, class F>
-__device__ __forceinline__ void largest_keys(TopLds<NT>& s, u64 bound, u32 count, u32 k, bool all, F&& keys_of) {
+// The few threads whose own bound reaches it hold all keys that do; their items,
+// of parts that reach it, are looked at by the whole workgroup, and the few keys
+// found are ranked by counting.  Where they are too many (an order made for it)
+// or `all` is set (bounds that NaNs passed by), k rounds over everything find the
+// largest below the last.
+template <int NT, bool PARTED, class F>
+__device__ __forceinline__ void largest_keys(TopLds<NT>& s, u64 bound, u32 count, u32 each, u32 k, bool all,
+                                             F&& keys_of) {
   constexpr int W = NT / kWave;
   const u32 t = threadIdx.x, lane = t % kWave, wave = t / kWave;
   s.keys[t] = bound;
@@ -181,19 +237,28 @@ __device__ __forceinline__ void largest_keys(TopLds<NT>& s, u64 bound, u32 count
   u32 larger = 0;
 #pragma unroll
   for (int i = 0; i < kWave / W; ++i) larger += readlane64(g, wave * (kWave / W) + i) > g;
-  s.larger[t] = larger;
-  __syncthreads();
-  larger = 0;
+  if constexpr (W > 1) {
+    s.larger[t] = larger;
+    __syncthreads();
+    larger = 0;
 #pragma unroll
-  for (int i = 0; i < NT; i += kWave) larger += s.larger[lane + i];
+    for (int i = 0; i < NT; i += kWave) larger += s.larger[lane + i];
+  }
   const u64 least = readlane64(g, __builtin_ctzll(ballot(larger == k - 1)));
   if (!all) {
-    if (bound >= least && bound != 0) s.owner[atomicAdd(&s.owners, 1u)] = t;
+    if (bound >= least && bound != 0) {
+      if constexpr (PARTED) {
+        for (u32 i = 0; i * each < count; ++i)
+          if (score_order(s.parts[i * NT + t]) >= (u32)(least >> 32)) s.owner[atomicAdd(&s.owners, 1u)] = (u16)(i * NT + t);
+      } else {
+        s.owner[atomicAdd(&s.owners, 1u)] = (u16)t;
+      }
+    }
     __syncthreads();
-    const u32 items = s.owners * count;
+    const u32 items = s.owners * each;
     for (u32 i = t; i < items; i += NT) {
-      const u32 o = i / count;
-      keys_of(s.owner[o], i - o * count, [&](u64 key) {
+      const u32 o = i / each, owner = s.owner[o];
+      keys_of(owner % NT, owner / NT * each + (i - o * each), [&](u64 key) {
         if (key < least) return;
         const u32 at = atomicAdd(&s.listed, 1u);
         if (at < TopLds<NT>::kList) s.list[at] = key;
