@@ -166,24 +166,31 @@ __global__ __launch_bounds__(NT) void k_logprobs(LogprobsArgs a) {
   }
   const int token = (int)given;
   const float score = to_f32(z[token]);
+  const u32 first = c0 + threadIdx.x * E, at = first + h.at * (NT * E);
+  u64 bound = first < c1 ? entry_key(h.top, min(at + E, c1) - 1) : 0;
+  if constexpr (TOP) {
+    offer_bound(s_top, bound);
+    if constexpr (NT == kWave) __syncthreads();  // else there is one in what comes next
+  }
   RowSums r = join_shares<NT>(h, a.z.c2, s_red);
   const u64* keys = nullptr;
   if constexpr (TOP) {
-    const u32 first = c0 + threadIdx.x * E, at = first + h.at * (NT * E);
-    const u64 bound = first < c1 ? entry_key(h.top, min(at + E, c1) - 1) : 0;
     const u32 count = (c1 - c0 + NT * E - 1) / (NT * E), each = span.part<NT * E>();
     largest_keys<NT, true>(s_top, bound, count, each, a.top, r.s != r.s, [&](u32 owner, u32 j, auto&& f) {
       const u32 c = c0 + (owner + j * NT) * E;
       if (c >= c1) return;
+      float x[E];
       if (c1 - c0 < (u32)E) {
-        for (u32 i = c; i < c1; ++i) f(entry_key(to_f32(z[i]), i));
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = c + e < c1 ? to_f32(z[c + e]) : 0.0f;
+        f(x, c, 0u, c1 - c);
         return;
       }
       const u32 from = min(c, c1 - E);
       const Vec<T, E> v = load_vec<T, E>(z + from);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (from + e >= c) f(entry_key(to_f32(v.v[e]), from + e));
+      for (int e = 0; e < E; ++e) x[e] = to_f32(v.v[e]);
+      f(x, from, c - from, (u32)E);
     });
     keys = s_top.out;
   }
@@ -197,21 +204,25 @@ __global__ __launch_bounds__(NT) void k_logprobs(LogprobsArgs a) {
     r = join_slices(a.split, part, a.z.c2, s_sums);
     if constexpr (TOP) {
       // thread t holds the keys t, t + NT, .. of the slices'
-      const u32 n = slices * a.top;
+      const u32 n = slices * a.top, count = (n + NT - 1) / NT;
       const u64* all = a.split.keys + part * n;
-      u64 held[kMostSlices * kMostTop / NT], bound = 0;
+      constexpr int kHeld = kMostSlices * kMostTop / NT;
+      u64 held[kHeld];
 #pragma unroll
-      for (int j = 0; j < kMostSlices * kMostTop / NT; ++j) {
+      for (int j = 0; j < kHeld; ++j) {
         const u32 i = threadIdx.x + j * NT;
         held[j] = i < n ? ld_agent64(all + i) : 0;
       }
+      bound = 0;
 #pragma unroll
       for (u64 key : held) bound = max(bound, key);
-      const u32 count = (n + NT - 1) / NT;
-      largest_keys<NT, false>(s_top, bound, count, count, a.top, false, [&](u32 owner, u32 j, auto&& f) {
+      offer_bound(s_top, bound);
+      __syncthreads();
+      largest_keys<NT, false>(s_top, bound, count, count, a.top, r.s != r.s, [&](u32 owner, u32 j, auto&& f) {
         const u32 i = owner + j * NT;
         const u64 key = i < n ? ld_agent64(all + i) : 0;
-        if (key != 0) f(key);
+        const float x[1] = {key_score(key)};
+        if (key != 0) f(x, key_index(key), 0u, 1u);
       });
     }
   }
