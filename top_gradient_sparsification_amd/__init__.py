@@ -1121,7 +1121,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
         out_dtype = out_dtype or x.dtype
         if out_dtype not in _FLOATS:
             raise TypeError("out_dtype must be one of %s" % ", ".join(map(str, _FLOATS)))
-        out = x.new_empty(x.shape, dtype=out_dtype)
+        out = torch.empty_like(x, dtype=out_dtype)
     else:
         _places(out, _FLOATS if out_dtype is None else (out_dtype,), "out", dev, x.shape)
     mean = rstd = None
@@ -1172,7 +1172,7 @@ def layer_norm_grad(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rst
         return results if params else (results[0], None, None)
     given = out is not None
     if not given:
-        out = x.new_empty(x.shape)
+        out = torch.empty_like(x)
     else:
         _places(out, (x.dtype,), "out", dev, x.shape)
     gw = gb = None
@@ -1253,9 +1253,9 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: floa
         return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, temperature, top, entropy, ws))
     top = int(top)
     shape = tokens.shape
-    logprobs = logits.new_empty(shape, dtype=torch.float32)
+    logprobs = torch.empty_like(tokens, dtype=torch.float32)
     stats = logits.new_empty((*shape, 2), dtype=torch.float32)
-    ent = logits.new_empty(shape, dtype=torch.float32) if entropy else None
+    ent = torch.empty_like(logprobs) if entropy else None
     at = values = None
     if top > 0:
         at = logits.new_empty((*shape, top), dtype=torch.int32)
