@@ -368,14 +368,16 @@ tgs_status tgs_muon_step(void* weight, tgs_dtype weight_dtype, const void* grad,
  *   weight, bias  [D] of one type, fp32, bf16 or fp16; either may be null (1, 0).
  *   mean, rstd    [T] float, out, for the gradients; either may be null.
  * 0 <= T <= 2^31 - 1, 1 <= D <= 2^24, eps >= 0.  The mean is known before the
- * squares are summed, so a large mean costs no more than x's own rounding.
+ * squares are summed, so a large mean costs no more than x's own rounding; rows
+ * whose squares pass fp32's range are normed too.  A row's NaN or infinity makes the
+ * whole row NaN.
  */
 tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T, int64_t D, const void* weight, const void* bias,
                           tgs_dtype weight_dtype, float eps, void* out, tgs_dtype out_dtype, float* mean, float* rstd,
                           hipStream_t stream);
 
 /* Bytes of workspace tgs_layer_norm_grad needs (0 if the sizes are invalid): up
-   to 512 partial rows of 2 D floats. */
+   to 1,280 partial rows of 2 D floats, 34 MB at most. */
 size_t tgs_layer_norm_grad_workspace_bytes(int64_t T, int64_t D);
 
 /*
@@ -403,7 +405,7 @@ size_t tgs_token_logprobs_workspace_bytes(int64_t T, int64_t V, tgs_dtype dtype,
  *   logits    [T] rows of V scores, fp32, bf16 or fp16, `ld` elements from row to
  *             row (ld >= V; what lies between rows is not read).
  *   tokens    [T] int32 or int64.  A negative token is a masked place: its row
- *             is not read, and its results are +0 and -1.  A token >= V sets
+ *             is not needed, and its results are +0 and -1.  A token >= V sets
  *             the bad-input bit of the device error word and is masked too.
  *   logprobs  [T] float: log p(token).
  *   stats     [T][2] float: (r, l) with log sum e^(logits / temperature) = r /
@@ -417,6 +419,7 @@ size_t tgs_token_logprobs_workspace_bytes(int64_t T, int64_t V, tgs_dtype dtype,
  * score like any other.  A row of which every score is -inf has log
  * probabilities of -inf and entropy 0.  NaN or +inf in a row makes its
  * log probabilities and entropy NaN; among alternatives a NaN ranks above all.
+ * Equal calls give equal bits.
  */
 tgs_status tgs_token_logprobs(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
                               const void* tokens, tgs_dtype tokens_dtype, float temperature, float* logprobs,

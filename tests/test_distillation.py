@@ -313,6 +313,20 @@ def test_offsets_past_32_bits(tgs_gpu):
 
 
 @pytest.mark.gpu
+def test_more_rows_than_a_launch_takes(tgs_gpu):
+    T, V = 2**22 + 1000, 3  # the two-in-one call's launches are cut for its largest workgroups
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    logits = torch.randn(T, V, device="cuda", generator=gen)
+    indices = torch.randint(-1, V, (T, 2), device="cuda", generator=gen)
+    teacher = torch.randn(T, 2, device="cuda", generator=gen)
+    tail = slice(T - 2000, T)
+    loss, grad = tgs_gpu.distillation_loss_and_grad(logits, indices, teacher)
+    want, wgrad = tgs_gpu.distillation_loss_and_grad(logits[tail], indices[tail], teacher[tail])
+    assert torch.equal(loss[tail], want) and torch.equal(grad[tail], wgrad)
+    check(tgs_gpu, logits[tail], indices[tail], teacher[tail])
+
+
+@pytest.mark.gpu
 def test_gradients_flow(tgs_gpu):
     z = scores(24, 300, torch.float32, 3).clone()
     indices, teacher = make_teacher(z, 12, torch.float32, torch.int32, 3)

@@ -149,6 +149,8 @@ def test_refusals_of_each(lib):
     assert grad_call(lib, gb=0x400000) == EINVAL
     need = lib.tgs_layer_norm_grad_workspace_bytes(16, 8)
     assert need >= 32768 and grad_call(lib, wsn=need - 1) == EWORKSPACE
+    for T, D in ((1, 2**24), (10**6, 2**20), (10**6, 40_000), (10**6, 16_384), (10**6, 512), (2**31 - 1, 1)):
+        assert 32768 < lib.tgs_layer_norm_grad_workspace_bytes(T, D) <= 32768 + max(2**25, 8 * D)
     for bad in ((-1, 8), (2**31, 8), (8, 0), (8, 2**24 + 1)):
         assert lib.tgs_layer_norm_grad_workspace_bytes(*bad) == 0
 
@@ -296,6 +298,28 @@ def test_offsets_past_32_bits(tgs_gpu):
     gx, gw, gb = tgs_gpu.layer_norm_grad(y, x, mean, rstd, w, param_dtype=torch.float32)
     px, _, _ = tgs_gpu.layer_norm_grad(part, x[-4000:], pm, pr, w)
     assert torch.equal(gx[-4000:], px)
+
+
+@pytest.mark.gpu
+def test_very_long_rows(tgs_gpu):
+    D = 300_001
+    x = make(40, D, torch.bfloat16, 1)
+    check(tgs_gpu, x, *params(D, torch.float32, 2))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D", [(517, 131), (1024, 256), (1025, 256), (4096, 100), (8192, 60), (8193, 60), (64, 257)])
+def test_either_side_of_the_one_launch_rule(tgs_gpu, T, D):
+    """The gradient twice on one workspace of the caller's: its counter is left as it was found."""
+    for dtype in (torch.float32, torch.bfloat16):
+        x, (w, b) = make(T, D, dtype, 3), params(D, torch.float32, 4)
+        first = check(tgs_gpu, x, w, b)
+        ws = torch.zeros(tgs_gpu.layer_norm_grad_workspace_bytes(T, D), dtype=torch.uint8, device="cuda")
+        _, mean, rstd = tgs_gpu.layer_norm(x, w, b, return_stats=True)
+        for _ in range(3):
+            for got, want in zip(tgs_gpu.layer_norm_grad(first[1], x, mean, rstd, w, ws=ws), first[2:]):
+                assert torch.equal(got, want)
+            assert not ws[:32768].any()
 
 
 @pytest.mark.gpu

@@ -387,6 +387,22 @@ def test_offsets_past_32_bits(tgs_gpu):
 
 
 @pytest.mark.gpu
+def test_more_rows_than_a_launch_takes(tgs_gpu):
+    """2^26 workgroups of a wave are a launch: the rows behind them."""
+    T, V = 2**26 + 1000, 2
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    logits = torch.randn(T, V, device="cuda", generator=gen).to(torch.bfloat16)
+    tokens = torch.randint(-1, V, (T,), device="cuda", generator=gen, dtype=torch.int32)
+    r = tgs_gpu.token_logprobs(logits, tokens, entropy=True)
+    g = tgs_gpu.token_logprobs_grad(logits, tokens, r.stats, r.logprobs)
+    tail = slice(T - 2000, T)
+    part = check_forward(tgs_gpu, logits[tail], tokens[tail])
+    for a, b in zip((r.logprobs, r.entropy, r.stats), (part.logprobs, part.entropy, part.stats)):
+        assert torch.equal(a[tail], b)
+    assert torch.equal(g[tail], tgs_gpu.token_logprobs_grad(logits[tail], tokens[tail], part.stats, part.logprobs))
+
+
+@pytest.mark.gpu
 def test_gradients_flow(tgs_gpu):
     z = scores(24, 300, torch.float32, 3).reshape(4, 6, 300).clone().requires_grad_()
     tokens = make_tokens(z.detach().reshape(24, 300), 0.2, torch.int64, 3).view(4, 6)

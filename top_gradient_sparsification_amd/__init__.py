@@ -1241,7 +1241,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: floa
     to the lower index) and ``top_logprobs``, ``[..., top]``; and ``stats``, as
     ``token_logprobs_grad`` takes them.
 
-    A negative token is a masked place: its row is not read and its results are
+    A negative token is a masked place: its row is not needed and its results are
     0 (alternatives -1); a token >= V too, and it sets the bad-input bit that
     ``check_device_error(ws)`` reports.  Scores of -inf have no probability.
 

@@ -532,7 +532,7 @@ static bool with_shape(int64_t D, int64_t most, F&& f) {
 // 14.9.
 template <int E>
 static int64_t norm_groups(int64_t T, int64_t D, bool* one) {
-  int64_t rows = 1, most = 64;
+  int64_t rows = 1, most = std::max<int64_t>(1, std::min<int64_t>(64, ((int64_t)1 << 22) / D));  // 34 MB at most
   *one = false;
   with_shape<E>(D, kMostHeldBack<E>, [&](auto, auto l, auto nv) {
     constexpr int NT = norm_threads(decltype(l)::value);
