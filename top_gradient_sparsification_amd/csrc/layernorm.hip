@@ -527,6 +527,11 @@ static bool with_shape(int64_t D, int64_t most, F&& f) {
 // and 86.  Of 1,024 threads 256: 16,384 rows of 16,384 480, 309 and 328 with 128, 256
 // and 512.
 //
+// Each takes two sets of rows at least, whose partial rows few rows would outweigh:
+// with one, two, four and eight 512 rows of 4,096 in bf16 take 21.1, 15.3, 14.8 and
+// 19.6 us a call, 512 of 8,192 30, 22.5, 23.3 and 31, 2,048 of 2,048 21.1, 17.9, 20.5
+// and 29.5.
+//
 // `one`: few rows of few columns, whose last workgroup adds the partial rows itself
 // instead of a second launch: 517 rows of 131 in fp32 take 12.7 us a call instead of
 // 14.9.
@@ -540,6 +545,7 @@ static int64_t norm_groups(int64_t T, int64_t D, bool* one) {
     *one = D <= 256 && (T + rows - 1) / rows <= 256;
     most = *one ? 64 : NT > 256 ? 256 : decltype(nv)::value == 1 ? 1280 : 512;
   });
+  if (!*one) rows *= 2;
   return std::max<int64_t>(1, std::min(most, (T + rows - 1) / rows));
 }
 
