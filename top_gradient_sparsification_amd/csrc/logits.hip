@@ -278,7 +278,7 @@ __device__ __forceinline__ u32 aligned_column(const T* out, u32 c0, u32 c1) {
 // the caches.
 template <class T, int NT, class F, class P>
 __device__ __forceinline__ void map_row(const T* z, T* out, u32 c0, u32 c1, bool streaming, F&& f, P&& patch) {
-  constexpr int E = kLogitsVector<T>, U = kUnroll;
+  constexpr int E = kLogitsVector<T>, U = 2;
   constexpr u32 kStep = NT * E;
   const u32 start = aligned_column(out, c0, c1);
   const auto one = [&](const Vec<T, E>& v, u32 at) {
@@ -609,9 +609,9 @@ struct RowPlan {
 
 // Slices of a row for about `groups` workgroups in all, none shorter than one
 // round of loads.
-static RowPlan row_plan(int64_t T, int64_t V, u32 unit, int64_t groups, int64_t most) {
+static RowPlan row_plan(int64_t T, int64_t V, u32 unit, int64_t groups, int64_t most, int64_t least = 1) {
   const int64_t want = std::max<int64_t>(1, std::min(most, groups / std::max<int64_t>(T, 1)));
-  const int64_t per = std::max<int64_t>((V + want - 1) / want, kUnroll * (int64_t)unit);
+  const int64_t per = std::max<int64_t>({(V + want - 1) / want, kUnroll * (int64_t)unit, least});
   const int64_t length = (per + unit - 1) / unit * unit;
   return RowPlan{(u32)((V + length - 1) / length), (u32)std::min<int64_t>(length, (int64_t)1 << 31)};
 }
@@ -642,7 +642,16 @@ static u32 row_unit(tgs_dtype t) { return kRowThreads * (u32)(16 / dtype_bytes(t
 static RowPlan pass_plan(int64_t T, int64_t V, tgs_dtype t) {
   return row_plan(T, V, row_unit(t), kPassGroups, kMostSlices);
 }
-static RowPlan grad_plan_of(int64_t T, int64_t V, tgs_dtype t) { return row_plan(T, V, row_unit(t), 4096, INT32_MAX); }
+// Gradients go in short slices, each of four vectors a thread: many workgroups that
+// end and are followed by the next in memory reach what few long ones do not.  With
+// 4,096, 16,384 and 32,768 workgroups 8,192 rows of 32,000 in bf16 take 207, 208 and
+// 189 us, with 64 slots 212, 212 and 184, 2,048 of 128,000 210, 211 and 190; with
+// slices of two vectors 198, 219 and 180.  Each slice reads the row's slots: 512 of
+// them on 2,048 rows of 50,001 take 139 us in one slice a row and 178 in slices of
+// 8,192, so a slice is 64 times as long as the slots are many.
+static RowPlan grad_plan_of(int64_t T, int64_t V, tgs_dtype t, int64_t K) {
+  return row_plan(T, V, row_unit(t), 32768, INT32_MAX, 64 * K);
+}
 
 static size_t sums_bytes(int64_t T, const RowPlan& p) {
   return p.slices == 1 ? 0 : round_up_256((size_t)T * p.slices * sizeof(SliceSums));
@@ -807,7 +816,7 @@ extern "C" tgs_status tgs_token_logprobs_grad(const void* logits, tgs_dtype dtyp
                         {"the workspace", workspace, workspace_bytes, 256, true}};
   if ((st = check_arrays(what, in, outs, same)) != TGS_OK) return st;
   if (T == 0) return TGS_OK;
-  const RowPlan p = grad_plan_of(T, V, dtype);
+  const RowPlan p = grad_plan_of(T, V, dtype, 0);
   LogprobsGradArgs a{};
   a.z = logits_of(logits, ld, V, temperature);
   a.tokens = tokens;
@@ -853,7 +862,7 @@ static tgs_status distillation(const char* what, const void* logits, tgs_dtype d
   if (K < 1 || K > kMostSlots) return fail(TGS_EINVAL, "%s: K=%lld outside [1, %d]", what, (long long)K, kMostSlots);
   if (has_grad && (ld_out < V || ld_out > INT32_MAX))
     return fail(TGS_EINVAL, "%s: rows of out %lld elements apart", what, (long long)ld_out);
-  const RowPlan p = pass_plan(T, V, dtype), g = grad_plan_of(T, V, dtype);
+  const RowPlan p = pass_plan(T, V, dtype), g = grad_plan_of(T, V, dtype, K);
   const size_t need = has_loss ? tgs_distillation_workspace_bytes(T, V, dtype) : kWorkspaceHeader;
   if ((st = check_rows_workspace(what, workspace, workspace_bytes, need)) != TGS_OK) return st;
   const size_t is = dtype_bytes(indices_dtype), es = dtype_bytes(teacher_dtype), n = (size_t)T * 4;
