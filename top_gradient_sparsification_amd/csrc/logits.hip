@@ -276,8 +276,9 @@ __device__ __forceinline__ u32 aligned_column(const T* out, u32 c0, u32 c1) {
 // where with 16 bytes.
 // From the end to the start: a pass over the row that came before left its end in
 // the caches.
-template <class T, int NT, class F, class P>
-__device__ __forceinline__ void map_row(const T* z, T* out, u32 c0, u32 c1, bool streaming, F&& f, P&& patch) {
+template <class T, int NT, bool KEPT, class F, class P>
+__device__ __forceinline__ void map_row(const T* z, T* out, u32 c0, u32 c1, bool streaming,
+                                        const Vec<T, kLogitsVector<T>>* kept, F&& f, P&& patch) {
   constexpr int E = kLogitsVector<T>, U = 2;
   constexpr u32 kStep = NT * E;
   const u32 start = aligned_column(out, c0, c1);
@@ -306,10 +307,17 @@ __device__ __forceinline__ void map_row(const T* z, T* out, u32 c0, u32 c1, bool
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (c + u * kStep + E <= c1) one(v[u], c + u * kStep);
+  // with KEPT (c0 = 0) the row's first vectors are at hand where out's lines begin with one of them
+  const u32 held = KEPT && start % E == 0 ? kUnroll * kStep : 0;
   for (; rounds > 0; --rounds) {
     c -= U * kStep;
+    if (KEPT && start + rounds * (U * kStep) <= held) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = load_vec<T, E>(z + c + u * kStep);
+      for (int u = 0; u < U; ++u) v[u] = kept[c / E + u * NT];
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = load_vec<T, E>(z + c + u * kStep);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) one(v[u], c + u * kStep);
   }
@@ -347,8 +355,8 @@ __global__ __launch_bounds__(NT) void k_logprobs_grad(LogprobsGradArgs a) {
   k.b = -g;
   k.a = ENTROPY ? a.grad_entropy[row] * a.z.inv : 0.0f;
   k.h = ENTROPY ? a.entropy[row] : 0.0f;
-  map_row<T, NT>(
-      (const T*)a.z.p + row * a.z.ld, out, c0, c1, a.streaming, [&](float x) { return slope<ENTROPY>(a.z, k, x); },
+  map_row<T, NT, false>(
+      (const T*)a.z.p + row * a.z.ld, out, c0, c1, a.streaming, nullptr, [&](float x) { return slope<ENTROPY>(a.z, k, x); },
       [&](auto& y, u32 at) {
         constexpr u32 N = sizeof(y) / sizeof(y[0]);
         if ((u32)token - at >= N) return;
@@ -510,12 +518,13 @@ __device__ __forceinline__ Coefficients distill_coefficients(const DistillArgs& 
 }
 
 // out = (p - q) b for columns [c0, c1) of a row.
-template <class T, int NT>
+template <class T, int NT, bool KEPT>
 __device__ __forceinline__ void write_distill_grad(const DistillArgs& a, const T* z, T* out, u32 c0, u32 c1,
-                                                   const Coefficients& k, const Slots& s) {
+                                                   const Coefficients& k, const Slots& s,
+                                                   const Vec<T, kLogitsVector<T>>* kept) {
   const u32 start = aligned_column(out, c0, c1);
-  map_row<T, NT>(
-      z, out, c0, c1, a.streaming, [&](float x) { return slope<false>(a.z, k, x); },
+  map_row<T, NT, KEPT>(
+      z, out, c0, c1, a.streaming, kept, [&](float x) { return slope<false>(a.z, k, x); },
       [&](auto& y, u32 at) {
         constexpr u32 N = sizeof(y) / sizeof(y[0]);
         for (u32 o = s.head[head_of<T>(at, start)]; o != kNoSlot; o = s.next[o]) {
@@ -540,8 +549,10 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, fl
 // row is read again, from the caches.
 template <class T, int NT, bool GRAD>
 __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
+  constexpr bool KEEP = GRAD && NT >= 512;
   extern __shared__ float s_slots[];
   __shared__ float s_red[kJoinLds<NT>], s_more[4][16];
+  __shared__ Vec<T, kLogitsVector<T>> s_kept[KEEP ? kUnroll * NT : 1];
   const Slots s = slots_in<true, GRAD>(s_slots, a.K, s_more);
   const int64_t row = a.row0 + blockIdx.x;
   const T* z = (const T*)a.z.p + row * a.z.ld;
@@ -551,13 +562,13 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
     if constexpr (GRAD) zero_row<T, NT>(out, 0, a.z.V, a.streaming);
     return;
   }
-  const Share h = row_pass<T, NT, false, false>(z, Span{0, a.z.V}, a.z.c2, nullptr);
+  const Share h = row_pass<T, NT, false, false, KEEP>(z, Span{0, a.z.V}, a.z.c2, nullptr, s_kept);
   const RowSums r = join_shares<NT>(h, a.z.c2, s_red);
   const float log_s = r.s == 0.0f ? 0.0f : logf(r.s);
   write_loss(a, row, slots_loss<NT>(a, r, log_s, s), r.m, log_s);
   if constexpr (GRAD) {
     if (r.s == 0.0f) zero_row<T, NT>(out, 0, a.z.V, a.streaming);
-    else write_distill_grad<T, NT>(a, z, out, 0, a.z.V, distill_coefficients(a, row, r.m, log_s, s), s);
+    else write_distill_grad<T, NT, KEEP>(a, z, out, 0, a.z.V, distill_coefficients(a, row, r.m, log_s, s), s, s_kept);
   }
 }
 
@@ -599,7 +610,7 @@ __global__ __launch_bounds__(NT) void k_distill_grad(DistillArgs a) {
   const T* z = (const T*)a.z.p + row * a.z.ld;
   const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
   if (!load_slots<T, NT, false, true>(a, row, z, out, c0, c1, s) || m == -kInf) zero_row<T, NT>(out, c0, c1, a.streaming);
-  else write_distill_grad<T, NT>(a, z, out, c0, c1, distill_coefficients(a, row, m, log_s, s), s);
+  else write_distill_grad<T, NT, false>(a, z, out, c0, c1, distill_coefficients(a, row, m, log_s, s), s, nullptr);
 }
 
 // ------------------------------------------------------------------ host --

@@ -94,8 +94,10 @@ __device__ __forceinline__ void take(const float (&x)[E], u32 j, float c2, Share
 // start at c0 + (t + j NT) E.  The last vector is moved back to end with the
 // row, so that it too is one load without a branch; what it has in common with
 // the one before counts as -inf.  parts: with TOP, [kParts][NT] largest scores.
-template <class T, int NT, bool ENTROPY, bool TOP>
-__device__ __forceinline__ Share row_pass(const T* row, const Span& sp, float c2, float* parts) {
+// kept: where the first round of a row from column 0 on is left, in order.
+template <class T, int NT, bool ENTROPY, bool TOP, bool KEEP = false>
+__device__ __forceinline__ Share row_pass(const T* row, const Span& sp, float c2, float* parts,
+                                          Vec<T, kLogitsVector<T>>* kept = nullptr) {
   constexpr int E = kLogitsVector<T>, U = kUnroll;
   constexpr u32 kStep = NT * E;
   const u32 c0 = sp.c0, c1 = sp.c1;
@@ -115,6 +117,12 @@ __device__ __forceinline__ Share row_pass(const T* row, const Span& sp, float c2
     Vec<T, E> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = load_vec<T, E>(row + c + u * kStep);
+    if constexpr (KEEP) {
+      if (j == 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) kept[u * NT + threadIdx.x] = v[u];
+      }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float x[E];
