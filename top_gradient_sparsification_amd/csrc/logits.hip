@@ -299,16 +299,22 @@ __device__ __forceinline__ void map_row(const T* z, T* out, u32 c0, u32 c1, bool
     patch(y, at);
     out[at] = round_vec<T, 1>(y).v[0];
   }
+  // with KEPT (c0 = 0) the row's first vectors are at hand where out's lines begin with one of them
+  const u32 held = KEPT && start % E == 0 ? kUnroll * kStep : 0;
   u32 rounds = (c1 - start) / (U * kStep), c = start + rounds * (U * kStep) + threadIdx.x * E;
   Vec<T, E> v[U];
+  if (KEPT && c1 <= held) {
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (c + u * kStep + E <= c1) v[u] = load_vec<T, E>(z + c + u * kStep);
+    for (int u = 0; u < U; ++u)
+      if (c + u * kStep + E <= c1) v[u] = kept[c / E + u * NT];
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c + u * kStep + E <= c1) v[u] = load_vec<T, E>(z + c + u * kStep);
+  }
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (c + u * kStep + E <= c1) one(v[u], c + u * kStep);
-  // with KEPT (c0 = 0) the row's first vectors are at hand where out's lines begin with one of them
-  const u32 held = KEPT && start % E == 0 ? kUnroll * kStep : 0;
   for (; rounds > 0; --rounds) {
     c -= U * kStep;
     if (KEPT && start + rounds * (U * kStep) <= held) {
@@ -546,10 +552,12 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, fl
 }
 
 // The losses; with GRAD the gradient of their weighted sum too, for which the
-// row is read again, from the caches.
+// row is read again: its first round of vectors, 16 to 64 KB, from LDS, the rest from
+// the caches (8,192 rows of 32,000 in bf16 take 212 us, 243 without LDS; 4,096 of
+// 128,000 448 and 492).
 template <class T, int NT, bool GRAD>
 __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
-  constexpr bool KEEP = GRAD && NT >= 512;
+  constexpr bool KEEP = GRAD && NT >= kRowThreads;
   extern __shared__ float s_slots[];
   __shared__ float s_red[kJoinLds<NT>], s_more[4][16];
   __shared__ Vec<T, kLogitsVector<T>> s_kept[KEEP ? kUnroll * NT : 1];
@@ -633,12 +641,14 @@ static RowPlan row_plan(int64_t T, int64_t V, u32 unit, int64_t groups, int64_t 
 // 54 and 49.  In fp32 1,500 scores take 19 and 23 us, 2,500 29 and 28.
 static bool short_row(int64_t V, tgs_dtype t) { return V * (int64_t)dtype_bytes(t) <= 320 * 16; }
 // The call that reads a row twice keeps fewer rows in flight where they are long, so
-// that the second reading finds them in the caches.  With 256, 512 and 1,024 threads
-// 8,192 rows of 32,000 in bf16 take 267, 243 and 281 us, 4,096 of 128,000 606, 561
-// and 491, 2,048 of 64,000 in fp32 301, 280 and 258.
+// that the second reading finds them in the caches.  In bf16, with 256, 512 and 1,024
+// threads, before any of a row was kept in LDS, 8,192 rows of 32,000 take 267, 243 and
+// 281 us, 4,096 of 128,000 606, 561 and 491.  With what is kept, 8,192 rows of 9,000
+// take 77 us with 256 and 96 with 512, of 20,000 147 with 512 and 194 with 1,024, of
+// 64,000 443 with 512 and 421 with 1,024; 2,048 of 50,001 in fp16 110 and 116.
 static int step_threads(int64_t V, tgs_dtype t) {
   const int64_t bytes = V * (int64_t)dtype_bytes(t);
-  return short_row(V, t) ? kWave : bytes < 32 << 10 ? kRowThreads : bytes < 128 << 10 ? 512 : 1024;
+  return short_row(V, t) ? kWave : bytes < 32 << 10 ? kRowThreads : bytes < 112 << 10 ? 512 : 1024;
 }
 
 // Workgroups of a call whose rows go in slices.  Every slice, and every row's join,

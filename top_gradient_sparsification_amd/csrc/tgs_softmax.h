@@ -94,7 +94,8 @@ __device__ __forceinline__ void take(const float (&x)[E], u32 j, float c2, Share
 // start at c0 + (t + j NT) E.  The last vector is moved back to end with the
 // row, so that it too is one load without a branch; what it has in common with
 // the one before counts as -inf.  parts: with TOP, [kParts][NT] largest scores.
-// kept: where the first round of a row from column 0 on is left, in order.
+// kept: where the whole vectors of the first round of a row from column 0 on are
+// left, in order.
 template <class T, int NT, bool ENTROPY, bool TOP, bool KEEP = false>
 __device__ __forceinline__ Share row_pass(const T* row, const Span& sp, float c2, float* parts,
                                           Vec<T, kLogitsVector<T>>* kept = nullptr) {
@@ -148,6 +149,9 @@ __device__ __forceinline__ Share row_pass(const T* row, const Span& sp, float c2
     const u32 at = c + u * kStep;
     if (at >= c1) continue;
     const u32 skip = at - min(at, c1 - E);
+    if constexpr (KEEP) {
+      if (j == 0 && skip == 0) kept[u * NT + threadIdx.x] = v[u];
+    }
     float x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = (u32)e >= skip ? to_f32(v[u].v[e]) : -kInf;
