@@ -9,7 +9,8 @@
 // row stays in the registers of the lanes that read it (8 lanes to 1,024,
 // several vectors each), so that the mean is known before the squares are
 // summed and no value is read twice.  Rows that registers do not hold are read
-// again, from the caches.
+// again, from the caches.  131,072 rows of 2,048 in bf16: 185 us (5.8 TB/s, as a copy);
+// 65,536 of 4,096 back, with weight and bias: 297 us (5.4).
 #include <type_traits>
 
 #include "tgs_rows.h"

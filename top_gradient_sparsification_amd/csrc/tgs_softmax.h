@@ -29,11 +29,6 @@ struct Logits {
 template <class T>
 constexpr int kLogitsVector = 16 / sizeof(T);
 
-template <class T>
-__device__ __forceinline__ T lowest_fill() {
-  return from_f32<T>(-kInf);
-}
-
 // A thread's share: sums relative to `ref`, the largest score and the first
 // vector that holds it (counted in the thread's own).
 struct Share {
@@ -199,10 +194,6 @@ __device__ __forceinline__ float key_score(u64 key) {
   const u32 o = (u32)(key >> 32);
   if (o == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
   return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
-}
-
-__device__ __forceinline__ u64 readlane64(u64 v, int lane) {
-  return (u64)(u32)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 | (u32)__builtin_amdgcn_readlane((int)v, lane);
 }
 
 constexpr int kMostTop = 64;
