@@ -197,6 +197,33 @@ def test_slots(tgs_gpu, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V", [9000, 16_000, 16_001, 32_768, 32_775, 60_000, 60_001])
+def test_rows_read_twice_by_one_workgroup(tgs_gpu, V):
+    """Rows kept in LDS whole and in part, by 256, 512 and 1,024 threads, from and to lines and between them."""
+    T = 520
+    for dtype, pad, K in ((torch.bfloat16, 0, 9), (torch.float32, 3, 70)):
+        logits = scores(T, V, dtype, V, pad=pad)
+        indices, teacher = make_teacher(logits, K, torch.float32, torch.int32, V)
+        g = torch.randn(T, generator=torch.Generator().manual_seed(3)).cuda()
+        loss, grad = tgs_gpu.distillation_loss_and_grad(logits, indices, teacher, g, 1.5)
+        _, want, tol, _, _, live = exact(logits, indices, teacher, 1.5)
+        assert_close(loss, torch.where(live, want, 0.0), tol * live, "loss")
+        check_grad(grad, logits, indices, teacher, g, 1.5)
+        again, out = tgs_gpu.distillation_loss_and_grad(logits, indices, teacher, g, 1.5, out=logits)
+        assert torch.equal(again, loss) and torch.equal(logits, grad)
+
+
+@pytest.mark.gpu
+def test_most_slots_beside_a_row_in_lds(tgs_gpu):
+    logits = scores(515, 60_000, torch.bfloat16, 1)
+    indices, teacher = make_teacher(logits, 1024, torch.bfloat16, torch.int64, 1)
+    loss, grad = tgs_gpu.distillation_loss_and_grad(logits, indices, teacher)
+    _, want, tol, _, _, live = exact(logits, indices, teacher, 1.0)
+    assert_close(loss, torch.where(live, want, 0.0), tol * live, "loss")
+    check_grad(grad, logits, indices, teacher, torch.ones(515))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,V", [(9, 100), (9, 3000), (9, 60_000), (1100, 3000)])
 def test_an_index_in_several_slots(tgs_gpu, T, V):
     for dtype in FLOATS:
