@@ -173,3 +173,27 @@ def test_one_workspace_for_calls_of_all_kinds(tgs_gpu):
         r = tgs_gpu.token_logprobs(logits, tokens, top=9, entropy=True, ws=ws)
         assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(torch.equal(a, b) for a, b in zip(r, first))
         tgs_gpu.check_device_error(ws)
+
+
+@pytest.mark.gpu
+def test_an_out_that_requires_a_gradient_is_refused(tgs_gpu):
+    """Written behind autograd's back it would keep a graph of the values that it held before."""
+    T, D, V, K = 6, 40, 50, 3
+    i = inputs(T, D, V, K, torch.float32, 9)
+    z = scores(T, V, torch.float32, 1)
+    f, st = torch.ones(T, device="cuda"), torch.zeros(T, 2, device="cuda")
+    for make in (lambda *shape: torch.zeros(shape, device="cuda").requires_grad_(),
+                 lambda *shape: torch.zeros(shape, device="cuda").requires_grad_() * 2):
+        row, out = make(T, D), make(T, V)
+        for call in (lambda: tgs_gpu.layer_norm(i["x"], out=row),
+                     lambda: tgs_gpu.layer_norm_grad(i["x"], i["x"], f, f, out=row),
+                     lambda: tgs_gpu.token_logprobs_grad(z, i["tokens"], st, f, out=out),
+                     lambda: tgs_gpu.distillation_grad(z, i["at"], i["teacher"], st, f, out=out),
+                     lambda: tgs_gpu.distillation_loss_and_grad(z, i["at"], i["teacher"], f, out=out)):
+            with pytest.raises(RuntimeError, match="out requires a gradient"):
+                call()
+            assert not out.any() and not row.any()
+            with torch.no_grad():
+                call()
+            with torch.no_grad():
+                row.zero_(), out.zero_()

@@ -1001,6 +1001,12 @@ def _tracked(*tensors) -> bool:
     return False
 
 
+def _untracked_out(out):
+    """A graph that ``out`` belongs to would go back through values that are no longer there."""
+    if _tracked(out):
+        raise RuntimeError("out requires a gradient, which a call with out= has not")
+
+
 @functools.lru_cache(maxsize=1024)
 def _need(query, *sizes) -> int:
     """What a workspace query of the library says of these sizes and types."""
@@ -1053,6 +1059,7 @@ def _rows_out(logits, out):
     _, _, gap = _spaced_rows(out, "out", (logits.dtype,), logits.device)
     if out.shape != logits.shape:
         raise ValueError("out must have shape %s" % (tuple(logits.shape),))
+    _untracked_out(out)
     return out, gap, True
 
 
@@ -1124,6 +1131,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
         out = torch.empty_like(x, dtype=out_dtype)
     else:
         _places(out, _FLOATS if out_dtype is None else (out_dtype,), "out", dev, x.shape)
+        _untracked_out(out)
     mean = rstd = None
     if return_stats:
         mean, rstd = x.new_empty((2, *x.shape[:-1]), dtype=torch.float32).unbind()
@@ -1175,6 +1183,7 @@ def layer_norm_grad(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rst
         out = torch.empty_like(x)
     else:
         _places(out, (x.dtype,), "out", dev, x.shape)
+        _untracked_out(out)
     gw = gb = None
     if params:
         param_dtype = param_dtype or (torch.float32 if weight is None else weight.dtype)
