@@ -434,8 +434,9 @@ tgs_status tgs_token_logprobs(const void* logits, tgs_dtype dtype, int64_t T, in
  *   out       [T] rows of V of the logits' type, ld_out elements apart (what lies
  *             between rows is left as it is); the logits themselves with ld_out
  *             == ld included.
- * Rows of masked places, and rows of which every score is -inf, are +0.  The
- * workspace is a header (32 KB).
+ * Rows of masked places, and rows of which every score is -inf, are +0.  NaN or
+ * +inf in a row of any other place makes its gradient NaN.  The workspace is a
+ * header (32 KB).
  */
 tgs_status tgs_token_logprobs_grad(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
                                    const void* tokens, tgs_dtype tokens_dtype, float temperature, const float* stats,

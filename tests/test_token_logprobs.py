@@ -462,3 +462,32 @@ def test_shapes_and_binding_refusals(tgs_gpu):
                         (lambda: tgs_gpu.token_logprobs_grad(z, t, st, f, ws=torch.zeros(64, dtype=torch.uint8)), "ws is on cpu")):
         with pytest.raises((ValueError, TypeError), match=error):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V", [(6, 40), (6, 700), (6, 9000), (6, 70_001), (1030, 9000)])
+@pytest.mark.parametrize("dtype", FLOATS)
+def test_rows_of_nan_alone(tgs_gpu, dtype, T, V):
+    """Such a row's gradient is NaN as its loss is, and not the zeros of a row of -inf; by every route."""
+    logits = scores(T, V, dtype, 6)
+    tokens = make_tokens(logits, 0.0, torch.int64, 6)
+    top = min(V, 20)
+    g = torch.randn(T, generator=torch.Generator().manual_seed(3)).cuda()
+    want = tgs_gpu.token_logprobs(logits, tokens, top=top, entropy=True)
+    bad = logits.clone()
+    bad[1] = math.nan
+    bad[2], bad[2, V // 2] = -math.inf, math.nan
+    bad[4] = -math.inf
+    r = tgs_gpu.token_logprobs(bad, tokens, top=top, entropy=True)
+    for x in (r.logprobs, r.entropy, r.top_logprobs):
+        assert torch.isnan(x[1:3]).all()
+    assert r.top_indices[1].tolist() == list(range(top))
+    assert r.top_indices[2].tolist() == [V // 2] + [i for i in range(top) if i != V // 2][:top - 1]
+    keep = torch.tensor([0, 3] + list(range(5, T)), device="cuda")
+    for ge in (None, 0.1 * g):
+        grad = tgs_gpu.token_logprobs_grad(bad, tokens, r.stats, g, r.entropy, ge)
+        ok = tgs_gpu.token_logprobs_grad(logits, tokens, want.stats, g, want.entropy, ge)
+        assert torch.isnan(grad[1:3]).all() and (grad[4] == 0).all() and torch.equal(grad[keep], ok[keep])
+    leaf = bad.clone().requires_grad_()
+    (-tgs_gpu.token_logprobs(leaf, tokens).logprobs).sum().backward()
+    assert torch.isnan(leaf.grad[1:3]).all() and (leaf.grad[4] == 0).all()

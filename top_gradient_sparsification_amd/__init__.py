@@ -1292,7 +1292,8 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, stats: torch
     ``stats`` (and ``entropy``, with ``grad_entropy``) are what the forward pass
     left; either incoming gradient may be left out.  ``out`` may be the logits
     themselves, which are then overwritten.  Masked places, and rows of which
-    every score is -inf, give zeros.  It has no gradient itself."""
+    every score is -inf, give zeros; NaN or +inf in another row makes its gradient
+    NaN.  It has no gradient itself."""
     T, V, gap = _spaced_rows(logits, "logits", _FLOATS)
     dev = logits.device
     shape = logits.shape[:-1]

@@ -257,6 +257,11 @@ struct Coefficients {
   float a, b, h;
 };
 
+// Whether every score of a row is -inf: no distribution, gradient 0.  A maximum
+// passes NaN by, so a row of nothing else, or of NaN among -inf, has m = -inf too;
+// its sum, and so log s, is NaN, and its gradient with them.
+__device__ __forceinline__ bool no_scores(float m, float log_s) { return m == -kInf && log_s == log_s; }
+
 template <bool ENTROPY>
 __device__ __forceinline__ float slope(const Logits& z, const Coefficients& k, float x) {
   const float d = x - k.m;
@@ -357,7 +362,7 @@ __global__ __launch_bounds__(NT) void k_logprobs_grad(LogprobsGradArgs a) {
   Coefficients k;
   k.m = a.stats[2 * row];
   k.log_s = a.stats[2 * row + 1];
-  if (token < 0 || k.m == -kInf) {  // masked, or no score above -inf
+  if (token < 0 || no_scores(k.m, k.log_s)) {  // masked, or no score above -inf
     zero_row<T, NT>(out, c0, c1, a.streaming);
     return;
   }
