@@ -476,7 +476,8 @@ tgs_status tgs_distillation_loss(const void* logits, tgs_dtype dtype, int64_t T,
  * sums the slots that name a token.
  *   grad_loss [T] float; stats as tgs_distillation_loss left them.
  *   out, ld_out  as tgs_token_logprobs_grad, the logits themselves included.
- * Rows of which every score is -inf are +0.  The workspace is a header (32 KB).
+ * Rows of which every score is -inf are +0; those of NaN, alone or among -inf, are
+ * NaN, from this call and from the one below.  The workspace is a header (32 KB).
  */
 tgs_status tgs_distillation_grad(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
                                  const void* indices, tgs_dtype indices_dtype, const void* teacher,

@@ -403,3 +403,36 @@ def test_shapes_and_binding_refusals(tgs_gpu):
                          (lambda: tgs_gpu.distillation_loss(z, i, t, ws=torch.zeros(64, dtype=torch.uint8, device="cuda")), "need")):
         with pytest.raises((ValueError, TypeError, MemoryError), match=error):
             call_()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V", [(6, 60), (6, 4000), (6, 70_001), (1030, 4000)])
+@pytest.mark.parametrize("dtype", FLOATS)
+def test_rows_of_nan_alone(tgs_gpu, dtype, T, V):
+    """Such a row's gradient is NaN as its loss is, and not the zeros of a row of -inf: from the
+    separate calls and from the one that makes both, in one workgroup and in slices."""
+    logits = scores(T, V, dtype, 4)
+    indices, teacher = make_teacher(logits, 12, torch.float32, torch.int64, 4, empty=0.3, masked=0.0)
+    bad = logits.clone()
+    bad[1] = math.nan
+    bad[2], bad[2, V // 2] = -math.inf, math.nan
+    bad[4] = -math.inf
+    indices[5], bad[5] = -1, math.nan            # masked: nothing of it is needed
+    want, stats = tgs_gpu.distillation_loss(logits, indices, teacher, return_stats=True)
+    ok = tgs_gpu.distillation_grad(logits, indices, teacher, stats, torch.ones_like(want))
+    loss, stats = tgs_gpu.distillation_loss(bad, indices, teacher, return_stats=True)
+    grad = tgs_gpu.distillation_grad(bad, indices, teacher, stats, torch.ones_like(loss))
+    both, step = tgs_gpu.distillation_loss_and_grad(bad, indices, teacher)
+    keep = torch.tensor([0, 3, 5] + list(range(6, T)), device="cuda")
+    for x in (loss, both, grad, step):
+        assert torch.isnan(x[1:3]).all()
+    assert loss[4] == math.inf and both[4] == math.inf and loss[5] == 0 and both[5] == 0
+    assert (grad[4:6] == 0).all() and (step[4:6] == 0).all()
+    assert torch.equal(loss[keep], want[keep]) and torch.equal(grad[keep], ok[keep])
+    teacher[4, 0], indices[4, 0] = math.nan, 1   # a teacher's NaN goes to such a row too
+    loss, stats = tgs_gpu.distillation_loss(bad, indices, teacher, return_stats=True)
+    grad = tgs_gpu.distillation_grad(bad, indices, teacher, stats, torch.ones_like(loss))
+    both, step = tgs_gpu.distillation_loss_and_grad(bad, indices, teacher)
+    for x in (loss, both, grad, step):
+        assert torch.isnan(x[4]).all()
+    assert torch.equal(loss[keep], want[keep]) and torch.equal(grad[keep], ok[keep])

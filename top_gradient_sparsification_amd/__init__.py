@@ -1405,7 +1405,8 @@ def distillation_grad(logits: torch.Tensor, teacher_indices: torch.Tensor, teach
 
     ``stats`` are what the forward pass left.  ``out`` may be the logits
     themselves, which are then overwritten.  Masked places, and rows of which
-    every score is -inf, give zeros.  It has no gradient itself."""
+    every score is -inf, give zeros; NaN or +inf in another row's logits or
+    teacher makes its gradient NaN.  It has no gradient itself."""
     T, V, gap, K = _slots(logits, teacher_indices, teacher_logits)
     dev = logits.device
     _places(stats, (torch.float32,), "stats", dev, (*logits.shape[:-1], 2))

@@ -533,6 +533,12 @@ __device__ __forceinline__ Coefficients distill_coefficients(const DistillArgs& 
   return Coefficients{m, log_s, log_s * kLog2e, 0.0f, fmaf(0.0f, s.q[0], g * a.z.inv), 0.0f};
 }
 
+// Whether a row's gradient is 0 because its logits have no distribution; not where
+// its teacher's q are NaN.
+__device__ __forceinline__ bool no_gradient(float m, float log_s, const Slots& s) {
+  return no_scores(m, log_s) && s.q[0] == s.q[0];
+}
+
 // out = (p - q) b for columns [c0, c1) of a row.
 template <class T, int NT, bool KEPT>
 __device__ __forceinline__ void write_distill_grad(const DistillArgs& a, const T* z, T* out, u32 c0, u32 c1,
@@ -585,7 +591,7 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
   const float log_s = r.s == 0.0f ? 0.0f : logf(r.s);
   write_loss(a, row, slots_loss<NT>(a, r, log_s, s), r.m, log_s);
   if constexpr (GRAD) {
-    if (r.s == 0.0f) zero_row<T, NT>(out, 0, a.z.V, a.streaming);
+    if (no_gradient(r.m, log_s, s)) zero_row<T, NT>(out, 0, a.z.V, a.streaming);
     else write_distill_grad<T, NT, KEEP>(a, z, out, 0, a.z.V, distill_coefficients(a, row, r.m, log_s, s), s, s_kept);
   }
 }
@@ -627,7 +633,8 @@ __global__ __launch_bounds__(NT) void k_distill_grad(DistillArgs a) {
   T* out = (T*)a.out + row * a.ld_out;
   const T* z = (const T*)a.z.p + row * a.z.ld;
   const float m = a.stats[2 * row], log_s = a.stats[2 * row + 1];
-  if (!load_slots<T, NT, false, true>(a, row, z, out, c0, c1, s) || m == -kInf) zero_row<T, NT>(out, c0, c1, a.streaming);
+  if (!load_slots<T, NT, false, true>(a, row, z, out, c0, c1, s) || no_gradient(m, log_s, s))
+    zero_row<T, NT>(out, c0, c1, a.streaming);
   else write_distill_grad<T, NT, false>(a, z, out, c0, c1, distill_coefficients(a, row, m, log_s, s), s, nullptr);
 }
 
