@@ -36,6 +36,8 @@ Operators of the training step around it:
 * ``distillation_loss`` / ``distillation_grad`` / ``distillation_loss_and_grad``
   -- KL divergence from a teacher's top logits, its gradient, and both at once.
 
+Gradients are reverse-mode; a tensor with a forward-mode tangent is refused.
+
 There is no fallback: if ``libtgs.so`` is missing or cannot be loaded, every
 call raises.
 """
@@ -49,6 +51,7 @@ from typing import NamedTuple
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtgs.so")
@@ -698,9 +701,17 @@ _FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 _TOKENS = (torch.int32, torch.int64)
 
 
+def _no_tangent(t, name):
+    """Refuses a dual tensor: the result of a call that autograd cannot see has no tangent, which reads as a zero one."""
+    if forward_ad.unpack_dual(t).tangent is not None:
+        raise NotImplementedError("%s has a tangent, and the call no forward-mode derivative" % name)
+
+
 def _require_any(t, dtypes, name, device=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
+    if forward_ad._current_level >= 0:  # a level of forward mode is open
+        _no_tangent(t, name)
     if t.dtype not in dtypes:
         raise TypeError("%s must be one of %s, got %s" % (name, ", ".join(map(str, dtypes)), t.dtype))
     if not t.is_cuda:
@@ -1017,6 +1028,8 @@ def _spaced_rows(t, name, dtypes, device=None):
     """(rows, columns, elements from row to row) of ``[..., V]``, whose rows may lie further apart than they are long."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
+    if forward_ad._current_level >= 0:  # a level of forward mode is open
+        _no_tangent(t, name)
     if t.dtype not in dtypes:
         raise TypeError("%s must be one of %s, got %s" % (name, ", ".join(map(str, dtypes)), t.dtype))
     if not t.is_cuda:
