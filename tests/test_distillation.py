@@ -436,3 +436,18 @@ def test_rows_of_nan_alone(tgs_gpu, dtype, T, V):
     for x in (loss, both, grad, step):
         assert torch.isnan(x[4]).all()
     assert torch.equal(loss[keep], want[keep]) and torch.equal(grad[keep], ok[keep])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V", [(3, 50), (3, 70_001), (1030, 9000)])
+def test_scores_further_apart_than_the_type_reaches(tgs_gpu, T, V):
+    """x - m is no fp32 number, (x - m) / temperature is one."""
+    for dtype in (torch.float32, torch.bfloat16):
+        low = torch.finfo(dtype).min
+        logits = scores(T, V, dtype, 3).clone()
+        indices, teacher = make_teacher(logits, 5, torch.float32, torch.int32, 3, masked=0.0)
+        logits[0, 7], logits[0, 9] = low, -low
+        indices[0, 0], teacher[0, 0] = 7, 3.0
+        for tau in (2.5, 1e6):
+            loss = check(tgs_gpu, logits, indices, teacher, tau)[0]
+            assert torch.isfinite(loss[0]) and loss[0] > 1e31

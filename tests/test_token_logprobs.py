@@ -491,3 +491,19 @@ def test_rows_of_nan_alone(tgs_gpu, dtype, T, V):
     leaf = bad.clone().requires_grad_()
     (-tgs_gpu.token_logprobs(leaf, tokens).logprobs).sum().backward()
     assert torch.isnan(leaf.grad[1:3]).all() and (leaf.grad[4] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V", [(3, 50), (3, 30_000), (1030, 9000)])
+def test_scores_further_apart_than_the_type_reaches(tgs_gpu, T, V):
+    """x - m is no fp32 number, (x - m) / temperature is one."""
+    for dtype in (torch.float32, torch.bfloat16):
+        logits = scores(T, V, dtype, 3).clone()
+        logits[0, 7], logits[0, 9] = LOWEST[dtype], -LOWEST[dtype]
+        logits[1, 1], logits[1, 2:] = -LOWEST[dtype], LOWEST[dtype]
+        tokens = make_tokens(logits, 0.0, torch.int32, 3)
+        tokens[0], tokens[1] = 7, 5
+        for tau in (2.5, 1e6):
+            r = check_forward(tgs_gpu, logits, tokens, tau, min(V, 10))
+            check_backward(tgs_gpu, logits, tokens, r, tau)
+            assert torch.isfinite(r.logprobs[:2]).all() and (r.logprobs[:2] < -1e32).all()

@@ -116,8 +116,10 @@ struct LogprobsArgs {
   bool wide;  // 64-bit tokens
 };
 
+// The difference is taken of halves, with the same bits: of scores at either end of
+// the type it is no fp32 number, over the temperature it may be one.
 __device__ __forceinline__ float log_probability(const Logits& z, float x, const RowSums& r, float log_s) {
-  return r.s == 0.0f ? -kInf : (x - r.m) * z.inv - log_s;
+  return r.s == 0.0f ? -kInf : fmaf(0.5f, x, -0.5f * r.m) * (2.0f * z.inv) - log_s;
 }
 
 // One row's results from its sums, by any number of threads.
@@ -520,7 +522,7 @@ __device__ __forceinline__ float slots_loss(const DistillArgs& a, const RowSums&
   float sum[1] = {0.0f};
   for (u32 i = threadIdx.x; i < a.K; i += NT) {
     const float q = s.q[i];
-    if (!(q == 0.0f)) sum[0] = fmaf(q, s.lq[i] - (r.s == 0.0f ? -kInf : (s.x[i] - r.m) * a.z.inv - log_s), sum[0]);
+    if (!(q == 0.0f)) sum[0] = fmaf(q, s.lq[i] - log_probability(a.z, s.x[i], r, log_s), sum[0]);
   }
   group_reduce<Sum, NT>(sum, s.red[3]);
   return sum[0];
