@@ -368,9 +368,10 @@ tgs_status tgs_muon_step(void* weight, tgs_dtype weight_dtype, const void* grad,
  *   weight, bias  [D] of one type, fp32, bf16 or fp16; either may be null (1, 0).
  *   mean, rstd    [T] float, out, for the gradients; either may be null.
  * 0 <= T <= 2^31 - 1, 1 <= D <= 2^24, eps >= 0.  The mean is known before the
- * squares are summed, so a large mean costs no more than x's own rounding; rows
- * whose squares pass fp32's range are normed too.  A row's NaN or infinity makes the
- * whole row NaN.
+ * squares are summed, and where the values lie flat around it (within a 256th of
+ * it) the roundings of its sum are taken off: a large mean costs no more than x's
+ * own rounding, and a row of one value gives the bias.  Rows whose sum or squares
+ * pass fp32's range are normed too.  A row's NaN or infinity makes the whole row NaN.
  */
 tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T, int64_t D, const void* weight, const void* bias,
                           tgs_dtype weight_dtype, float eps, void* out, tgs_dtype out_dtype, float* mean, float* rstd,

@@ -388,3 +388,30 @@ def test_tolerances_are_tight():
     with pytest.raises(AssertionError):
         assert_close(coarse, y, tol)
     assert half_step(torch.float32) == U and tiny(torch.float32) == 2.0**-150
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [7, 64, 130, 1001, 5000, 16384, 20_001, 300_001, 1 << 20, 1 << 24])
+def test_rows_of_one_value(tgs_gpu, D):
+    """y = bias, whatever the value and however many of it are summed.
+
+    The mean is the value itself: the first one is off by k roundings at most (k < 700 for D = 2^24), each value's
+    distance to it is exact, and those distances' mean, off by 650 U of itself at most, brings it within 0.03 of
+    a step of the value."""
+    w, b = params(D, torch.float32, 2)
+    other = make(1, D, torch.float32, 3)
+    for dtype in (torch.float32, torch.bfloat16):
+        alone = tgs_gpu.layer_norm(other.to(dtype), w, b)
+        for value in (0.0, 0.1, 1000.1, -3.3e-21, 7e15, 2e38, torch.finfo(dtype).min):
+            for eps in (1e-5, 2.0**-125):
+                x = torch.full((3, D), value, device="cuda")
+                x[1] = other
+                x = x.to(dtype)
+                y, mean, rstd = tgs_gpu.layer_norm(x, w, b, eps=eps, out_dtype=torch.float32, return_stats=True)
+                assert torch.equal(y[::2], b.expand(2, D)), (value, eps)
+                assert torch.equal(mean[::2], x[::2, 0].float()), (value, eps)
+                # the root and the division, and eps itself as a float
+                want = torch.full((2,), eps**-0.5, dtype=torch.float64)
+                assert_close(rstd[::2], want, 3 * U * want, "rstd")
+                if eps == 1e-5:
+                    assert torch.equal(tgs_gpu.layer_norm(x, w, b)[1], alone[0])

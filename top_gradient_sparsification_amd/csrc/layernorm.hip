@@ -31,9 +31,28 @@ struct NormArgs {
   bool streaming;
 };
 
-// Where the sum of squares passes fp32's range it is taken of values smaller by
-// this, beside which eps is nothing.
+// Where the sum of squares passes fp32's range it is taken of values smaller by this.
 constexpr float kShrink = 0x1p-80f;
+// A row's values lie flat where the squares of their distances to the mean sum up to
+// no more than they would at a 256th of the mean each.  The roundings of the mean's own
+// sum, up to about 20 (more in a long row), would stand out beside such distances: they
+// are taken off by the mean of the distances, each of which is exact.
+constexpr float kFlat = 0x1p-8f;
+__device__ __forceinline__ bool lies_flat(float mean, float squares, float D) {
+  const float m = mean * kFlat;
+  return mean != 0.0f && squares <= m * m * D;
+}
+
+// What a row is normed by: out = (x scale - mean) rstd.
+struct Moments {
+  float mean, rstd, scale;
+};
+// From the sum of the squares of x scale - mean.  Of a row of one value the
+// variance is eps alone.
+__device__ __forceinline__ Moments moments(float mean, float squares, float scale, float D, float eps) {
+  if (squares == 0.0f) return Moments{mean / scale, 1.0f / sqrtf(eps), 1.0f};
+  return Moments{mean, 1.0f / sqrtf(squares / D + eps * scale * scale), scale};
+}
 
 constexpr int norm_threads(int L) { return L > 256 ? L : 256; }
 
@@ -93,7 +112,7 @@ __device__ __forceinline__ void lane_params(const Place<E, L>& at, const void* p
 template <class TX, class TY, int E, int L, int NV>
 __global__ __launch_bounds__(norm_threads(L)) void k_norm(NormArgs a) {
   constexpr int NT = norm_threads(L);
-  __shared__ float s_red[2][L > kWave ? L / kWave : 1];
+  __shared__ float s_red[4][L > kWave ? L / kWave : 1];
   const Place<E, L> at{a.D, threadIdx.x % L};
   const float D = (float)a.D;
   float w[NV][E], b[NV][E];
@@ -107,48 +126,54 @@ __global__ __launch_bounds__(norm_threads(L)) void k_norm(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (at.inside(i)) raw[i] = load_vec<TX, E>(x + at.at(i));
-    float sum[1] = {0.0f}, squares[1] = {0.0f};
+    float scale = 1.0f, mean = 0.0f, sum[1], squares[1];
+    // of x scale - mean
+    const auto add_up = [&](float* lds) {
+      sum[0] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float part = 0.0f;
-      at.each(i, [&](int e, bool counts) { part += counts ? to_f32(raw[i].v[e]) : 0.0f; });
-      sum[0] += part;
-    }
-    group_reduce<Sum, L>(sum, s_red[0]);
-    float mean = sum[0] / D, shrink = 1.0f;
-    forget(raw);
+      for (int i = 0; i < NV; ++i) {
+        float part = 0.0f;
+        at.each(i, [&](int e, bool counts) { part += counts ? fmaf(to_f32(raw[i].v[e]), scale, -mean) : 0.0f; });
+        sum[0] += part;
+      }
+      group_reduce<Sum, L>(sum, lds);
+    };
     const auto add_squares = [&] {
       squares[0] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float part = 0.0f;
         at.each(i, [&](int e, bool counts) {
-          const float d = counts ? fmaf(to_f32(raw[i].v[e]), shrink, -mean) : 0.0f;
+          const float d = counts ? fmaf(to_f32(raw[i].v[e]), scale, -mean) : 0.0f;
           part = fmaf(d, d, part);
         });
         squares[0] += part;
       }
       group_reduce<Sum, L>(squares, s_red[1]);
     };
+    add_up(s_red[0]);
+    mean = sum[0] / D;
+    forget(raw);
     add_squares();
-    float rstd = 1.0f / sqrtf(squares[0] / D + a.eps);
-    const bool far = !(squares[0] < __builtin_huge_valf());
-    if (__any(far)) {  // the same for a whole workgroup where a row is one
-      if (far) shrink = kShrink;
-      sum[0] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        at.each(i, [&](int e, bool counts) { sum[0] += counts ? to_f32(raw[i].v[e]) * shrink : 0.0f; });
-      group_reduce<Sum, L>(sum, s_red[0]);
-      if (far) mean = sum[0] / D;
+    const bool far = !(squares[0] < __builtin_huge_valf()), flat = lies_flat(mean, squares[0], D);
+    if (__any(far || flat)) {  // the same for a whole workgroup where a row is one
+      const float before = mean;
+      if (far) scale = kShrink;
+      mean = 0.0f;
+#pragma unroll 1
+      for (int turn = 0; turn < 2; ++turn) {
+        add_up(s_red[2 + turn]);
+        mean += sum[0] / D;
+      }
+      if (!(far || flat)) mean = before;
       add_squares();
-      if (far) rstd = 1.0f / sqrtf(squares[0] / D);
     }
+    const Moments m = moments(mean, squares[0], scale, D, a.eps);
     forget(raw);
     if (real) {
       if (at.t == 0) {
-        if (a.mean) a.mean[row] = mean / shrink;
-        if (a.rstd) a.rstd[row] = rstd * shrink;
+        if (a.mean) a.mean[row] = m.mean / m.scale;
+        if (a.rstd) a.rstd[row] = m.rstd * m.scale;
       }
       TY* out = (TY*)a.out + row * (int64_t)a.D;
 #pragma unroll
@@ -156,7 +181,7 @@ __global__ __launch_bounds__(norm_threads(L)) void k_norm(NormArgs a) {
         if (!at.inside(i)) continue;
         float y[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = fmaf(fmaf(to_f32(raw[i].v[e]), shrink, -mean) * rstd, w[i][e], b[i][e]);
+        for (int e = 0; e < E; ++e) y[e] = fmaf(fmaf(to_f32(raw[i].v[e]), m.scale, -m.mean) * m.rstd, w[i][e], b[i][e]);
         const Vec<TY, E> r = round_vec<TY, E>(y);
         if (a.streaming) store_vec_streaming<TY, E>(out + at.at(i), r);
         else store_vec<TY, E>(out + at.at(i), r);
@@ -180,68 +205,76 @@ __device__ __forceinline__ void in_row(u32 c, u32 n, F&& f) {
 
 constexpr int kLongThreads = 1024;
 
-// Rows longer than registers hold: read three times, twice from the caches.
+// Rows longer than registers hold: read three times, twice from the caches.  The
+// distances to the first mean are summed beside their squares, since its sum takes
+// up to D / 4,096 additions a thread.
 // out may be x: a thread writes what it alone reads.
 template <class TX, class TY, int E>
 __global__ __launch_bounds__(kLongThreads) void k_norm_long(NormArgs a) {
-  __shared__ float s_red[2][kLongThreads / kWave];
+  __shared__ float s_red[2][2 * (kLongThreads / kWave)];
   const int64_t row = a.row0 + blockIdx.x;
-  const u32 D = a.D;
-  const TX* x = (const TX*)a.x + row * (int64_t)D;
-  float sum[1] = {0.0f}, squares[1] = {0.0f};
-  for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
-    const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+  const u32 n = a.D;
+  const float D = (float)n;
+  const TX* x = (const TX*)a.x + row * (int64_t)n;
+  float scale = 1.0f, mean = 0.0f, sum[2];
+  // of x scale - mean, and of its square
+  const auto add_up = [&](float* lds) {
+    sum[0] = sum[1] = 0.0f;
+    for (u32 c = threadIdx.x * E; c < n; c += kLongThreads * E) {
+      const Vec<TX, E> raw = load_part<TX, E>(x, c, n, from_f32<TX>(0.0f));
+      float p0 = 0.0f, p1 = 0.0f;
+      in_row<E>(c, n, [&](int e) {
+        const float d = fmaf(to_f32(raw.v[e]), scale, -mean);
+        p0 += d;
+        p1 = fmaf(d, d, p1);
+      });
+      sum[0] += p0;
+      sum[1] += p1;
+    }
+    group_reduce<Sum, kLongThreads>(sum, lds);
+  };
+  float first[1] = {0.0f};
+  for (u32 c = threadIdx.x * E; c < n; c += kLongThreads * E) {
+    const Vec<TX, E> raw = load_part<TX, E>(x, c, n, from_f32<TX>(0.0f));
     float part = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) part += to_f32(raw.v[e]);
-    sum[0] += part;
+    first[0] += part;
   }
-  group_reduce<Sum, kLongThreads>(sum, s_red[0]);
-  float mean = sum[0] / (float)D;
-  for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
-    const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
-    float part = 0.0f;
-    in_row<E>(c, D, [&](int e) {
-      const float d = to_f32(raw.v[e]) - mean;
-      part = fmaf(d, d, part);
-    });
-    squares[0] += part;
-  }
-  group_reduce<Sum, kLongThreads>(squares, s_red[1]);
-  float rstd = 1.0f / sqrtf(squares[0] / (float)D + a.eps), shrink = 1.0f;
-  if (!(squares[0] < __builtin_huge_valf())) {
-    float again[1] = {0.0f};
-    for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
-      const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
-      in_row<E>(c, D, [&](int e) { again[0] += to_f32(raw.v[e]) * kShrink; });
+  group_reduce<Sum, kLongThreads>(first, s_red[0]);
+  mean = first[0] / D;
+  add_up(s_red[1]);
+  float off = sum[0] / D, squares = fmaf(-off * off, D, sum[1]);
+  mean += off;
+  const bool far = !(sum[1] < __builtin_huge_valf());
+  // the same for the whole workgroup: little is left of the squares without the first mean's error
+  if (far || (off != 0.0f && !(squares > 0.5f * sum[1]))) {
+    if (far) {
+      scale = kShrink;
+      mean = 0.0f;
     }
-    group_reduce<Sum, kLongThreads>(again, s_red[0]);
-    mean = again[0] / (float)D;
-    again[0] = 0.0f;
-    for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
-      const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
-      in_row<E>(c, D, [&](int e) {
-        const float d = to_f32(raw.v[e]) * kShrink - mean;
-        again[0] = fmaf(d, d, again[0]);
-      });
+    // a mean of smaller values takes two passes more
+#pragma unroll 1
+    for (int turn = far ? 0 : 2; turn < 3; ++turn) {
+      add_up(s_red[turn % 2]);
+      if (turn < 2) mean += sum[0] / D;
     }
-    group_reduce<Sum, kLongThreads>(again, s_red[1]);
-    rstd = 1.0f / sqrtf(again[0] / (float)D);
-    shrink = kShrink;
+    squares = sum[1];
   }
+  const Moments m = moments(mean, squares, scale, D, a.eps);
   if (threadIdx.x == 0) {
-    if (a.mean) a.mean[row] = mean / shrink;
-    if (a.rstd) a.rstd[row] = rstd * shrink;
+    if (a.mean) a.mean[row] = m.mean / m.scale;
+    if (a.rstd) a.rstd[row] = m.rstd * m.scale;
   }
-  TY* out = (TY*)a.out + row * (int64_t)D;
-  for (u32 c = threadIdx.x * E; c < D; c += kLongThreads * E) {
-    const Vec<TX, E> raw = load_part<TX, E>(x, c, D, from_f32<TX>(0.0f));
+  TY* out = (TY*)a.out + row * (int64_t)n;
+  for (u32 c = threadIdx.x * E; c < n; c += kLongThreads * E) {
+    const Vec<TX, E> raw = load_part<TX, E>(x, c, n, from_f32<TX>(0.0f));
     float w[E], b[E], y[E];
-    load_params<E>(a.weight, a.weight_dtype, c, D, 1.0f, w);
-    load_params<E>(a.bias, a.weight_dtype, c, D, 0.0f, b);
+    load_params<E>(a.weight, a.weight_dtype, c, n, 1.0f, w);
+    load_params<E>(a.bias, a.weight_dtype, c, n, 0.0f, b);
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = fmaf((to_f32(raw.v[e]) * shrink - mean) * rstd, w[e], b[e]);
-    store_part<TY, E>(out, c, D, round_vec<TY, E>(y), a.streaming);
+    for (int e = 0; e < E; ++e) y[e] = fmaf(fmaf(to_f32(raw.v[e]), m.scale, -m.mean) * m.rstd, w[e], b[e]);
+    store_part<TY, E>(out, c, n, round_vec<TY, E>(y), a.streaming);
   }
 }
 
