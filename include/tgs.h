@@ -371,7 +371,8 @@ tgs_status tgs_muon_step(void* weight, tgs_dtype weight_dtype, const void* grad,
  * squares are summed, and where the values lie flat around it (within a 256th of
  * it) the roundings of its sum are taken off: a large mean costs no more than x's
  * own rounding, and a row of one value gives the bias.  Rows whose sum or squares
- * pass fp32's range are normed too.  A row's NaN or infinity makes the whole row NaN.
+ * pass fp32's range, or fall below it beside as small an eps, are normed too.  A
+ * row's NaN or infinity makes the whole row NaN.
  */
 tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T, int64_t D, const void* weight, const void* bias,
                           tgs_dtype weight_dtype, float eps, void* out, tgs_dtype out_dtype, float* mean, float* rstd,

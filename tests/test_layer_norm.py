@@ -415,3 +415,19 @@ def test_rows_of_one_value(tgs_gpu, D):
                 assert_close(rstd[::2], want, 3 * U * want, "rstd")
                 if eps == 1e-5:
                     assert torch.equal(tgs_gpu.layer_norm(x, w, b)[1], alone[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [7, 64, 130, 1001, 5000, 20000, 33000])
+def test_rows_whose_squares_fall_below_the_range(tgs_gpu, D, dtype):
+    """Without an eps, or with one as small, rows of the smallest values are normed like any other."""
+    w, b = params(D, torch.float32, 2)
+    for size in (1e-15, 1e-18, 1e-22, 1e-25, 1e-30, 1e-37):
+        x = size * make(9, D, torch.float32, D)
+        x[1:4] = make(3, D, torch.float32, 5)          # beside rows of ordinary ones
+        check(tgs_gpu, x.to(dtype), w, b, eps=0.0)
+        check(tgs_gpu, x.to(dtype), w, b, eps=2.0**-125)
+    x = (1e-41 * make(3, D, torch.float32, D).cpu()).cuda()  # rstd is no fp32 number, the results are
+    want, tol, _, _ = exact_norm(x, w, b, 0.0)
+    assert_close(tgs_gpu.layer_norm(x, w, b, eps=0.0), want, tol + rounded(want, torch.float32), "y")

@@ -33,14 +33,22 @@ struct NormArgs {
 
 // Where the sum of squares passes fp32's range it is taken of values smaller by this.
 constexpr float kShrink = 0x1p-80f;
+// Where it falls below, down to where squares are lost or keep few bits, and eps does
+// not outweigh it, it is taken of values larger by this.  The mean is small then too:
+// values of 2^-20 and more are either equal or 2^-45 apart, with squares of 2^-90.
+constexpr float kGrow = 0x1p100f, kFaint = 0x1p-96f, kFaintEps = 0x1p-100f, kFaintMean = 0x1p-20f;
+__device__ __forceinline__ bool is_faint(float mean, float squares, float eps) {
+  return squares < kFaint && eps < kFaintEps && fabsf(mean) < kFaintMean;
+}
 // A row's values lie flat where the squares of their distances to the mean sum up to
 // no more than they would at a 256th of the mean each.  The roundings of the mean's own
 // sum, up to about 20 (more in a long row), would stand out beside such distances: they
 // are taken off by the mean of the distances, each of which is exact.
 constexpr float kFlat = 0x1p-8f;
-__device__ __forceinline__ bool lies_flat(float mean, float squares, float D) {
+// The squares' sum that a row has to exceed, to be neither flat nor faint.
+__device__ __forceinline__ float least_squares(float mean, float D, float eps) {
   const float m = mean * kFlat;
-  return mean != 0.0f && squares <= m * m * D;
+  return fmaxf(m * m * D, eps < kFaintEps ? kFaint : 0.0f);
 }
 
 // What a row is normed by: out = (x scale - mean) rstd.
@@ -108,9 +116,11 @@ __device__ __forceinline__ void lane_params(const Place<E, L>& at, const void* p
 }
 
 // A row in L lanes of NV vectors of E elements each; a workgroup takes every
-// gridDim.x-th set of rows and keeps its columns' parameters in registers.
+// gridDim.x-th set of rows and keeps its columns' parameters in registers.  Of 16
+// lanes a row the compiler is held to six waves a SIMD, where it would take two
+// registers too many for them (200,000 rows of 100 in bf16 24.4 us with five waves).
 template <class TX, class TY, int E, int L, int NV>
-__global__ __launch_bounds__(norm_threads(L)) void k_norm(NormArgs a) {
+__global__ __launch_bounds__(norm_threads(L), L == 16 ? 6 : 1) void k_norm(NormArgs a) {
   constexpr int NT = norm_threads(L);
   __shared__ float s_red[4][L > kWave ? L / kWave : 1];
   const Place<E, L> at{a.D, threadIdx.x % L};
@@ -155,25 +165,33 @@ __global__ __launch_bounds__(norm_threads(L)) void k_norm(NormArgs a) {
     mean = sum[0] / D;
     forget(raw);
     add_squares();
-    const bool far = !(squares[0] < __builtin_huge_valf()), flat = lies_flat(mean, squares[0], D);
-    if (__any(far || flat)) {  // the same for a whole workgroup where a row is one
-      const float before = mean;
-      if (far) scale = kShrink;
-      mean = 0.0f;
+    float rstd = 1.0f / sqrtf(squares[0] / D + a.eps);
+    if (__any(!(squares[0] > least_squares(mean, D, a.eps) && squares[0] < __builtin_huge_valf()))) {
+      // the same for a whole workgroup where a row is one
+      const bool far = !(squares[0] < __builtin_huge_valf()), faint = is_faint(mean, squares[0], a.eps);
+      const bool again = far || faint || (mean != 0.0f && squares[0] <= least_squares(mean, D, a.eps));
+      if (__any(again)) {
+        const float before = mean;
+        if (far) scale = kShrink;
+        if (faint) scale = kGrow;
+        mean = 0.0f;
 #pragma unroll 1
-      for (int turn = 0; turn < 2; ++turn) {
-        add_up(s_red[2 + turn]);
-        mean += sum[0] / D;
+        for (int turn = 0; turn < 2; ++turn) {
+          add_up(s_red[2 + turn]);
+          mean += sum[0] / D;
+        }
+        add_squares();
+        const Moments m = moments(mean, squares[0], scale, D, a.eps);
+        mean = again ? m.mean : before;
+        rstd = again ? m.rstd : rstd;
+        scale = m.scale;
       }
-      if (!(far || flat)) mean = before;
-      add_squares();
     }
-    const Moments m = moments(mean, squares[0], scale, D, a.eps);
     forget(raw);
     if (real) {
       if (at.t == 0) {
-        if (a.mean) a.mean[row] = m.mean / m.scale;
-        if (a.rstd) a.rstd[row] = m.rstd * m.scale;
+        if (a.mean) a.mean[row] = mean / scale;
+        if (a.rstd) a.rstd[row] = rstd * scale;
       }
       TY* out = (TY*)a.out + row * (int64_t)a.D;
 #pragma unroll
@@ -181,7 +199,7 @@ __global__ __launch_bounds__(norm_threads(L)) void k_norm(NormArgs a) {
         if (!at.inside(i)) continue;
         float y[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = fmaf(fmaf(to_f32(raw[i].v[e]), m.scale, -m.mean) * m.rstd, w[i][e], b[i][e]);
+        for (int e = 0; e < E; ++e) y[e] = fmaf(fmaf(to_f32(raw[i].v[e]), scale, -mean) * rstd, w[i][e], b[i][e]);
         const Vec<TY, E> r = round_vec<TY, E>(y);
         if (a.streaming) store_vec_streaming<TY, E>(out + at.at(i), r);
         else store_vec<TY, E>(out + at.at(i), r);
@@ -246,16 +264,16 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(NormArgs a) {
   add_up(s_red[1]);
   float off = sum[0] / D, squares = fmaf(-off * off, D, sum[1]);
   mean += off;
-  const bool far = !(sum[1] < __builtin_huge_valf());
+  const bool far = !(sum[1] < __builtin_huge_valf()), faint = is_faint(mean, sum[1], a.eps);
   // the same for the whole workgroup: little is left of the squares without the first mean's error
-  if (far || (off != 0.0f && !(squares > 0.5f * sum[1]))) {
-    if (far) {
-      scale = kShrink;
+  if (far || faint || (off != 0.0f && !(squares > 0.5f * sum[1]))) {
+    if (far || faint) {
+      scale = far ? kShrink : kGrow;
       mean = 0.0f;
     }
-    // a mean of smaller values takes two passes more
+    // a mean of other values takes two passes more
 #pragma unroll 1
-    for (int turn = far ? 0 : 2; turn < 3; ++turn) {
+    for (int turn = far || faint ? 0 : 2; turn < 3; ++turn) {
       add_up(s_red[turn % 2]);
       if (turn < 2) mean += sum[0] / D;
     }
