@@ -391,7 +391,7 @@ size_t tgs_layer_norm_grad_workspace_bytes(int64_t T, int64_t D);
  *   grad_x    [T][D] of x's type; x itself, or grad where the types agree, included.
  *   grad_weight, grad_bias  [D] of param_dtype; either may be null.
  * The sums over rows are fp32, in an order that depends on the sizes and types
- * alone: equal inputs give equal bits.
+ * alone: equal inputs give equal bits.  x - mean need be no fp32 number.
  */
 tgs_status tgs_layer_norm_grad(const void* grad, tgs_dtype grad_dtype, const void* x, tgs_dtype x_dtype, int64_t T,
                                int64_t D, const float* mean, const float* rstd, const void* weight,

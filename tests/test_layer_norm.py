@@ -431,3 +431,13 @@ def test_rows_whose_squares_fall_below_the_range(tgs_gpu, D, dtype):
     x = (1e-41 * make(3, D, torch.float32, D).cpu()).cuda()  # rstd is no fp32 number, the results are
     want, tol, _, _ = exact_norm(x, w, b, 0.0)
     assert_close(tgs_gpu.layer_norm(x, w, b, eps=0.0), want, tol + rounded(want, torch.float32), "y")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [7, 130, 1001, 5000, 33000])
+def test_gradients_of_rows_wider_than_the_type(tgs_gpu, D, dtype):
+    """x - mean is no fp32 number, (x - mean) rstd is one."""
+    x = make(9, D, torch.float32, D)
+    x[2:7] = torch.where(x[2:7] > 0.9, 3.2e38, -3.2e38)
+    check(tgs_gpu, x.to(dtype), *params(D, torch.float32, 3))
