@@ -558,12 +558,11 @@ constexpr int64_t kMostHeld = 4096;
 template <int E>
 constexpr int64_t kMostHeldBack = E == 4 ? 4096 : 2048;
 
-
 // Elements of a vector, lanes of a row and vectors a lane for rows of D: the
 // smallest that holds them.  Calls f(E, L, NV) as integral constants; false where
 // none does.
-template <int E, class F>
-static bool with_shape(int64_t D, int64_t most, F&& f) {
+template <int E, int64_t MOST, class F>
+static bool with_shape(int64_t D, F&& f) {
   const int64_t vectors = (D + E - 1) / E;
   const auto call = [&](auto e, auto l, auto nv) { f(e, l, nv); };
   using std::integral_constant;
@@ -577,8 +576,8 @@ static bool with_shape(int64_t D, int64_t most, F&& f) {
   else if (vectors <= 512) call(e, integral_constant<int, 256>{}, integral_constant<int, 2>{});
   else if (vectors <= 1024) call(e, integral_constant<int, 256>{}, integral_constant<int, 4>{});
   else if (vectors <= 2048) call(e, integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-  else if (vectors <= most) call(e, integral_constant<int, 1024>{}, integral_constant<int, 4>{});
-  else return false;
+  else if (vectors > MOST) return false;
+  else if constexpr (MOST > 2048) call(e, integral_constant<int, 1024>{}, integral_constant<int, 4>{});
   return true;
 }
 
@@ -602,7 +601,7 @@ template <int E>
 static int64_t norm_groups(int64_t T, int64_t D, bool* one) {
   int64_t rows = 1, most = std::max<int64_t>(1, std::min<int64_t>(64, ((int64_t)1 << 22) / D));  // 34 MB at most
   *one = false;
-  with_shape<E>(D, kMostHeldBack<E>, [&](auto, auto l, auto nv) {
+  with_shape<E, kMostHeldBack<E>>(D, [&](auto, auto l, auto nv) {
     constexpr int NT = norm_threads(decltype(l)::value);
     rows = NT / decltype(l)::value;
     *one = D <= 256 && (T + rows - 1) / rows <= 256;
@@ -670,7 +669,7 @@ extern "C" tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T
     using TX = std::remove_pointer_t<decltype(tx)>;
     using TY = std::remove_pointer_t<decltype(ty)>;
     constexpr int E = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
-    const bool held = with_shape<E>(D, kMostHeld, [&](auto e, auto l, auto nv) {
+    const bool held = with_shape<E, kMostHeld>(D, [&](auto e, auto l, auto nv) {
       constexpr int L = decltype(l)::value, NT = norm_threads(L);
       // Workgroups at most.  Of several rows each 8,192 (131,072 rows of 2,048 in bf16 190 us; 193 with 4,096, 197
       // with 16,384).  Of one row, as many as reside: with two and four vectors a thread 1,024 and 768 (65,536 of
@@ -764,7 +763,7 @@ extern "C" tgs_status tgs_layer_norm_grad(const void* grad, tgs_dtype grad_dtype
       constexpr int E = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
       groups = norm_groups<E>(T, D, &one);
       a.arrived = one && params ? header_hist(workspace)->hist : nullptr;
-      const bool held = with_shape<E>(D, kMostHeldBack<E>, [&](auto e, auto l, auto nv) {
+      const bool held = with_shape<E, kMostHeldBack<E>>(D, [&](auto e, auto l, auto nv) {
         constexpr int L = decltype(l)::value;
         hipLaunchKernelGGL((k_norm_grad<TX, TY, decltype(e)::value, L, decltype(nv)::value>), dim3((u32)groups),
                            dim3(norm_threads(L)), 0, stream, a);

@@ -111,7 +111,7 @@ struct LogprobsArgs {
   int32_t* top_indices;
   float* top_logprobs;
   u32* err;
-  int64_t T, row0;
+  int64_t row0;
   u32 top;
   bool wide;  // 64-bit tokens
 };
@@ -808,7 +808,6 @@ extern "C" tgs_status tgs_token_logprobs(const void* logits, tgs_dtype dtype, in
   a.top_indices = top_indices;
   a.top_logprobs = top_logprobs;
   a.err = (u32*)workspace;
-  a.T = T;
   a.top = (u32)top;
   a.wide = tokens_dtype == TGS_INT64;
   with_float_dtype(dtype, [&](auto* z) {
@@ -817,7 +816,7 @@ extern "C" tgs_status tgs_token_logprobs(const void* logits, tgs_dtype dtype, in
       with_flag(top > 0, [&](auto tops) {
         constexpr bool ENT = decltype(ent)::value, TOP = decltype(tops)::value;
         const bool wave = short_row(V, dtype);
-    const int threads = wave ? kWave : kRowThreads;
+        const int threads = wave ? kWave : kRowThreads;
         over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
           a.row0 = row0;
           const dim3 grid((u32)(rows * p.slices));
@@ -876,7 +875,7 @@ extern "C" tgs_status tgs_token_logprobs_grad(const void* logits, tgs_dtype dtyp
     with_flag(grad_entropy != nullptr, [&](auto ent) {
       constexpr bool ENT = decltype(ent)::value;
       const bool wave = short_row(V, dtype);
-    const int threads = wave ? kWave : kRowThreads;
+      const int threads = wave ? kWave : kRowThreads;
       over_rows(T, p.slices, threads, [&](int64_t row0, int64_t rows) {
         a.row0 = row0;
         const dim3 grid((u32)(rows * p.slices));
