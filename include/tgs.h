@@ -379,7 +379,8 @@ tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T, int64_t D
                           hipStream_t stream);
 
 /* Bytes of workspace tgs_layer_norm_grad needs (0 if the sizes are invalid): up
-   to 1,280 partial rows of 2 D floats, 34 MB at most. */
+   to 1,280 partial rows of 2 D floats, 34 MB or one row (8 D bytes: 134 MB for
+   2^24 columns) at most. */
 size_t tgs_layer_norm_grad_workspace_bytes(int64_t T, int64_t D);
 
 /*

@@ -595,11 +595,14 @@ static bool with_shape(int64_t D, F&& f) {
 // and 29.5.
 //
 // `one`: few rows of few columns, whose last workgroup adds the partial rows itself
-// instead of a second launch: 517 rows of 131 in fp32 take 12.7 us a call instead of
-// 14.9.
+// instead of a second launch: 13 us a call instead of 15.3 from 64 rows of 64 to 1,024
+// of 256, the rule's edge, in fp32 and bf16.  Past it the gain ends: 4,096 rows of 256
+// in fp32 take 14.0 and 15.3, 8,192 21.2 and 15.6, 2,048 of 512 15.4 and 15.5, 64 of
+// 512 20.8 and 15.4.
 template <int E>
 static int64_t norm_groups(int64_t T, int64_t D, bool* one) {
-  int64_t rows = 1, most = std::max<int64_t>(1, std::min<int64_t>(64, ((int64_t)1 << 22) / D));  // 34 MB at most
+  // rows that registers do not hold: 34 MB of partial rows at most, but one
+  int64_t rows = 1, most = std::max<int64_t>(1, std::min<int64_t>(64, ((int64_t)1 << 22) / D));
   *one = false;
   with_shape<E, kMostHeldBack<E>>(D, [&](auto, auto l, auto nv) {
     constexpr int NT = norm_threads(decltype(l)::value);
@@ -675,7 +678,8 @@ extern "C" tgs_status tgs_layer_norm(const void* x, tgs_dtype x_dtype, int64_t T
       // with 16,384).  Of one row, as many as reside: with two and four vectors a thread 1,024 and 768 (65,536 of
       // 4,096 225, 200 and 216 us with 768, 1,024 and 1,536; 32,768 of 8,192 193, 227 and 201 with 768, 1,024 and
       // 1,280), of 1,024 threads 512 and 256 (8,192 of 8,192, fp32 to bf16, 87, 77 and 76 us with 256, 512 and 1,024;
-      // 4,000 of 20,000 in bf16 124 and 134 with 256 and 512).
+      // with four vectors 4,000 of 20,000 in bf16 122, 134 and 159, 8,192 of 32,768 286, 306 and 315, in fp32 8,192 of
+      // 8,200 115, 116 and 117, of 12,288 146, 147 and 148, of 16,384 192, 188 and 186).
       constexpr int64_t kOneRow = decltype(nv)::value == 2 ? (L == 256 ? 1024 : 512) : (L == 256 ? 768 : 256);
       const int64_t sets = (T + NT / L - 1) / (NT / L), most = L <= kWave ? 8192 : kOneRow;
       hipLaunchKernelGGL((k_norm<TX, TY, decltype(e)::value, L, decltype(nv)::value>), dim3((u32)std::min(sets, most)),
