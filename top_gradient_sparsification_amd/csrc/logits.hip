@@ -686,11 +686,14 @@ static RowPlan pass_plan(int64_t T, int64_t V, tgs_dtype t) {
 // end and are followed by the next in memory reach what few long ones do not.  With
 // 4,096, 16,384 and 32,768 workgroups 8,192 rows of 32,000 in bf16 take 207, 208 and
 // 189 us, with 64 slots 212, 212 and 184, 2,048 of 128,000 210, 211 and 190; with
-// slices of two vectors 198, 219 and 180.  Each slice reads the row's slots: 512 of
-// them on 2,048 rows of 50,001 take 139 us in one slice a row and 178 in slices of
-// 8,192, so a slice is 64 times as long as the slots are many.
+// slices of two vectors 198, 219 and 180.  Each slice reads the row's slots, so
+// it is 16 times as long as the slots are many at least: with no such bound, 16, 64 and
+// 256 times 2,048 rows of 128,000 with 1,024 slots take 269, 231, 224 and 254 us, with
+// 512 200, 201, 218 and 230, 8,192 of 32,000 with 256 190, 190, 211 and 218, 512 of
+// 128,000 with 512 54, 54, 52 and 70, 64 of them 12.9, 13.0, 15.5 and 52, 2,048 of
+// 50,001 with 512 in bf16 99, 99, 97 and 95, in fp32 169, 165, 182 and 175.
 static RowPlan grad_plan_of(int64_t T, int64_t V, tgs_dtype t, int64_t K) {
-  return row_plan(T, V, row_unit(t), 32768, INT32_MAX, 64 * K);
+  return row_plan(T, V, row_unit(t), 32768, INT32_MAX, 16 * K);
 }
 
 static size_t sums_bytes(int64_t T, const RowPlan& p) {
