@@ -451,3 +451,19 @@ def test_scores_further_apart_than_the_type_reaches(tgs_gpu, T, V):
         for tau in (2.5, 1e6):
             loss = check(tgs_gpu, logits, indices, teacher, tau)[0]
             assert torch.isfinite(loss[0]) and loss[0] > 1e31
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("V", [65_537, 65_539, 65_543, 65_545])
+def test_last_slices_of_a_few_scores(tgs_gpu, dtype, V):
+    """Rows in slices of 4,096 or 8,192 scores, of which the last holds less than a vector or little more; and
+    enough slots for longer ones."""
+    for K in (7, 700):
+        logits = scores(5, V, dtype, 7).clone()
+        indices, teacher = make_teacher(logits, K, torch.float32, torch.int64, 7, masked=0.0)
+        indices[:, 0] = V - 1
+        logits[1, 65_536:] = 30.0
+        logits[2, :65_000] = -math.inf
+        indices[2, 1:] = -1
+        check(tgs_gpu, logits, indices, teacher, 0.8)

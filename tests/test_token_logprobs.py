@@ -507,3 +507,19 @@ def test_scores_further_apart_than_the_type_reaches(tgs_gpu, T, V):
             r = check_forward(tgs_gpu, logits, tokens, tau, min(V, 10))
             check_backward(tgs_gpu, logits, tokens, r, tau)
             assert torch.isfinite(r.logprobs[:2]).all() and (r.logprobs[:2] < -1e32).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("V", [65_537, 65_539, 65_543, 65_545])
+def test_last_slices_of_a_few_scores(tgs_gpu, dtype, V):
+    """Rows in slices of 4,096 or 8,192 scores, of which the last holds less than a vector or little more."""
+    logits = scores(5, V, dtype, 7, pad=3).clone()
+    logits[1, 65_536:] = 30.0
+    logits[2, :65_536] = -math.inf
+    logits[3, 65_536:] = -math.inf
+    tokens = make_tokens(logits, 0.0, torch.int64, 7)
+    tokens[1:4] = V - 1
+    for top in (1, 12, 64):
+        r = check_forward(tgs_gpu, logits, tokens, 0.8, top)
+    check_backward(tgs_gpu, logits, tokens, r, 0.8)
