@@ -491,7 +491,8 @@ tgs_status tgs_distillation_grad(const void* logits, tgs_dtype dtype, int64_t T,
 /*
  * Both in one call, for rows whose weights are known: the losses, and in out the
  * gradient of sum over rows of weights loss (weights [T] float, or null for 1).
- * The logits come from memory once, where the two calls above read them twice.
+ * A row's second reading follows its first, so that LDS and the caches serve what
+ * they still hold of it; the two calls above read all rows from memory twice.
  */
 tgs_status tgs_distillation_loss_and_grad(const void* logits, tgs_dtype dtype, int64_t T, int64_t V, int64_t ld,
                                           const void* indices, tgs_dtype indices_dtype, const void* teacher,

@@ -1447,7 +1447,8 @@ def distillation_loss_and_grad(logits: torch.Tensor, teacher_indices: torch.Tens
                                weights: torch.Tensor | None = None, temperature: float = 1.0, out=None,
                                ws: torch.Tensor | None = None):
     """``distillation_loss`` and the gradient of ``sum(weights * loss)`` with
-    respect to the logits in one call that reads the logits from memory once:
+    respect to the logits in one call, whose second reading of a row follows the
+    first and finds what LDS and the caches still hold of it:
     ``(loss, grad)``.
 
     ``weights`` (fp32, ``logits.shape[:-1]``) are 1 if not given: a training

@@ -571,8 +571,9 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, fl
 
 // The losses; with GRAD the gradient of their weighted sum too, for which the
 // row is read again: its first round of vectors, 16 to 64 KB, from LDS, the rest from
-// the caches (8,192 rows of 32,000 in bf16 take 212 us, 243 without LDS; 4,096 of
-// 128,000 448 and 492).
+// beyond the L2 (8,192 rows of 32,000 in bf16 take 212 us, 243 without LDS; 4,096 of
+// 128,000 441 and 492: their rows in flight outgrow the L2, which fetches 1.78 GB where
+// the logits are 1.03, and memory and the last cache together give 6.4 TB/s).
 template <class T, int NT, bool GRAD>
 __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
   constexpr bool KEEP = GRAD && NT >= kRowThreads;
