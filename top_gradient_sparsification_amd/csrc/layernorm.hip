@@ -121,7 +121,8 @@ __device__ __forceinline__ void lane_params(const Place<E, L>& at, const void* p
 // A row in L lanes of NV vectors of E elements each; a workgroup takes every
 // gridDim.x-th set of rows and keeps its columns' parameters in registers.  Of 16
 // lanes a row the compiler is held to six waves a SIMD, where it would take two
-// registers too many for them (200,000 rows of 100 in bf16 24.4 us with five waves).
+// registers too many for them (200,000 rows of 100 in bf16 24.4 us with five waves,
+// 21.7 with six).
 template <class TX, class TY, int E, int L, int NV>
 __global__ __launch_bounds__(norm_threads(L), L == 16 ? 6 : 1) void k_norm(NormArgs a) {
   constexpr int NT = norm_threads(L);

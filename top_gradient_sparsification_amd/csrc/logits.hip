@@ -116,8 +116,8 @@ struct LogprobsArgs {
   bool wide;  // 64-bit tokens
 };
 
-// The difference is taken of halves, with the same bits: of scores at either end of
-// the type it is no fp32 number, over the temperature it may be one.
+// The difference is taken of halves, with the same bits where it is no denormal: of
+// scores at either end of the type it is no fp32 number, over the temperature it may be.
 __device__ __forceinline__ float log_probability(const Logits& z, float x, const RowSums& r, float log_s) {
   return r.s == 0.0f ? -kInf : fmaf(0.5f, x, -0.5f * r.m) * (2.0f * z.inv) - log_s;
 }
